@@ -388,6 +388,197 @@ w4a4_status w4a4_dualquant_solve(w4a4_format fmt, int64_t N, int64_t K,
                                  void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The paged key-value cache and the attention that reads it: what a decoder
+ * layer does between its QKV linear and its O linear.
+ * ---------------------------------------------------------------------------
+ *
+ * A cache holds the keys and values of one layer in pages of page_size tokens:
+ * element (page, token of the page, head, d) of K is at k[page * page_stride +
+ * token * token_stride + head * head_stride + d], of V likewise, so any order
+ * of the three outer axes is served.  The token at position p of sequence s is
+ * on page tables[s * table_stride + p / page_size], row p % page_size.  lens[s]
+ * is the number of tokens of sequence s, the tokens of the present call
+ * included.  Several layers have a cache each and share tables and lens.
+ *
+ * Element types: BF16 and FP16, or E4M3 (OCP FP8) with one positive fp32 scale
+ * per head for K and for V (NULL: 1): a stored code stands for code * scale.
+ *
+ * tables, lens and the other index arrays are device memory that the host
+ * never reads, so their contents cannot be refused by a status.  Nothing is
+ * ever read or written outside the buffers for any contents: a sequence whose
+ * table lacks a valid page (an entry outside 0..pages-1, or a length beyond
+ * max_pages * page_size) for a token that a query sees gets BF16 / FP16 NaN
+ * for that query's kv head, and tokens without a page are not stored.
+ */
+typedef enum { W4A4_BF16 = 0, W4A4_F16 = 1, W4A4_E4M3 = 2 } w4a4_dtype;
+
+typedef struct {
+  void* k;                 /* device, 16-byte aligned                            */
+  void* v;                 /* device, 16-byte aligned                            */
+  const float* k_scale;    /* device, fp32 [heads]; E4M3 only, NULL means 1      */
+  const float* v_scale;
+  int64_t page_stride;     /* elements; page, token and head strides are         */
+  int64_t token_stride;    /*   multiples of 16 bytes                            */
+  int64_t head_stride;
+  int32_t dtype;           /* w4a4_dtype                                         */
+  int32_t pages;
+  int32_t page_size;       /* tokens; any value from 1 to 65536                  */
+  int32_t heads;
+  int32_t head_dim;        /* 64, 128 or 256                                     */
+} w4a4_kv_cache;
+
+typedef struct {
+  int32_t* tables;         /* device, int32 [seqs x max_pages], rows table_stride apart */
+  int32_t* lens;           /* device, int32 [seqs]                               */
+  int64_t table_stride;
+  int32_t seqs;
+  int32_t max_pages;
+} w4a4_kv_seqs;
+
+/*
+ * w4a4_kv_append - store the keys and values of new tokens.
+ *
+ *   cu      device, int32 [seqs + 1]: sequence s has the rows cu[s]..cu[s+1]-1
+ *           of k and v, its last cu[s+1] - cu[s] tokens (positions lens[s] -
+ *           count .. lens[s] - 1).  NULL: one row per sequence.
+ *   tokens  rows of k and v (cu[seqs]; seqs if cu is NULL).
+ *   dtype   W4A4_BF16 or W4A4_F16, the type of k and v: the cache's own, or
+ *           either of them for an E4M3 cache.
+ *   k, v    device, 16-byte aligned, heads x head_dim values per row; rows and
+ *           heads at the given strides (elements, multiples of 8), so that the
+ *           slices of a fused projection's output serve as they are.
+ *
+ * E4M3: code = RNE_E4M3(fp32(x) / scale[head]) saturating at +-448, NaN kept.
+ * A row whose position is negative or has no valid page is not stored.
+ */
+w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, const int32_t* cu,
+                           int64_t tokens, w4a4_dtype dtype, const void* k, int64_t k_row, int64_t k_head,
+                           const void* v, int64_t v_row, int64_t v_head, void* stream);
+
+/*
+ * w4a4_attn_decode - attention of one new token per sequence over the cache.
+ *
+ *   out[s, h] = sum_t w_t V_t,  w = softmax over the visible t of
+ *               scale * <q[s, h], K_t>,   K, V of head h / (q_heads / heads)
+ *
+ * The query of sequence s is at position p = lens[s] - 1 and sees token t if
+ * t <= p and (window == 0, or t > p - window, or t < sinks): with a window, the
+ * last `window` tokens and the first `sinks` ones.  A sequence of length 0
+ * sees nothing: out = 0, lse = -inf.  Masked tokens are left out of the sums
+ * whatever they hold (Inf and NaN included).
+ *
+ *   dtype   W4A4_BF16 or W4A4_F16, of q and out: the cache's type, or either
+ *           of them with an E4M3 cache.
+ *   q_heads a multiple of cache->heads.
+ *   q, out  device, 16-byte aligned, [seqs, q_heads, head_dim] at the given row
+ *           and head strides (elements, multiples of 8).
+ *   scale   positive and finite (1 / sqrt(head_dim) is usual).
+ *   lse     device, fp32 [seqs x q_heads], or NULL: ln sum exp(scale <q, K_t>).
+ *   workspace/ws_bytes: device scratch of at least
+ *           w4a4_attn_decode_workspace_bytes() bytes, 16-byte aligned, no
+ *           initial contents needed.
+ *
+ * Scores, softmax statistics and sums are fp32.  The work is split evenly over
+ * the card by the sequences' visible lengths, read on the device; results do
+ * not depend on timing.
+ */
+size_t w4a4_attn_decode_workspace_bytes(const w4a4_kv_cache* cache, int64_t seqs, int q_heads);
+w4a4_status w4a4_attn_decode(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, w4a4_dtype dtype, int q_heads,
+                             const void* q, int64_t q_row, int64_t q_head, float scale, int window, int sinks,
+                             void* out, int64_t o_row, int64_t o_head, float* lse, void* workspace,
+                             size_t ws_bytes, void* stream);
+
+/*
+ * w4a4_attn_prefill - attention of several new tokens per sequence over the
+ * cache, in which they are already stored (w4a4_kv_append comes first).
+ *
+ * As w4a4_attn_decode, with the queries of sequence s in the rows cu[s] ..
+ * cu[s+1]-1 of q, at positions lens[s] - count .. lens[s] - 1; cu, tokens as in
+ * w4a4_kv_append (cu must not be NULL).  A query at a negative position sees
+ * nothing.  lse is fp32 [tokens x q_heads].  Where the rows are too few to fill the
+ * card the keys are split as well.  The softmax weights are rounded to `dtype`
+ * for the matrix cores; statistics and sums are fp32.
+ */
+size_t w4a4_attn_prefill_workspace_bytes(const w4a4_kv_cache* cache, int64_t seqs, int64_t tokens, int q_heads);
+w4a4_status w4a4_attn_prefill(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, const int32_t* cu,
+                              int64_t tokens, w4a4_dtype dtype, int q_heads, const void* q, int64_t q_row,
+                              int64_t q_head, float scale, int window, int sinks, void* out, int64_t o_row,
+                              int64_t o_head, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Page bookkeeping.  refs is device int32 [pages]: the number of sequences
+ * that hold a page, 0 for a free one.  A table entry is -1 where the sequence
+ * holds no page.  Allocation takes the lowest free pages, so every result is
+ * determined by the inputs.  Index lists are device int32.
+ *
+ * Page data is moved for `n` arrays at once (K and V of every layer): arrays
+ * is a host array of n device pointers (16-byte aligned), page i of each at
+ * byte i * page_stride_bytes, page_bytes long, densely filled.
+ */
+
+/* Copy page src[i] to page dst[i] in every array.  Pairs with an index outside
+ * 0..pages-1 are skipped; no page may be the target of two pairs, or target of
+ * one and source of another. */
+w4a4_status w4a4_kv_copy_pages(int n, void* const* arrays, int64_t page_stride_bytes, int64_t page_bytes,
+                               int pages, const int32_t* src, const int32_t* dst, int64_t pairs, void* stream);
+
+/*
+ * Scratch of w4a4_kv_reserve and w4a4_kv_fork (rows: the sequences, or the
+ * children) and of w4a4_kv_compact (rows: 0): 16-byte aligned device memory,
+ * no initial contents needed.
+ */
+size_t w4a4_kv_workspace_bytes(int64_t rows, int64_t pages);
+
+/*
+ * Give every sequence pages for lens[s] tokens: the entries after the last one
+ * it holds, up to ceil(lens[s] / page_size), get the lowest free pages,
+ * sequences in order.  lacking: device int32[1] or NULL, out: the number of
+ * pages that were not to be had (0: all is well); those entries stay -1.
+ */
+w4a4_status w4a4_kv_reserve(const w4a4_kv_seqs* seqs, int page_size, int32_t* refs, int pages, int32_t* lacking,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Make sequence children[i] a copy of parents[i] as far as the parent's tokens
+ * go, i < n: whole pages are shared (refs + 1), a last page that is not full
+ * is copied, so that either can go on alone; lens[child] = lens[parent].  The
+ * children's rows are overwritten: let their pages go with w4a4_kv_free
+ * first.  Children are distinct and none is a parent; pairs with an index
+ * outside 0..seqs-1 are skipped.  lacking as in w4a4_kv_reserve.
+ */
+w4a4_status w4a4_kv_fork(int n_arrays, void* const* arrays, int64_t page_stride_bytes, int64_t page_bytes,
+                         const w4a4_kv_seqs* seqs, int page_size, int32_t* refs, int pages, const int32_t* parents,
+                         const int32_t* children, int n, int32_t* lacking, void* workspace, size_t ws_bytes,
+                         void* stream);
+
+/*
+ * Let go of all pages of the sequences ids[0..n-1] (ids NULL: of all n == seqs
+ * sequences): refs - 1 for each, entries -1, lens 0.  An id that is listed
+ * twice is freed once; ids outside 0..seqs-1 are skipped.
+ */
+w4a4_status w4a4_kv_free(const w4a4_kv_seqs* seqs, int32_t* refs, int pages, const int32_t* ids, int n,
+                         void* stream);
+
+/*
+ * Let go of the pages that no later token of the sequences sees under a window
+ * (window >= 1) with sinks: those whose tokens are all at positions from
+ * `sinks` to lens[s] - window.  The page of a sequence's last token stays.
+ */
+w4a4_status w4a4_kv_trim(const w4a4_kv_seqs* seqs, int page_size, int32_t* refs, int pages, const int32_t* ids,
+                         int n, int window, int sinks, void* stream);
+
+/*
+ * Close the holes: with L pages in use, the i-th page in use at or above L
+ * moves to the i-th free page below L, in every array; tables (every row) and
+ * refs follow.  remap: device int32 [pages], out: the new index of every page
+ * in use, -1 for free ones (for tables kept elsewhere).
+ */
+w4a4_status w4a4_kv_compact(int n_arrays, void* const* arrays, int64_t page_stride_bytes, int64_t page_bytes,
+                            const w4a4_kv_seqs* seqs, int32_t* refs, int pages, int32_t* remap, void* workspace,
+                            size_t ws_bytes, void* stream);
+
+/*
  * Measurement aids for the decode roofline (not part of the quantized
  * linear).  w4a4_probe_stream_read reads `bytes` of device memory once, in
  * one launch, with 16-byte non-temporal loads four in flight per lane (the

@@ -10,6 +10,11 @@ without the ``w4a4_`` prefix:
     blob             = pack_weight(w_codes, w_scales, t_w, r, "mxfp4")
     y_bf16           = linear(codes, scales, t, blob, "mxfp4", N, K)
 
+The paged key-value cache and the attention between the linears:
+
+    kv_append(k, v, k_cache, v_cache, tables, lens)
+    out = attn_decode(q, k_cache, v_cache, tables, lens)
+
 There is no fallback: if the library is missing or fails to load, the
 functions raise.
 """
@@ -22,7 +27,9 @@ from typing import Optional, Tuple
 import torch
 
 __all__ = ["FORMATS", "lib", "library_path", "block_size", "scale_dtype", "quantize_act", "pack_weight",
-           "unpack_weight", "linear", "linear_noalloc", "linear_workspace", "packed_weight_bytes", "W4A4Error"]
+           "unpack_weight", "linear", "linear_noalloc", "linear_workspace", "packed_weight_bytes", "W4A4Error",
+           "attn_decode", "attn_prefill", "kv_append", "kv_copy_pages", "kv_reserve", "kv_fork", "kv_free", "kv_trim",
+           "kv_compact"]
 
 FORMATS = {"mxfp4": 0, "nvfp4": 1, "mxint4": 2, "int4g64": 3, "mxfp8": 4, "mxint8": 5, "int8g128": 6}
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,6 +48,18 @@ def library_path() -> str:
     """The in-tree libw4a4.so, or the file W4A4_LIBRARY names (a variant build
     of the same sources, e.g. the AddressSanitizer one)."""
     return os.environ.get("W4A4_LIBRARY") or os.path.join(_HERE, "libw4a4.so")
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _KvSeqs(ctypes.Structure):
+    _fields_ = [("tables", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
 def lib() -> ctypes.CDLL:
@@ -86,6 +105,25 @@ def lib() -> ctypes.CDLL:
     L.w4a4_probe_empty.restype = i32
     L.w4a4_probe_mfma_fp4.argtypes = [vp, ctypes.c_int, ctypes.c_int, vp, vp]
     L.w4a4_probe_mfma_fp4.restype = i32
+    cp, sp, f32 = ctypes.POINTER(_KvCache), ctypes.POINTER(_KvSeqs), ctypes.c_float
+    L.w4a4_kv_append.argtypes = [cp, sp, vp, i64, i32, vp, i64, i64, vp, i64, i64, vp]
+    L.w4a4_attn_decode_workspace_bytes.argtypes = [cp, i64, i32]
+    L.w4a4_attn_decode_workspace_bytes.restype = sz
+    L.w4a4_attn_decode.argtypes = [cp, sp, i32, i32, vp, i64, i64, f32, i32, i32, vp, i64, i64, vp, vp, sz, vp]
+    L.w4a4_attn_prefill_workspace_bytes.argtypes = [cp, i64, i64, i32]
+    L.w4a4_attn_prefill_workspace_bytes.restype = sz
+    L.w4a4_attn_prefill.argtypes = [cp, sp, vp, i64, i32, i32, vp, i64, i64, f32, i32, i32, vp, i64, i64, vp, vp, sz, vp]
+    L.w4a4_kv_copy_pages.argtypes = [i32, vp, i64, i64, i32, vp, vp, i64, vp]
+    L.w4a4_kv_workspace_bytes.argtypes = [i64, i64]
+    L.w4a4_kv_workspace_bytes.restype = sz
+    L.w4a4_kv_reserve.argtypes = [sp, i32, vp, i32, vp, vp, sz, vp]
+    L.w4a4_kv_fork.argtypes = [i32, vp, i64, i64, sp, i32, vp, i32, vp, vp, i32, vp, vp, sz, vp]
+    L.w4a4_kv_free.argtypes = [sp, vp, i32, vp, i32, vp]
+    L.w4a4_kv_trim.argtypes = [sp, i32, vp, i32, vp, i32, i32, i32, vp]
+    L.w4a4_kv_compact.argtypes = [i32, vp, i64, i64, sp, vp, i32, vp, vp, sz, vp]
+    for name in ("kv_append", "attn_decode", "attn_prefill", "kv_copy_pages", "kv_reserve", "kv_fork", "kv_free",
+                 "kv_trim", "kv_compact"):
+        getattr(L, "w4a4_" + name).restype = i32
     L.w4a4_last_error.argtypes = []
     L.w4a4_last_error.restype = ctypes.c_char_p
     L.w4a4_version.argtypes = []
@@ -342,3 +380,265 @@ def probe_empty(device) -> None:
     """w4a4_probe_empty: one empty kernel on the current stream of `device`."""
     _check(lib().w4a4_probe_empty(_stream(torch.device(device))))
 
+
+# ---------------------------------------------------------------------------
+# The paged key-value cache and its attention.  Everywhere:
+#
+#   k_cache, v_cache  [pages, page_size, heads, head_dim], the last dimension
+#                     contiguous, the others in any order in memory (the same
+#                     for both); bfloat16, float16 or float8_e4m3fn
+#   k_scale, v_scale  fp32 [heads] or None (1): a stored E4M3 value stands for
+#                     value * scale
+#   tables            int32 [seqs, max_pages]: page of the tokens page_size * j ..
+#   lens              int32 [seqs]: tokens of each sequence, new ones included
+#   refs              int32 [pages]: sequences on each page, 0 for a free one
+#   caches            tensors of pages [..., pages, page_size, heads, head_dim], or
+#                     one such tensor (leading dimensions: layers, K and V)
+
+_KV_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+
+
+def _kv_type(t: torch.Tensor, what: str) -> int:
+    f = _KV_TYPES.get(t.dtype)
+    if f is None:
+        raise W4A4Error(4, f"{what}: type {t.dtype} (bfloat16, float16 or float8_e4m3fn)")
+    return f
+
+
+def _int32(what: str, device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and (t.dtype != torch.int32 or t.device != device or
+                              (t.dim() == 1 and t.stride(0) != 1 and t.numel() > 1)):
+            raise W4A4Error(2, f"{what}: index tensors are int32, on {device}, with contiguous entries")
+
+
+def _kv_cache(what: str, k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> _KvCache:
+    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1 or k.dtype != v.dtype or \
+            k.device != v.device:
+        raise W4A4Error(2, f"{what}: caches {tuple(k.shape)} and {tuple(v.shape)} must be alike, [pages, page_size, "
+                           "heads, head_dim] with a contiguous last dimension")
+    f = _kv_type(k, what)
+    ks = vs = None
+    if f == 2:
+        for t in (k_scale, v_scale):
+            if t is not None and (t.dtype != torch.float32 or t.numel() != k.shape[2] or not t.is_contiguous() or
+                                  t.device != k.device):
+                raise W4A4Error(2, f"{what}: scales are contiguous float32 [heads] on the cache's device")
+        ks, vs = (None if t is None else t.data_ptr() for t in (k_scale, v_scale))
+    elif k_scale is not None or v_scale is not None:
+        raise W4A4Error(4, f"{what}: scales belong to a float8_e4m3fn cache")
+    pages, page, heads, dim = k.shape
+    ps, ts, hs, _ = k.stride()
+    return _KvCache(k.data_ptr(), v.data_ptr(), ks, vs, ps, ts, hs, f, pages, page, heads, dim)
+
+
+def _kv_seqs(what: str, tables: torch.Tensor, lens: Optional[torch.Tensor], device) -> _KvSeqs:
+    if tables.dim() != 2 or (tables.shape[1] > 1 and tables.stride(1) != 1) or \
+            (lens is not None and tuple(lens.shape) != (tables.shape[0],)):
+        raise W4A4Error(2, f"{what}: tables {tuple(tables.shape)} must be [seqs, max_pages] with contiguous rows, lens [seqs]")
+    _int32(what, device, tables, lens)
+    seqs, width = tables.shape
+    return _KvSeqs(tables.data_ptr(), None if lens is None else lens.data_ptr(),
+                   tables.stride(0) if seqs > 1 else width, seqs, width)
+
+
+def _kv_rows(what: str, x: torch.Tensor, rows: int, heads, dim: int, like: torch.Tensor) -> None:
+    if x.dim() != 3 or x.shape[0] != rows or x.shape[2] != dim or (heads is not None and x.shape[1] != heads) or \
+            x.stride(2) != 1 or x.device != like.device:
+        raise W4A4Error(2, f"{what}: {tuple(x.shape)} (need [{rows}, {'heads' if heads is None else heads}, {dim}] with a "
+                           f"contiguous last dimension, on {like.device})")
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, tables: torch.Tensor,
+              lens: torch.Tensor, *, cu_seqlens: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+              v_scale: Optional[torch.Tensor] = None) -> None:
+    """w4a4_kv_append: store new keys and values [tokens, heads, head_dim] (any
+    row and head strides) at the ends of their sequences.
+
+    cu_seqlens int32 [seqs + 1]: sequence s has the rows cu[s] .. cu[s + 1] - 1,
+    its last tokens; None: one row per sequence.
+    """
+    c = _kv_cache("kv_append", k_cache, v_cache, k_scale, v_scale)
+    s = _kv_seqs("kv_append", tables, lens, k_cache.device)
+    tokens = k.shape[0]
+    _kv_rows("kv_append: k", k, tokens, c.heads, c.head_dim, k_cache)
+    _kv_rows("kv_append: v", v, tokens, c.heads, c.head_dim, k_cache)
+    if k.dtype != v.dtype:
+        raise W4A4Error(4, f"kv_append: k is {k.dtype}, v is {v.dtype}")
+    if cu_seqlens is not None:
+        _int32("kv_append", k_cache.device, cu_seqlens)
+        if cu_seqlens.numel() != s.seqs + 1:
+            raise W4A4Error(2, f"kv_append: cu_seqlens has {cu_seqlens.numel()} entries for {s.seqs} sequences")
+    _check(lib().w4a4_kv_append(c, s, None if cu_seqlens is None else cu_seqlens.data_ptr(), tokens,
+                                _kv_type(k, "kv_append"), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
+                                v.stride(0), v.stride(1), _stream(k_cache.device)))
+
+
+def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, scale, window, sinks, out, return_lse,
+          workspace):
+    dev = k_cache.device
+    c = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
+    s = _kv_seqs(name, tables, lens, dev)
+    L = lib()
+    rows, q_heads = q.shape[0], q.shape[1]
+    _kv_rows(name + ": q", q, s.seqs if cu is None else rows, None, c.head_dim, k_cache)
+    if out is None:
+        out = torch.empty((rows, q_heads, c.head_dim), dtype=q.dtype, device=dev)
+    else:
+        _kv_rows(name + ": out", out, rows, q_heads, c.head_dim, k_cache)
+        if out.dtype != q.dtype:
+            raise W4A4Error(4, f"{name}: out is {out.dtype}, q is {q.dtype}")
+    lse = torch.empty((rows, q_heads), dtype=torch.float32, device=dev) if return_lse else None
+    if cu is None:
+        need = L.w4a4_attn_decode_workspace_bytes(c, rows, q_heads)
+    else:
+        _int32(name, dev, cu)
+        if cu.numel() != s.seqs + 1:
+            raise W4A4Error(2, f"{name}: cu_seqlens has {cu.numel()} entries for {s.seqs} sequences")
+        need = L.w4a4_attn_prefill_workspace_bytes(c, s.seqs, rows, q_heads)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    tail = (_kv_type(q, name), q_heads, q.data_ptr(), q.stride(0), q.stride(1),
+            c.head_dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), out.stride(0), out.stride(1),
+            None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(dev))
+    _check(L.w4a4_attn_decode(c, s, *tail) if cu is None else
+           L.w4a4_attn_prefill(c, s, cu.data_ptr(), rows, *tail))
+    return (out, lse) if return_lse else out
+
+
+def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, tables: torch.Tensor,
+                lens: torch.Tensor, *, k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                scale: Optional[float] = None, window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,
+                return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
+    """w4a4_attn_decode: one new token per sequence, q [seqs, q_heads, head_dim]
+    -> out of the same shape and type (and lse fp32 [seqs, q_heads]).
+
+    scale None: 1 / sqrt(head_dim).  window 0: every token is seen; otherwise
+    the last `window` ones and the first `sinks`.
+    """
+    return _attn("attn_decode", q, None, k_cache, v_cache, tables, lens, k_scale, v_scale, scale, window, sinks, out,
+                 return_lse, workspace)
+
+
+def attn_prefill(q: torch.Tensor, cu_seqlens: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 tables: torch.Tensor, lens: torch.Tensor, *, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None, scale: Optional[float] = None, window: int = 0,
+                 sinks: int = 0, out: Optional[torch.Tensor] = None, return_lse: bool = False,
+                 workspace: Optional[torch.Tensor] = None):
+    """w4a4_attn_prefill: the new tokens of every sequence, q [tokens, q_heads,
+    head_dim], sequence s in the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1, already
+    stored in the cache; causal, with window and sinks as in attn_decode."""
+    return _attn("attn_prefill", q, cu_seqlens, k_cache, v_cache, tables, lens, k_scale, v_scale, scale, window, sinks,
+                 out, return_lse, workspace)
+
+
+def _kv_arrays(what: str, caches):
+    """(n, host array of base pointers, page stride, page bytes, pages, page_size, device)."""
+    tensors = [caches] if isinstance(caches, torch.Tensor) else list(caches)
+    ptrs, first = [], None
+    for t in tensors:
+        if t.dim() < 4:
+            raise W4A4Error(2, f"{what}: a cache is [..., pages, page_size, heads, head_dim], got {tuple(t.shape)}")
+        size, elt = tuple(t.shape[-4:]), t.element_size()
+        stride = tuple(n * elt for n in t.stride()[-4:])
+        dense = elt
+        for st, n in sorted(zip(stride[1:], size[1:])):
+            if n > 1 and st != dense:
+                raise W4A4Error(2, f"{what}: a page's {size[1:]} values must lie densely in memory")
+            dense *= n
+        key = (size, stride[0], dense, t.device)
+        if first is None:
+            first = key
+        elif key != first:
+            raise W4A4Error(2, f"{what}: the caches must be alike")
+        at = [t.data_ptr()]
+        for n, st in zip(t.shape[:-4], t.stride()[:-4]):
+            at = [a + i * st * elt for a in at for i in range(n)]
+        ptrs += at
+    if first is None:
+        raise W4A4Error(2, f"{what}: no caches")
+    (pages, page, _, _), stride, dense, dev = first
+    return len(ptrs), (ctypes.c_void_p * max(len(ptrs), 1))(*ptrs), stride if pages > 1 else dense, dense, pages, page, dev
+
+
+def _kv_workspace(rows: int, pages: int, device) -> torch.Tensor:
+    return torch.empty(lib().w4a4_kv_workspace_bytes(rows, pages), dtype=torch.uint8, device=device)
+
+
+def _same_length(what: str, a: torch.Tensor, b: torch.Tensor) -> int:
+    if a.dim() != 1 or a.shape != b.shape:
+        raise W4A4Error(2, f"{what}: lists of {tuple(a.shape)} and {tuple(b.shape)} entries")
+    return a.numel()
+
+
+def kv_copy_pages(caches, src: torch.Tensor, dst: torch.Tensor) -> None:
+    """w4a4_kv_copy_pages: page src[i] to page dst[i] (int32) in every cache."""
+    n, arrays, stride, size, pages, _, dev = _kv_arrays("kv_copy_pages", caches)
+    _int32("kv_copy_pages", dev, src, dst)
+    pairs = _same_length("kv_copy_pages", src, dst)
+    _check(lib().w4a4_kv_copy_pages(n, arrays, stride, size, pages, src.data_ptr(), dst.data_ptr(), pairs, _stream(dev)))
+
+
+def kv_reserve(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int, *,
+               lacking: Optional[torch.Tensor] = None) -> None:
+    """w4a4_kv_reserve: pages for lens[s] tokens of every sequence, the lowest
+    free ones first; lacking int32 [1]: the number that was not to be had."""
+    s = _kv_seqs("kv_reserve", tables, lens, refs.device)
+    _int32("kv_reserve", refs.device, refs, lacking)
+    ws = _kv_workspace(s.seqs, refs.numel(), refs.device)
+    _check(lib().w4a4_kv_reserve(s, page_size, refs.data_ptr(), refs.numel(),
+                                 None if lacking is None else lacking.data_ptr(), ws.data_ptr(), ws.numel(),
+                                 _stream(refs.device)))
+
+
+def _check_pages(what: str, refs: torch.Tensor, pages: int) -> None:
+    if refs.numel() != pages:
+        raise W4A4Error(2, f"{what}: refs has {refs.numel()} entries for {pages} pages")
+
+
+def kv_fork(caches, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, parents: torch.Tensor,
+            children: torch.Tensor, *, lacking: Optional[torch.Tensor] = None) -> None:
+    """w4a4_kv_fork: sequence children[i] becomes a copy of parents[i] (int32):
+    whole pages shared, a last page that is not full copied in every cache."""
+    n, arrays, stride, size, pages, page, dev = _kv_arrays("kv_fork", caches)
+    s = _kv_seqs("kv_fork", tables, lens, dev)
+    _int32("kv_fork", dev, refs, parents, children, lacking)
+    _check_pages("kv_fork", refs, pages)
+    count = _same_length("kv_fork", parents, children)
+    ws = _kv_workspace(count, pages, dev)
+    _check(lib().w4a4_kv_fork(n, arrays, stride, size, s, page, refs.data_ptr(), pages, parents.data_ptr(),
+                              children.data_ptr(), count, None if lacking is None else lacking.data_ptr(),
+                              ws.data_ptr(), ws.numel(), _stream(dev)))
+
+
+def kv_free(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, seqs: Optional[torch.Tensor] = None) -> None:
+    """w4a4_kv_free: let go of all pages of the sequences `seqs` (int32; None: all)."""
+    s = _kv_seqs("kv_free", tables, lens, refs.device)
+    _int32("kv_free", refs.device, refs, seqs)
+    _check(lib().w4a4_kv_free(s, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
+                              s.seqs if seqs is None else seqs.numel(), _stream(refs.device)))
+
+
+def kv_trim(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int, window: int, sinks: int = 0,
+            seqs: Optional[torch.Tensor] = None) -> None:
+    """w4a4_kv_trim: let go of the pages that no later token of the sequences
+    `seqs` (None: all) sees under a window with sinks."""
+    s = _kv_seqs("kv_trim", tables, lens, refs.device)
+    _int32("kv_trim", refs.device, refs, seqs)
+    _check(lib().w4a4_kv_trim(s, page_size, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
+                              s.seqs if seqs is None else seqs.numel(), window, sinks, _stream(refs.device)))
+
+
+def kv_compact(caches, tables: torch.Tensor, refs: torch.Tensor) -> torch.Tensor:
+    """w4a4_kv_compact: move the pages in use to the front, in every cache, with
+    tables and refs; returns remap int32 [pages]: new index, -1 for free pages."""
+    n, arrays, stride, size, pages, _, dev = _kv_arrays("kv_compact", caches)
+    s = _kv_seqs("kv_compact", tables, None, dev)
+    _int32("kv_compact", dev, refs)
+    _check_pages("kv_compact", refs, pages)
+    remap = torch.empty(pages, dtype=torch.int32, device=dev)
+    ws = _kv_workspace(0, pages, dev)
+    _check(lib().w4a4_kv_compact(n, arrays, stride, size, s, refs.data_ptr(), pages, remap.data_ptr(), ws.data_ptr(),
+                                 ws.numel(), _stream(dev)))
+    return remap

@@ -1,0 +1,129 @@
+// Element types, matrix instructions and small reductions shared by the two
+// attention kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kvcache.h"
+
+namespace w4a4 {
+
+typedef uint32_t at_u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t at_u32x4 __attribute__((ext_vector_type(4)));
+typedef float at_f32x2 __attribute__((ext_vector_type(2)));
+typedef float at_f32x4 __attribute__((ext_vector_type(4)));
+typedef float at_f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// Whether either half of u is Inf or NaN (all bits of the exponent EXP set).
+template <uint32_t EXP>
+__device__ __forceinline__ bool has_odd(uint32_t u) {
+  return (u & EXP) == EXP || (u >> 16 & EXP) == EXP;
+}
+// u with 0 in the place of the halves that are Inf or NaN.
+template <uint32_t EXP>
+__device__ __forceinline__ uint32_t without_odd(uint32_t u) {
+  return ((u & EXP) == EXP ? 0 : u & 0xffffu) | ((u >> 16 & EXP) == EXP ? 0 : u & 0xffff0000u);
+}
+
+// 16-bit element types.  pack(a, b): two fp32 to two elements, RNE, a in the
+// low half.  mfma16: 16 x 16 x 32, mfma32: 32 x 32 x 16; operands 8 elements
+// per lane.
+struct Bf16 {
+  static constexpr uint32_t kExp = 0x7f80u;      // the exponent of Inf and NaN
+  static __device__ __forceinline__ bool not_finite(uint32_t u) { return has_odd<kExp>(u); }
+  static __device__ __forceinline__ uint32_t finite(uint32_t u) { return without_odd<kExp>(u); }
+  typedef __bf16 x8 __attribute__((ext_vector_type(8)));
+  typedef __bf16 x2 __attribute__((ext_vector_type(2)));
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((at_f32x2){a, b}, x2));
+  }
+  // pack() of values that the type holds exactly (E4M3 values): the upper halves
+  static __device__ __forceinline__ uint32_t pack_exact(float a, float b) {
+    return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302);
+  }
+  static __device__ __forceinline__ float low(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
+  static __device__ __forceinline__ float high(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
+  static __device__ __forceinline__ at_f32x4 mfma16(at_u32x4 a, at_u32x4 b, at_f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ at_f32x16 mfma32(at_u32x4 a, at_u32x4 b, at_f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
+  }
+};
+struct F16 {
+  static constexpr uint32_t kExp = 0x7c00u;      // the exponent of Inf and NaN
+  static __device__ __forceinline__ bool not_finite(uint32_t u) { return has_odd<kExp>(u); }
+  static __device__ __forceinline__ uint32_t finite(uint32_t u) { return without_odd<kExp>(u); }
+  typedef _Float16 x8 __attribute__((ext_vector_type(8)));
+  typedef _Float16 x2 __attribute__((ext_vector_type(2)));
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((at_f32x2){a, b}, x2));
+  }
+  static __device__ __forceinline__ uint32_t pack_exact(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+  }
+  static __device__ __forceinline__ float low(uint32_t u) {
+    return float(__builtin_bit_cast(x2, u).x);
+  }
+  static __device__ __forceinline__ float high(uint32_t u) {
+    return float(__builtin_bit_cast(x2, u).y);
+  }
+  static __device__ __forceinline__ at_f32x4 mfma16(at_u32x4 a, at_u32x4 b, at_f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ at_f32x16 mfma32(at_u32x4 a, at_u32x4 b, at_f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
+  }
+};
+
+// Two E4M3 codes (the low or the high half of u) as two elements of T, exact.
+template <class T, bool HI>
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t u) {
+  const at_f32x2 f = __builtin_amdgcn_cvt_pk_f32_fp8(int(u), HI);
+  return T::pack_exact(f.x, f.y);
+}
+
+// x of the lanes l and l ^ 32 (l ^ 16), in either order: halves (odd and even
+// quarters) of two registers change places.
+struct Pair {
+  float a, b;
+};
+__device__ __forceinline__ Pair pair_of(at_u32x2 r) {
+  const uint32_t x = r.x, y = r.y;      // a bit cast of r.y itself would read r.x
+  return {__builtin_bit_cast(float, x), __builtin_bit_cast(float, y)};
+}
+__device__ __forceinline__ Pair pair_xor32(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  return pair_of(__builtin_amdgcn_permlane32_swap(u, u, false, false));
+}
+__device__ __forceinline__ Pair pair_xor16(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  return pair_of(__builtin_amdgcn_permlane16_swap(u, u, false, false));
+}
+__device__ __forceinline__ float max_xor32(float x) {
+  const Pair p = pair_xor32(x);
+  return fmaxf(p.a, p.b);
+}
+__device__ __forceinline__ float sum_xor32(float x) {
+  const Pair p = pair_xor32(x);
+  return p.a + p.b;
+}
+__device__ __forceinline__ float max_xor16(float x) {
+  const Pair p = pair_xor16(x);
+  return fmaxf(p.a, p.b);
+}
+__device__ __forceinline__ float sum_xor16(float x) {
+  const Pair p = pair_xor16(x);
+  return p.a + p.b;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// exp2(x - m) as the weight of a partial result with maximum x against m;
+// 0 for a partial result without a visible token.
+__device__ __forceinline__ float rebase(float x, float m) { return x == kNegInf ? 0.0f : exp2_fast(x - m); }
+
+}  // namespace w4a4

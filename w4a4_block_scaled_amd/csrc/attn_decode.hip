@@ -1,0 +1,549 @@
+// Attention of one new token per sequence over the paged cache.
+//
+// Each kv head of each sequence is a unit with `rows` query rows (the group's
+// heads, in blocks of 16), and reads its visible keys and values once: 4 to 16
+// fp operations per byte, so HBM bandwidth bounds it.  The units' visible
+// tokens, in tiles of 128, form one list over all sequences, of which every
+// workgroup takes an equal contiguous piece, whatever the lengths are.  A
+// workgroup that holds a unit whole writes its output; a unit cut by the
+// pieces' ends leaves partial results (unnormalised sum, maximum, sum of
+// weights) that a second kernel joins.
+//
+// Inside a tile each of the 4 waves takes 32 tokens.  Scores come from the
+// transposed product S^T = K Q^T (16 x 16 x 32 MFMA, keys as the first operand,
+// loaded from the cache straight in operand order), so that a lane holds
+// scores of one query row and the 8 tokens 8 g .. 8 g + 7 of its quarter wave
+// g; the same registers are the second operand of O^T = V^T P^T.  V's operand
+// needs 8 tokens of one d per lane: a lane loads the same d's of 8 tokens and
+// transposes them in registers.  No value passes through LDS until the waves
+// of a workgroup are merged.  The weights enter the product as two 16-bit parts
+// (high and rest, about 16 bits together): the matrix cores idle here, so the
+// second product is free and only the output is rounded to 16 bits.
+#include <algorithm>
+
+#include "attn_common.h"
+
+namespace w4a4 {
+namespace {
+
+constexpr int kTile = 128;       // tokens per workgroup step: 4 waves x 32
+constexpr int kRows = 16;
+
+// The list of work: per sequence, tiles over [0, sink_end) and [start, len).
+// A length beyond the table's capacity is cut to it and marked (`over`).
+struct SeqSpan {
+  int len, low, start, sink_end, sink_tiles, tiles;
+  bool over;
+};
+
+__device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, int s) {
+  SeqSpan z;
+  const int cap = int(min(int64_t(a.kv.max_pages) * a.kv.page.d, int64_t(1) << 30));
+  const int len = max(a.kv.lens[s], 0);
+  z.over = len > cap;
+  z.len = min(len, cap);
+  z.low = a.window ? max(z.len - a.window, 0) : 0;   // first token of the window
+  z.start = z.low & ~7;
+  z.sink_end = min(a.sinks, z.start);
+  z.sink_tiles = (z.sink_end + kTile - 1) / kTile;
+  // at least one: a sequence without tokens still has outputs to write
+  z.tiles = max(z.sink_tiles + (z.len - z.start + kTile - 1) / kTile, 1);
+  return z;
+}
+
+// Results of a unit's piece: unnormalised sums o [rows x D], maxima m and sums
+// of weights l [rows], in the log2 domain.
+struct Partial {
+  float *o, *m, *l;
+};
+
+struct Work {
+  int32_t* first;   // [seqs x units]: workgroup that begins the unit
+  int32_t* count;   // [seqs x units]: workgroups that hold parts of it
+  float* parts;     // [workgroups x 2] partial results
+  int rows;         // min(group, 16)
+};
+
+__host__ __device__ constexpr int partial_floats(int rows, int D) { return (rows * (D + 2) + 3) / 4 * 4; }
+
+// A workgroup has at most two pieces of cut units: one that goes on from the
+// workgroup before (slot 0) and one that it begins (slot 1).
+__device__ __forceinline__ Partial partial_at(const Work& w, int D, int64_t wg, int slot) {
+  float* p = w.parts + (wg * 2 + slot) * partial_floats(w.rows, D);
+  return {p, p + w.rows * D, p + w.rows * (D + 1)};
+}
+
+// ---------------------------------------------------------------- operands --
+
+// Raw keys and values of 32 tokens of one head, in a wave's registers.  E:
+// element bytes.
+template <class T, int D, int E>
+struct Tile {
+  static constexpr int kSteps = D / 32;                 // MFMAs of one 16-token score block
+  static constexpr int kRun = D >= 128 ? 8 : D / 16;    // consecutive d's per lane of a value row
+  static constexpr int kRuns = D / 16 / kRun;
+  static constexpr int kVWords = kRun * E / 4;          // dwords per token and run
+
+  at_u32x4 k[2][kSteps * E / 2];
+  uint32_t v[8][kRuns][kVWords];
+
+  // First d of the 8 that quarter g holds of step j.  E4M3: one 16-byte load
+  // serves the steps 2 c and 2 c + 1.
+  static __device__ __forceinline__ int key_dim(int j, int g) {
+    return E == 2 ? 32 * j + 8 * g : 64 * (j >> 1) + 16 * g + 8 * (j & 1);
+  }
+  __device__ __forceinline__ void load_k(int b, const uint8_t* row, int g) {
+#pragma unroll
+    for (int c = 0; c < kSteps * E / 2; ++c)
+      k[b][c] = *reinterpret_cast<const at_u32x4*>(row + 64 * c + 16 * g);
+  }
+  __device__ __forceinline__ void load_v(int i, const uint8_t* row, int c) {
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) {
+      const uint8_t* p = row + (r * 128 + c * kRun) * E;
+      if constexpr (kVWords == 4) {
+        const at_u32x4 x = *reinterpret_cast<const at_u32x4*>(p);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v[i][r][w] = x[w];
+      } else if constexpr (kVWords == 2) {
+        const at_u32x2 x = *reinterpret_cast<const at_u32x2*>(p);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) v[i][r][w] = x[w];
+      } else {
+        v[i][r][0] = *reinterpret_cast<const uint32_t*>(p);
+      }
+    }
+  }
+  __device__ __forceinline__ void clear_v(int i) {
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r)
+#pragma unroll
+      for (int w = 0; w < kVWords; ++w) v[i][r][w] = 0;
+  }
+
+  // Key operand of block b, step j.
+  __device__ __forceinline__ at_u32x4 key(int b, int j) const {
+    if constexpr (E == 2) {
+      return k[b][j];
+    } else {
+      const uint32_t x = k[b][j >> 1][2 * (j & 1)], y = k[b][j >> 1][2 * (j & 1) + 1];
+      return (at_u32x4){e4m3_pair<T, false>(x), e4m3_pair<T, true>(x), e4m3_pair<T, false>(y), e4m3_pair<T, true>(y)};
+    }
+  }
+  // Value operands of the elements j and j + 1 (j even) of run r: 8 tokens each.
+  __device__ __forceinline__ void values(int r, int j, at_u32x4* lo, at_u32x4* hi) const {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if constexpr (E == 2) {
+        const uint32_t x = v[2 * t][r][j / 2], y = v[2 * t + 1][r][j / 2];
+        (*lo)[t] = __builtin_amdgcn_perm(y, x, 0x05040100);
+        (*hi)[t] = __builtin_amdgcn_perm(y, x, 0x07060302);
+      } else {
+        const int x = int(v[2 * t][r][j / 4]), y = int(v[2 * t + 1][r][j / 4]);
+        const at_f32x2 a = j % 4 ? __builtin_amdgcn_cvt_pk_f32_fp8(x, true) : __builtin_amdgcn_cvt_pk_f32_fp8(x, false);
+        const at_f32x2 b = j % 4 ? __builtin_amdgcn_cvt_pk_f32_fp8(y, true) : __builtin_amdgcn_cvt_pk_f32_fp8(y, false);
+        (*lo)[t] = T::pack_exact(a.x, b.x);
+        (*hi)[t] = T::pack_exact(a.y, b.y);
+      }
+    }
+  }
+};
+
+// Byte offsets of the rows that a lane reads of a tile.
+template <bool OCT>
+struct Rows {
+  int64_t k[OCT ? 1 : 2], v[OCT ? 1 : 8];
+};
+
+// ------------------------------------------------------------------ kernel --
+
+// OCT: the page size is a multiple of 8, so 8 tokens from a multiple of 8 lie
+// on one page and one lookup serves them; otherwise every row is looked up.
+template <class T, int D, int E, bool OCT>
+__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) decode_kernel(AttnArgs a, Work work) {
+  typedef Tile<T, D, E> TileT;
+  constexpr int kSteps = TileT::kSteps, kRun = TileT::kRun, kRuns = TileT::kRuns;
+  constexpr int kBlocks = D / 16;                        // MFMAs of the value product
+  __shared__ float lds_o[4][kRows][D + 4];
+  __shared__ float lds_m[4][kRows], lds_l[4][kRows];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, c = lane & 15;
+  const int blocks_per_head = (a.group + kRows - 1) / kRows;
+  const int units = a.kv.heads * blocks_per_head;
+
+  // this workgroup's piece [item, end) of the list: sequence, unit, tile
+  int64_t total = 0;
+  for (int base = 0; base < a.kv.seqs; base += 64) {
+    const int s = base + lane;
+    int t = s < a.kv.seqs ? seq_span(a, s).tiles : 0;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) t += __shfl_xor(t, d);
+    total += __builtin_amdgcn_readfirstlane(t);
+  }
+  total *= units;
+  const int64_t wgs = min(int64_t(gridDim.x), total);
+  const int64_t wg = blockIdx.x;
+  if (wg >= wgs) return;
+  int64_t item = wg * total / wgs;
+  const int64_t end = (wg + 1) * total / wgs;
+
+  // the sequence of `item` and the place in the list where it begins
+  int seq = 0;
+  int64_t seq_begin = 0;
+  for (int base = 0; base < a.kv.seqs; base += 64) {
+    const int s = base + lane;
+    const int t = s < a.kv.seqs ? seq_span(a, s).tiles : 0;
+    int in = t;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(in, d);
+      if (lane >= d) in += y;
+    }
+    const uint64_t past = __ballot(seq_begin + int64_t(in) * units > item);
+    if (past) {
+      const int l = __ffsll((unsigned long long)past) - 1;
+      seq = base + l;
+      seq_begin += int64_t(__builtin_amdgcn_readlane(in - t, l)) * units;
+      break;
+    }
+    seq_begin += int64_t(__builtin_amdgcn_readlane(in, 63)) * units;
+  }
+
+  while (item < end && seq < a.kv.seqs) {
+    const SeqSpan sp = seq_span(a, seq);
+    const int64_t in_seq = item - seq_begin;
+    if (in_seq >= int64_t(sp.tiles) * units) {
+      seq_begin += int64_t(sp.tiles) * units;
+      ++seq;
+      continue;
+    }
+    const int unit = int(in_seq / sp.tiles);
+    const int64_t unit_begin = seq_begin + int64_t(unit) * sp.tiles;
+    const int t0 = int(item - unit_begin);
+    const int t1 = int(min(int64_t(sp.tiles), end - unit_begin));
+    item += t1 - t0;
+
+    const int head = unit / blocks_per_head;
+    const int row0 = (unit % blocks_per_head) * kRows;
+    const int rows = min(a.group - row0, kRows);
+    const float cs = a.scale_log2 * (E == 1 && a.kv.k_scale ? a.kv.k_scale[head] : 1.0f);
+    const int32_t* table = a.kv.tables + seq * a.kv.table_stride;
+    const uint8_t* kbase = static_cast<const uint8_t*>(a.kv.k) + head * a.kv.head_stride * E;
+    const uint8_t* vbase = static_cast<const uint8_t*>(a.kv.v) + head * a.kv.head_stride * E;
+    const int64_t step = a.kv.token_stride * E;
+
+    // query operand: row c, zero past the unit's rows
+    at_u32x4 q[kSteps];
+    {
+      const uint16_t* qp = static_cast<const uint16_t*>(a.q) + seq * a.q_row +
+                           (int64_t(head) * a.group + row0 + min(c, rows - 1)) * a.q_head;
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        q[j] = *reinterpret_cast<const at_u32x4*>(qp + TileT::key_dim(j, g));
+        if (c >= rows) q[j] = (at_u32x4){0, 0, 0, 0};
+      }
+    }
+
+    at_f32x4 o[kBlocks];
+    float m, l;
+    bool bad = sp.over, both = true;      // both: the weights' second parts are used
+
+    // first token of this wave's part of tile t, and the end of its range
+    auto tile_at = [&](int t, int* stop) {
+      const bool sink = t < sp.sink_tiles;
+      *stop = sink ? sp.sink_end : sp.len;
+      return (sink ? t * kTile : sp.start + (t - sp.sink_tiles) * kTile) + wave * 32;
+    };
+    auto seen = [&](int t, int stop) { return t < stop && (t >= sp.low || t < a.sinks); };
+    // The row of token t; `any`: whether a query sees a token that is read with
+    // it.  A missing page is read as page 0, and spoils the result if seen.
+    auto row_of = [&](int t, bool any) -> int64_t {
+      int slot;
+      const int p = kv_page(a.kv, table, t, &slot);
+      bad |= p < 0 && any;
+      return (int64_t(max(p, 0)) * a.kv.page_stride + slot * a.kv.token_stride) * E;
+    };
+    // Rows past the end of the range are those of its last token (last 8 tokens).
+    auto find = [&](Rows<OCT>& r, int t) {
+      int stop;
+      const int base = tile_at(t, &stop);
+      if (base >= stop) return;
+      if constexpr (OCT) {
+        const int last = (stop - 1) & ~7;
+        const int kt = base + 8 * (c >> 2), vt = base + 8 * g;
+        r.k[0] = row_of(min(kt, last), kt < stop && (min(kt + 7, stop - 1) >= sp.low || kt < a.sinks));
+        r.v[0] = row_of(min(vt, last), false);     // the same pages as the keys'
+      } else {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int kt = base + 8 * (c >> 2) + 4 * b + (c & 3);
+          r.k[b] = row_of(min(kt, stop - 1), seen(kt, stop));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.v[i] = row_of(min(base + 8 * g + i, stop - 1), false);
+      }
+    };
+    auto load = [&](TileT& x, const Rows<OCT>& r, int t) {
+      int stop;
+      if (tile_at(t, &stop) >= stop) return;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        x.load_k(b, kbase + (OCT ? r.k[0] + (4 * b + (c & 3)) * step : r.k[OCT ? 0 : b]), g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x.load_v(i, vbase + (OCT ? r.v[0] + i * step : r.v[OCT ? 0 : i]), c);
+    };
+    auto compute = [&](TileT& x, int t) {
+      int stop;
+      const int base = tile_at(t, &stop);
+      if (base >= stop) return;
+      at_f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) s[b] = T::mfma16(x.key(b, j), q[j], s[b]);
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = s[i >> 2][i & 3] * cs;
+      if (!(base + 32 <= stop && (base >= sp.low || base + 32 <= a.sinks))) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!seen(base + 8 * g + i, stop)) {
+            p[i] = kNegInf;
+            x.clear_v(i);      // 0 x Inf and 0 x NaN would reach the sum
+          }
+      }
+      float mx = p[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, p[i]);
+      mx = max_xor32(max_xor16(mx));
+      if (__any(mx > m)) {
+        const float mn = fmaxf(m, mx), f = rebase(m, mn);
+#pragma unroll
+        for (int j = 0; j < kBlocks; ++j) o[j] *= f;
+        l *= f;
+        m = mn;
+      }
+      const float mm = m == kNegInf ? 0.0f : m;
+      at_u32x4 hi, lo;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = exp2_fast(p[i] - mm);
+        l += p[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        hi[i] = T::pack(p[2 * i], p[2 * i + 1]);
+        lo[i] = T::pack(p[2 * i] - T::low(hi[i]), p[2 * i + 1] - T::high(hi[i]));
+      }
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r)
+#pragma unroll
+        for (int j = 0; j < kRun; j += 2) {
+          at_u32x4 v0, v1;
+          x.values(r, j, &v0, &v1);
+          o[r * kRun + j] = T::mfma16(v0, hi, o[r * kRun + j]);
+          o[r * kRun + j + 1] = T::mfma16(v1, hi, o[r * kRun + j + 1]);
+          if (both) {
+            o[r * kRun + j] = T::mfma16(v0, lo, o[r * kRun + j]);
+            o[r * kRun + j + 1] = T::mfma16(v1, lo, o[r * kRun + j + 1]);
+          }
+        }
+    };
+
+    // Two tiles in registers: one is computed while the next one's loads (and
+    // the table lookups of the one after it) are in flight.  A sum that is not
+    // finite is taken again without the weights' second parts, which may be 0 or
+    // negative: times an Inf that the queries see they would give NaN.
+    for (;;) {
+#pragma unroll
+      for (int j = 0; j < kBlocks; ++j) o[j] = (at_f32x4){0, 0, 0, 0};
+      m = kNegInf;
+      l = 0.0f;
+      TileT x, y;
+      Rows<OCT> r;
+      find(r, t0);
+      load(x, r, t0);
+      if (t0 + 1 < t1) find(r, t0 + 1);
+      for (int t = t0; t < t1; t += 2) {
+        if (t + 1 < t1) load(y, r, t + 1);
+        if (t + 2 < t1) find(r, t + 2);
+        compute(x, t);
+        if (t + 1 >= t1) break;
+        if (t + 2 < t1) load(x, r, t + 2);
+        if (t + 3 < t1) find(r, t + 3);
+        compute(y, t + 1);
+      }
+      if (!both) break;
+      bool odd = false;
+#pragma unroll
+      for (int j = 0; j < kBlocks; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) odd |= !(fabsf(o[j][i]) < -kNegInf);
+      if (!__any(odd)) break;
+      both = false;
+    }
+
+    // merge the waves
+    l = sum_xor32(sum_xor16(l));
+    if (__any(bad)) l = __builtin_nanf("");
+    if (c < rows) {
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          lds_o[wave][c][(b / kRun) * 128 + (4 * g + i) * kRun + b % kRun] = o[b][i];
+      if (g == 0) {
+        lds_m[wave][c] = m;
+        lds_l[wave][c] = l;
+      }
+    }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == sp.tiles;
+    const int64_t u = int64_t(seq) * units + unit;
+    if (t0 == 0 && threadIdx.x == 0) {
+      const int64_t last = unit_begin + sp.tiles - 1;      // the unit's last item is in workgroup ...
+      work.first[u] = int32_t(wg);
+      work.count[u] = int32_t(((last + 1) * wgs - 1) / total - wg + 1);
+    }
+    const Partial part = partial_at(work, D, wg, t0 == 0);
+    for (int e = threadIdx.x; e < rows * (D / 4); e += 256) {
+      const int r = e / (D / 4), d = 4 * (e - r * (D / 4));
+      float M = lds_m[0][r];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) M = fmaxf(M, lds_m[w][r]);
+      float L = 0.0f;
+      at_f32x4 O = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = rebase(lds_m[w][r], M);
+        L += f * lds_l[w][r];
+        O += *reinterpret_cast<const at_f32x4*>(&lds_o[w][r][d]) * f;
+      }
+      if (whole) {
+        const int h = head * a.group + row0 + r;
+        const float inv = (E == 1 && a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / L;
+        const bool none = sp.len == 0 && !sp.over;
+        at_u32x2 y = {T::pack(O[0] * inv, O[1] * inv), T::pack(O[2] * inv, O[3] * inv)};
+        if (none) y = (at_u32x2){0, 0};
+        *reinterpret_cast<at_u32x2*>(static_cast<uint16_t*>(a.out) + seq * a.o_row + h * a.o_head + d) = y;
+        if (a.lse && d == 0)
+          a.lse[int64_t(seq) * a.q_heads + h] = none ? kNegInf : (M + __log2f(L)) * 0.693147180559945f;
+      } else {
+        *reinterpret_cast<at_f32x4*>(part.o + r * D + d) = O;
+        if (d == 0) {
+          part.m[r] = M;
+          part.l[r] = L;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the partial results of units that were cut: grid (seqs x units, rows).
+// D / 4 threads hold a column quad each, the rest of the 256 share the parts.
+template <class T, int D, int E>
+__global__ void __launch_bounds__(256) decode_join_kernel(AttnArgs a, Work work) {
+  constexpr int kQuads = D / 4, kSplits = 256 / kQuads;
+  __shared__ at_f32x4 lds_o[kSplits][kQuads];
+  __shared__ float lds_m[kSplits], lds_l[kSplits];
+  const int n = work.count[blockIdx.x];
+  if (n <= 1) return;
+  const int blocks_per_head = (a.group + kRows - 1) / kRows;
+  const int units = a.kv.heads * blocks_per_head;
+  const int seq = blockIdx.x / units, unit = blockIdx.x % units;
+  const int head = unit / blocks_per_head, row0 = (unit % blocks_per_head) * kRows;
+  const int r = blockIdx.y;
+  if (r >= min(a.group - row0, kRows)) return;
+  const int first = work.first[blockIdx.x];
+  const int quad = threadIdx.x % kQuads, split = threadIdx.x / kQuads;
+  float M = kNegInf, L = 0.0f;
+  at_f32x4 O = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int i = split; i < n; i += kSplits) {
+    const Partial p = partial_at(work, D, first + i, i == 0);
+    const float m = p.m[r], l = p.l[r];
+    const at_f32x4 o = *reinterpret_cast<const at_f32x4*>(p.o + r * D + 4 * quad);
+    const float mn = fmaxf(M, m), f = rebase(M, mn), h = rebase(m, mn);
+    L = L * f + l * h;
+    O = O * f + o * h;
+    M = mn;
+  }
+  lds_o[split][quad] = O;
+  if (quad == 0) {
+    lds_m[split] = M;
+    lds_l[split] = L;
+  }
+  __syncthreads();
+  if (split) return;
+  M = lds_m[0];
+  for (int i = 1; i < kSplits; ++i) M = fmaxf(M, lds_m[i]);
+  L = 0.0f;
+  O = (at_f32x4){0, 0, 0, 0};
+  for (int i = 0; i < kSplits; ++i) {
+    const float f = rebase(lds_m[i], M);
+    L += f * lds_l[i];
+    O += lds_o[i][quad] * f;
+  }
+  const int h = head * a.group + row0 + r;
+  const float inv = (E == 1 && a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / L;
+  const at_u32x2 y = {T::pack(O[0] * inv, O[1] * inv), T::pack(O[2] * inv, O[3] * inv)};
+  *reinterpret_cast<at_u32x2*>(static_cast<uint16_t*>(a.out) + seq * a.o_row + h * a.o_head + 4 * quad) = y;
+  if (a.lse && quad == 0) a.lse[int64_t(seq) * a.q_heads + h] = (M + __log2f(L)) * 0.693147180559945f;
+}
+
+// Workgroups of a full card: 256 CUs times the workgroups that fit one.
+constexpr int kWgs = 512;
+
+template <class T, int D, int E>
+hipError_t launch(const AttnArgs& a, const Work& w, unsigned grid, int64_t units, hipStream_t stream) {
+  if (a.kv.page.d % 8 == 0)
+    decode_kernel<T, D, E, true><<<grid, 256, 0, stream>>>(a, w);
+  else
+    decode_kernel<T, D, E, false><<<grid, 256, 0, stream>>>(a, w);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  decode_join_kernel<T, D, E><<<dim3(unsigned(units), unsigned(w.rows)), 256, 0, stream>>>(a, w);
+  return hipGetLastError();
+}
+
+template <class T, int E>
+hipError_t launch_dim(const AttnArgs& a, const Work& w, int D, unsigned grid, int64_t units, hipStream_t stream) {
+  if (D == 64) return launch<T, 64, E>(a, w, grid, units, stream);
+  if (D == 128) return launch<T, 128, E>(a, w, grid, units, stream);
+  return launch<T, 256, E>(a, w, grid, units, stream);
+}
+
+int64_t all_units(int64_t seqs, int q_heads, int heads) {
+  return seqs * heads * ((q_heads / heads + kRows - 1) / kRows);
+}
+
+}  // namespace
+
+// [parts] [first] [count]
+size_t attn_decode_workspace(int64_t seqs, int q_heads, int heads, int head_dim) {
+  const int rows = std::min(q_heads / heads, kRows);
+  return size_t(kWgs) * 2 * partial_floats(rows, head_dim) * 4 + size_t(all_units(seqs, q_heads, heads)) * 8;
+}
+
+hipError_t launch_attn_decode(const AttnArgs& a, int cache_dtype, int dtype, int head_dim, void* workspace,
+                              hipStream_t stream) {
+  const int64_t units = all_units(a.kv.seqs, a.q_heads, a.kv.heads);
+  Work w;
+  w.rows = std::min(a.group, kRows);
+  w.parts = static_cast<float*>(workspace);
+  w.first = reinterpret_cast<int32_t*>(w.parts + size_t(kWgs) * 2 * partial_floats(w.rows, head_dim));
+  w.count = w.first + units;
+  // no more workgroups than tiles that the tables can hold
+  const int64_t tiles = (int64_t(a.kv.max_pages) * a.kv.page.d + kTile - 1) / kTile + 2;
+  const unsigned grid = unsigned(std::min<int64_t>(kWgs, units * tiles));
+  const bool e4m3 = cache_dtype == W4A4_E4M3;
+  if (dtype == W4A4_BF16)
+    return e4m3 ? launch_dim<Bf16, 1>(a, w, head_dim, grid, units, stream)
+                : launch_dim<Bf16, 2>(a, w, head_dim, grid, units, stream);
+  return e4m3 ? launch_dim<F16, 1>(a, w, head_dim, grid, units, stream)
+              : launch_dim<F16, 2>(a, w, head_dim, grid, units, stream);
+}
+
+}  // namespace w4a4

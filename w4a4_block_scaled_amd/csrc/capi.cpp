@@ -9,12 +9,15 @@
 
 #include "common.h"
 #include "kernels.h"
+#include "status.h"
 
 static_assert(W4A4_NOALLOC_SCRATCH_BYTES == w4a4::kNoAllocScratchBytes, "scratch size");
 
 namespace {
-
 thread_local char g_err[512] = "";
+}
+
+namespace w4a4 {
 
 w4a4_status fail(w4a4_status st, const char* fmt, ...) {
   va_list ap;
@@ -28,6 +31,20 @@ w4a4_status ok() {
   g_err[0] = 0;
   return W4A4_OK;
 }
+
+w4a4_status hip_status(hipError_t e, const char* what) {
+  if (e != hipSuccess) return fail(W4A4_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+  return ok();
+}
+
+}  // namespace w4a4
+
+namespace {
+
+using w4a4::aligned;
+using w4a4::fail;
+using w4a4::hip_status;
+using w4a4::ok;
 
 bool valid_fmt(w4a4_format f) {
   return f == W4A4_MXFP4 || f == W4A4_NVFP4 || f == W4A4_MXINT4 || f == W4A4_MXFP8 ||
@@ -63,13 +80,6 @@ w4a4_status check_int_shape(w4a4_format fmt, int64_t N, int64_t K) {
 w4a4_status not_for_int(w4a4_format fmt, const char* what) {
   return fail(W4A4_ERR_FORMAT, "%s: not available for %s (MX and NVFP4 formats only)", what,
               bf16_int_name(fmt));
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-w4a4_status hip_status(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(W4A4_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  return ok();
 }
 
 // (K % 128, N % 16) shapes of the packed GEMM
