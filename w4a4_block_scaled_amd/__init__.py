@@ -21,6 +21,7 @@ functions raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -407,13 +408,13 @@ def _kv_type(t: torch.Tensor, what: str) -> int:
 
 def _int32(what: str, device, *tensors) -> None:
     for t in tensors:
-        if t is not None and (t.dtype != torch.int32 or t.device != device or
-                              (t.dim() == 1 and t.stride(0) != 1 and t.numel() > 1)):
+        if t is not None and (t.dtype != torch.int32 or t.device != device or (t.dim() == 1 and not t.is_contiguous())):
             raise W4A4Error(2, f"{what}: index tensors are int32, on {device}, with contiguous entries")
 
 
 def _kv_cache(what: str, k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> _KvCache:
-    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1 or k.dtype != v.dtype or \
+    shape, stride = k.shape, k.stride()
+    if len(shape) != 4 or shape != v.shape or stride != v.stride() or stride[3] != 1 or k.dtype != v.dtype or \
             k.device != v.device:
         raise W4A4Error(2, f"{what}: caches {tuple(k.shape)} and {tuple(v.shape)} must be alike, [pages, page_size, "
                            "heads, head_dim] with a contiguous last dimension")
@@ -421,32 +422,48 @@ def _kv_cache(what: str, k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> 
     ks = vs = None
     if f == 2:
         for t in (k_scale, v_scale):
-            if t is not None and (t.dtype != torch.float32 or t.numel() != k.shape[2] or not t.is_contiguous() or
+            if t is not None and (t.dtype != torch.float32 or t.numel() != shape[2] or not t.is_contiguous() or
                                   t.device != k.device):
                 raise W4A4Error(2, f"{what}: scales are contiguous float32 [heads] on the cache's device")
         ks, vs = (None if t is None else t.data_ptr() for t in (k_scale, v_scale))
     elif k_scale is not None or v_scale is not None:
         raise W4A4Error(4, f"{what}: scales belong to a float8_e4m3fn cache")
-    pages, page, heads, dim = k.shape
-    ps, ts, hs, _ = k.stride()
-    return _KvCache(k.data_ptr(), v.data_ptr(), ks, vs, ps, ts, hs, f, pages, page, heads, dim)
+    pages, page, heads, dim = shape
+    return _KvCache(k.data_ptr(), v.data_ptr(), ks, vs, stride[0], stride[1], stride[2], f, pages, page, heads, dim)
 
 
 def _kv_seqs(what: str, tables: torch.Tensor, lens: Optional[torch.Tensor], device) -> _KvSeqs:
-    if tables.dim() != 2 or (tables.shape[1] > 1 and tables.stride(1) != 1) or \
-            (lens is not None and tuple(lens.shape) != (tables.shape[0],)):
+    shape = tables.shape
+    if len(shape) != 2 or (shape[1] > 1 and tables.stride(1) != 1) or \
+            (lens is not None and (lens.dim() != 1 or lens.shape[0] != shape[0])):
         raise W4A4Error(2, f"{what}: tables {tuple(tables.shape)} must be [seqs, max_pages] with contiguous rows, lens [seqs]")
     _int32(what, device, tables, lens)
-    seqs, width = tables.shape
+    seqs, width = shape
     return _KvSeqs(tables.data_ptr(), None if lens is None else lens.data_ptr(),
                    tables.stride(0) if seqs > 1 else width, seqs, width)
 
 
-def _kv_rows(what: str, x: torch.Tensor, rows: int, heads, dim: int, like: torch.Tensor) -> None:
-    if x.dim() != 3 or x.shape[0] != rows or x.shape[2] != dim or (heads is not None and x.shape[1] != heads) or \
-            x.stride(2) != 1 or x.device != like.device:
+def _kv_rows(what: str, x: torch.Tensor, rows: int, heads, dim: int, device) -> Tuple[int, int, int]:
+    """(address, row stride, head stride) of rows x [rows, heads, dim]; heads None: any number."""
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != rows or shape[2] != dim or (heads is not None and shape[1] != heads) or \
+            stride[2] != 1 or x.device != device:
         raise W4A4Error(2, f"{what}: {tuple(x.shape)} (need [{rows}, {'heads' if heads is None else heads}, {dim}] with a "
-                           f"contiguous last dimension, on {like.device})")
+                           f"contiguous last dimension, on {device})")
+    return x.data_ptr(), stride[0], stride[1]
+
+
+def _kv_stream(device: torch.device) -> int:
+    """Handle of the current stream of `device` (_stream without the torch.cuda.Stream object)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
+
+
+@functools.lru_cache(maxsize=4096)
+def _attn_workspace_bytes(prefill: bool, dtype: int, heads: int, dim: int, seqs: int, tokens: int, q_heads: int) -> int:
+    """w4a4_attn_*_workspace_bytes: depends on these numbers alone."""
+    c = _KvCache(16, 16, None, None, 0, 0, 0, dtype, 1, 1, heads, dim)
+    return (lib().w4a4_attn_prefill_workspace_bytes(c, seqs, tokens, q_heads) if prefill else
+            lib().w4a4_attn_decode_workspace_bytes(c, seqs, q_heads))
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, tables: torch.Tensor,
@@ -458,20 +475,21 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     cu_seqlens int32 [seqs + 1]: sequence s has the rows cu[s] .. cu[s + 1] - 1,
     its last tokens; None: one row per sequence.
     """
+    dev = k_cache.device
     c = _kv_cache("kv_append", k_cache, v_cache, k_scale, v_scale)
-    s = _kv_seqs("kv_append", tables, lens, k_cache.device)
+    s = _kv_seqs("kv_append", tables, lens, dev)
     tokens = k.shape[0]
-    _kv_rows("kv_append: k", k, tokens, c.heads, c.head_dim, k_cache)
-    _kv_rows("kv_append: v", v, tokens, c.heads, c.head_dim, k_cache)
+    rows = (*_kv_rows("kv_append: k", k, tokens, c.heads, c.head_dim, dev),
+            *_kv_rows("kv_append: v", v, tokens, c.heads, c.head_dim, dev))
     if k.dtype != v.dtype:
         raise W4A4Error(4, f"kv_append: k is {k.dtype}, v is {v.dtype}")
+    cu = None
     if cu_seqlens is not None:
-        _int32("kv_append", k_cache.device, cu_seqlens)
+        _int32("kv_append", dev, cu_seqlens)
         if cu_seqlens.numel() != s.seqs + 1:
             raise W4A4Error(2, f"kv_append: cu_seqlens has {cu_seqlens.numel()} entries for {s.seqs} sequences")
-    _check(lib().w4a4_kv_append(c, s, None if cu_seqlens is None else cu_seqlens.data_ptr(), tokens,
-                                _kv_type(k, "kv_append"), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-                                v.stride(0), v.stride(1), _stream(k_cache.device)))
+        cu = cu_seqlens.data_ptr()
+    _check(lib().w4a4_kv_append(c, s, cu, tokens, _kv_type(k, "kv_append"), *rows, _kv_stream(dev)))
 
 
 def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, scale, window, sinks, out, return_lse,
@@ -479,31 +497,31 @@ def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, sc
     dev = k_cache.device
     c = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
     s = _kv_seqs(name, tables, lens, dev)
-    L = lib()
-    rows, q_heads = q.shape[0], q.shape[1]
-    _kv_rows(name + ": q", q, s.seqs if cu is None else rows, None, c.head_dim, k_cache)
-    if out is None:
-        out = torch.empty((rows, q_heads, c.head_dim), dtype=q.dtype, device=dev)
-    else:
-        _kv_rows(name + ": out", out, rows, q_heads, c.head_dim, k_cache)
-        if out.dtype != q.dtype:
-            raise W4A4Error(4, f"{name}: out is {out.dtype}, q is {q.dtype}")
-    lse = torch.empty((rows, q_heads), dtype=torch.float32, device=dev) if return_lse else None
-    if cu is None:
-        need = L.w4a4_attn_decode_workspace_bytes(c, rows, q_heads)
-    else:
+    rows, q_heads, dim = q.shape[0], q.shape[1], c.head_dim
+    q_at = _kv_rows(name + ": q", q, s.seqs if cu is None else rows, None, dim, dev)
+    if cu is not None:
         _int32(name, dev, cu)
         if cu.numel() != s.seqs + 1:
             raise W4A4Error(2, f"{name}: cu_seqlens has {cu.numel()} entries for {s.seqs} sequences")
-        need = L.w4a4_attn_prefill_workspace_bytes(c, s.seqs, rows, q_heads)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    tail = (_kv_type(q, name), q_heads, q.data_ptr(), q.stride(0), q.stride(1),
-            c.head_dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), out.stride(0), out.stride(1),
-            None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(dev))
-    _check(L.w4a4_attn_decode(c, s, *tail) if cu is None else
-           L.w4a4_attn_prefill(c, s, cu.data_ptr(), rows, *tail))
+    if out is None:
+        out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=dev)
+        out_at = (out.data_ptr(), q_heads * dim, dim)
+    else:
+        out_at = _kv_rows(name + ": out", out, rows, q_heads, dim, dev)
+        if out.dtype != q.dtype:
+            raise W4A4Error(4, f"{name}: out is {out.dtype}, q is {q.dtype}")
+    lse = torch.empty((rows, q_heads), dtype=torch.float32, device=dev) if return_lse else None
+    if workspace is None:
+        size = _attn_workspace_bytes(cu is not None, c.dtype, c.heads, dim, s.seqs, rows, q_heads)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    else:
+        size = workspace.numel() * workspace.element_size()
+    tail = (_kv_type(q, name), q_heads, *q_at, dim ** -0.5 if scale is None else scale, window, sinks, *out_at,
+            None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), size,
+            _kv_stream(dev))
+    L = lib()
+    _check(L.w4a4_attn_decode(c, s, *tail) if cu is None else L.w4a4_attn_prefill(c, s, cu.data_ptr(), rows, *tail))
     return (out, lse) if return_lse else out
 
 
@@ -577,7 +595,7 @@ def kv_copy_pages(caches, src: torch.Tensor, dst: torch.Tensor) -> None:
     n, arrays, stride, size, pages, _, dev = _kv_arrays("kv_copy_pages", caches)
     _int32("kv_copy_pages", dev, src, dst)
     pairs = _same_length("kv_copy_pages", src, dst)
-    _check(lib().w4a4_kv_copy_pages(n, arrays, stride, size, pages, src.data_ptr(), dst.data_ptr(), pairs, _stream(dev)))
+    _check(lib().w4a4_kv_copy_pages(n, arrays, stride, size, pages, src.data_ptr(), dst.data_ptr(), pairs, _kv_stream(dev)))
 
 
 def kv_reserve(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int, *,
@@ -589,7 +607,7 @@ def kv_reserve(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, pag
     ws = _kv_workspace(s.seqs, refs.numel(), refs.device)
     _check(lib().w4a4_kv_reserve(s, page_size, refs.data_ptr(), refs.numel(),
                                  None if lacking is None else lacking.data_ptr(), ws.data_ptr(), ws.numel(),
-                                 _stream(refs.device)))
+                                 _kv_stream(refs.device)))
 
 
 def _check_pages(what: str, refs: torch.Tensor, pages: int) -> None:
@@ -609,7 +627,7 @@ def kv_fork(caches, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor
     ws = _kv_workspace(count, pages, dev)
     _check(lib().w4a4_kv_fork(n, arrays, stride, size, s, page, refs.data_ptr(), pages, parents.data_ptr(),
                               children.data_ptr(), count, None if lacking is None else lacking.data_ptr(),
-                              ws.data_ptr(), ws.numel(), _stream(dev)))
+                              ws.data_ptr(), ws.numel(), _kv_stream(dev)))
 
 
 def kv_free(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, seqs: Optional[torch.Tensor] = None) -> None:
@@ -617,7 +635,7 @@ def kv_free(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, seqs: 
     s = _kv_seqs("kv_free", tables, lens, refs.device)
     _int32("kv_free", refs.device, refs, seqs)
     _check(lib().w4a4_kv_free(s, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
-                              s.seqs if seqs is None else seqs.numel(), _stream(refs.device)))
+                              s.seqs if seqs is None else seqs.numel(), _kv_stream(refs.device)))
 
 
 def kv_trim(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int, window: int, sinks: int = 0,
@@ -627,7 +645,7 @@ def kv_trim(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_s
     s = _kv_seqs("kv_trim", tables, lens, refs.device)
     _int32("kv_trim", refs.device, refs, seqs)
     _check(lib().w4a4_kv_trim(s, page_size, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
-                              s.seqs if seqs is None else seqs.numel(), window, sinks, _stream(refs.device)))
+                              s.seqs if seqs is None else seqs.numel(), window, sinks, _kv_stream(refs.device)))
 
 
 def kv_compact(caches, tables: torch.Tensor, refs: torch.Tensor) -> torch.Tensor:
@@ -640,5 +658,5 @@ def kv_compact(caches, tables: torch.Tensor, refs: torch.Tensor) -> torch.Tensor
     remap = torch.empty(pages, dtype=torch.int32, device=dev)
     ws = _kv_workspace(0, pages, dev)
     _check(lib().w4a4_kv_compact(n, arrays, stride, size, s, refs.data_ptr(), pages, remap.data_ptr(), ws.data_ptr(),
-                                 ws.numel(), _stream(dev)))
+                                 ws.numel(), _kv_stream(dev)))
     return remap

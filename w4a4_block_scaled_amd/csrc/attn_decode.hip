@@ -36,10 +36,10 @@ struct SeqSpan {
   bool over;
 };
 
-__device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, int s) {
+__device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, int length) {
   SeqSpan z;
   const int cap = int(min(int64_t(a.kv.max_pages) * a.kv.page.d, int64_t(1) << 30));
-  const int len = max(a.kv.lens[s], 0);
+  const int len = max(length, 0);
   z.over = len > cap;
   z.len = min(len, cap);
   z.low = a.window ? max(z.len - a.window, 0) : 0;   // first token of the window
@@ -149,18 +149,21 @@ struct Tile {
   }
 };
 
-// Byte offsets of the rows that a lane reads of a tile.
+// Table entries and page rows of the tokens that a lane reads of a tile.
 template <bool OCT>
 struct Rows {
-  int64_t k[OCT ? 1 : 2], v[OCT ? 1 : 8];
+  int page[OCT ? 2 : 10], slot[OCT ? 2 : 10];      // of the keys, then of the values
 };
 
 // ------------------------------------------------------------------ kernel --
 
+// Workgroups that share a CU: what the registers of two tiles leave room for.
+constexpr int wgs_per_cu(int D, int E, bool oct) { return D == 256 ? 1 : oct && D == 64 ? 3 : 2; }
+
 // OCT: the page size is a multiple of 8, so 8 tokens from a multiple of 8 lie
 // on one page and one lookup serves them; otherwise every row is looked up.
 template <class T, int D, int E, bool OCT>
-__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) decode_kernel(AttnArgs a, Work work) {
+__global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(AttnArgs a, Work work) {
   typedef Tile<T, D, E> TileT;
   constexpr int kSteps = TileT::kSteps, kRun = TileT::kRun, kRuns = TileT::kRuns;
   constexpr int kBlocks = D / 16;                        // MFMAs of the value product
@@ -172,46 +175,50 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) decode_kernel(AttnArgs 
   const int blocks_per_head = (a.group + kRows - 1) / kRows;
   const int units = a.kv.heads * blocks_per_head;
 
-  // this workgroup's piece [item, end) of the list: sequence, unit, tile
-  int64_t total = 0;
-  for (int base = 0; base < a.kv.seqs; base += 64) {
-    const int s = base + lane;
-    int t = s < a.kv.seqs ? seq_span(a, s).tiles : 0;
+  // This workgroup's piece [item, end) of the list of (sequence, unit, tile),
+  // and the sequence that `item` falls in, with the place where that begins.
+  // Lane l looks after the sequences l, l + 64, ...; up to 64 sequences take one
+  // load of the lengths.
+  auto length = [&](int s) { return s < a.kv.seqs ? a.kv.lens[s] : 0; };
+  auto tiles_of = [&](int s, int len) { return s < a.kv.seqs ? seq_span(a, len).tiles : 0; };
+  auto scan = [&](int t) {
 #pragma unroll
-    for (int d = 32; d; d >>= 1) t += __shfl_xor(t, d);
-    total += __builtin_amdgcn_readfirstlane(t);
-  }
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(t, d);
+      if (lane >= d) t += y;
+    }
+    return t;
+  };
+  const int len0 = length(lane), mine0 = tiles_of(lane, len0), in0 = scan(mine0);
+  int64_t total = __builtin_amdgcn_readlane(in0, 63);
+  for (int base = 64; base < a.kv.seqs; base += 64)
+    total += __builtin_amdgcn_readlane(scan(tiles_of(base + lane, length(base + lane))), 63);
   total *= units;
   const int64_t wgs = min(int64_t(gridDim.x), total);
   const int64_t wg = blockIdx.x;
   if (wg >= wgs) return;
   int64_t item = wg * total / wgs;
   const int64_t end = (wg + 1) * total / wgs;
-
-  // the sequence of `item` and the place in the list where it begins
   int seq = 0;
   int64_t seq_begin = 0;
   for (int base = 0; base < a.kv.seqs; base += 64) {
-    const int s = base + lane;
-    const int t = s < a.kv.seqs ? seq_span(a, s).tiles : 0;
-    int in = t;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int y = __shfl_up(in, d);
-      if (lane >= d) in += y;
+    int mine = mine0, in = in0;
+    if (base) {
+      mine = tiles_of(base + lane, length(base + lane));
+      in = scan(mine);
     }
     const uint64_t past = __ballot(seq_begin + int64_t(in) * units > item);
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
       seq = base + l;
-      seq_begin += int64_t(__builtin_amdgcn_readlane(in - t, l)) * units;
+      seq_begin += int64_t(__builtin_amdgcn_readlane(in - mine, l)) * units;
       break;
     }
     seq_begin += int64_t(__builtin_amdgcn_readlane(in, 63)) * units;
   }
 
   while (item < end && seq < a.kv.seqs) {
-    const SeqSpan sp = seq_span(a, seq);
+    const SeqSpan sp = seq_span(a, seq < 64 ? __builtin_amdgcn_readlane(len0, seq) : a.kv.lens[seq]);
     const int64_t in_seq = item - seq_begin;
     if (in_seq >= int64_t(sp.tiles) * units) {
       seq_begin += int64_t(sp.tiles) * units;
@@ -256,42 +263,51 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) decode_kernel(AttnArgs 
       return (sink ? t * kTile : sp.start + (t - sp.sink_tiles) * kTile) + wave * 32;
     };
     auto seen = [&](int t, int stop) { return t < stop && (t >= sp.low || t < a.sinks); };
-    // The row of token t; `any`: whether a query sees a token that is read with
-    // it.  A missing page is read as page 0, and spoils the result if seen.
-    auto row_of = [&](int t, bool any) -> int64_t {
-      int slot;
-      const int p = kv_page(a.kv, table, t, &slot);
-      bad |= p < 0 && any;
-      return (int64_t(max(p, 0)) * a.kv.page_stride + slot * a.kv.token_stride) * E;
-    };
-    // Rows past the end of the range are those of its last token (last 8 tokens).
+    // Tokens past the end of the range take the place of its last one (last 8
+    // tokens).  Only reads the table: what it gave is looked at in load(), an
+    // iteration later.
     auto find = [&](Rows<OCT>& r, int t) {
       int stop;
       const int base = tile_at(t, &stop);
-      if (base >= stop) return;
+      auto place = [&](int i, int u) {
+        const int j = a.kv.page.div(max(u, 0));
+        r.slot[i] = max(u, 0) - j * int(a.kv.page.d);
+        r.page[i] = table[j];
+      };
       if constexpr (OCT) {
         const int last = (stop - 1) & ~7;
-        const int kt = base + 8 * (c >> 2), vt = base + 8 * g;
-        r.k[0] = row_of(min(kt, last), kt < stop && (min(kt + 7, stop - 1) >= sp.low || kt < a.sinks));
-        r.v[0] = row_of(min(vt, last), false);     // the same pages as the keys'
+        place(0, min(base + 8 * (c >> 2), last));
+        place(1, min(base + 8 * g, last));
       } else {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int kt = base + 8 * (c >> 2) + 4 * b + (c & 3);
-          r.k[b] = row_of(min(kt, stop - 1), seen(kt, stop));
-        }
+        for (int b = 0; b < 2; ++b) place(b, min(base + 8 * (c >> 2) + 4 * b + (c & 3), stop - 1));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r.v[i] = row_of(min(base + 8 * g + i, stop - 1), false);
+        for (int i = 0; i < 8; ++i) place(2 + i, min(base + 8 * g + i, stop - 1));
       }
     };
+    // An entry outside the cache is read as page 0, and spoils the result if a
+    // query sees a token there (the keys' entries are the values').
     auto load = [&](TileT& x, const Rows<OCT>& r, int t) {
       int stop;
-      if (tile_at(t, &stop) >= stop) return;
+      const int base = tile_at(t, &stop);
+      auto row = [&](int i) -> int64_t {
+        const int p = uint32_t(r.page[i]) < uint32_t(a.kv.pages) ? r.page[i] : 0;
+        return (int64_t(p) * a.kv.page_stride + int64_t(r.slot[i]) * a.kv.token_stride) * E;
+      };
+      if constexpr (OCT) {
+        const int kt = base + 8 * (c >> 2);
+        bad |= uint32_t(r.page[0]) >= uint32_t(a.kv.pages) && kt < stop &&
+               (min(kt + 7, stop - 1) >= sp.low || kt < a.sinks);
+      } else {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-        x.load_k(b, kbase + (OCT ? r.k[0] + (4 * b + (c & 3)) * step : r.k[OCT ? 0 : b]), g);
+        for (int b = 0; b < 2; ++b)
+          bad |= uint32_t(r.page[b]) >= uint32_t(a.kv.pages) && seen(base + 8 * (c >> 2) + 4 * b + (c & 3), stop);
+      }
+      const int64_t k0 = row(0), v0 = row(OCT ? 1 : 2);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x.load_v(i, vbase + (OCT ? r.v[0] + i * step : r.v[OCT ? 0 : i]), c);
+      for (int b = 0; b < 2; ++b) x.load_k(b, kbase + (OCT ? k0 + (4 * b + (c & 3)) * step : b ? row(1) : k0), g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x.load_v(i, vbase + (OCT ? v0 + i * step : i ? row(OCT ? 1 : 2 + i) : v0), c);
     };
     auto compute = [&](TileT& x, int t) {
       int stop;
@@ -360,19 +376,34 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) decode_kernel(AttnArgs 
       for (int j = 0; j < kBlocks; ++j) o[j] = (at_f32x4){0, 0, 0, 0};
       m = kNegInf;
       l = 0.0f;
+      // No load depends on a condition inside the loop, and a tile's table
+      // entries are read before the loads of the tile ahead of it: loads come
+      // back in order, and waiting for either leaves the later ones in flight.
       TileT x, y;
-      Rows<OCT> r;
+      Rows<OCT> r, n;
+      auto at = [&](int t) { return min(t, t1 - 1); };
       find(r, t0);
+      find(n, at(t0 + 1));
       load(x, r, t0);
-      if (t0 + 1 < t1) find(r, t0 + 1);
-      for (int t = t0; t < t1; t += 2) {
-        if (t + 1 < t1) load(y, r, t + 1);
-        if (t + 2 < t1) find(r, t + 2);
+      int t = t0;
+      for (; t + 2 < t1; t += 2) {
+        find(r, t + 2);
+        load(y, n, t + 1);
+        __builtin_amdgcn_sched_barrier(0);
         compute(x, t);
-        if (t + 1 >= t1) break;
-        if (t + 2 < t1) load(x, r, t + 2);
-        if (t + 3 < t1) find(r, t + 3);
+        __builtin_amdgcn_sched_barrier(0);
+        find(n, at(t + 3));
+        load(x, r, t + 2);
+        __builtin_amdgcn_sched_barrier(0);
         compute(y, t + 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (t + 1 < t1) {
+        load(y, n, t + 1);
+        compute(x, t);
+        compute(y, t + 1);
+      } else {
+        compute(x, t);
       }
       if (!both) break;
       bool odd = false;
@@ -493,12 +524,15 @@ __global__ void __launch_bounds__(256) decode_join_kernel(AttnArgs a, Work work)
   if (a.lse && quad == 0) a.lse[int64_t(seq) * a.q_heads + h] = (M + __log2f(L)) * 0.693147180559945f;
 }
 
-// Workgroups of a full card: 256 CUs times the workgroups that fit one.
-constexpr int kWgs = 512;
+// Workgroups of a full card.
+int full_card(int D, int E, bool oct) { return 256 * wgs_per_cu(D, E, oct); }
+constexpr int kMaxWgs = 256 * 3;
 
 template <class T, int D, int E>
-hipError_t launch(const AttnArgs& a, const Work& w, unsigned grid, int64_t units, hipStream_t stream) {
-  if (a.kv.page.d % 8 == 0)
+hipError_t launch(const AttnArgs& a, const Work& w, int64_t tiles, int64_t units, hipStream_t stream) {
+  const bool oct = a.kv.page.d % 8 == 0;
+  const unsigned grid = unsigned(std::min<int64_t>(full_card(D, E, oct), tiles));
+  if (oct)
     decode_kernel<T, D, E, true><<<grid, 256, 0, stream>>>(a, w);
   else
     decode_kernel<T, D, E, false><<<grid, 256, 0, stream>>>(a, w);
@@ -509,10 +543,10 @@ hipError_t launch(const AttnArgs& a, const Work& w, unsigned grid, int64_t units
 }
 
 template <class T, int E>
-hipError_t launch_dim(const AttnArgs& a, const Work& w, int D, unsigned grid, int64_t units, hipStream_t stream) {
-  if (D == 64) return launch<T, 64, E>(a, w, grid, units, stream);
-  if (D == 128) return launch<T, 128, E>(a, w, grid, units, stream);
-  return launch<T, 256, E>(a, w, grid, units, stream);
+hipError_t launch_dim(const AttnArgs& a, const Work& w, int D, int64_t tiles, int64_t units, hipStream_t stream) {
+  if (D == 64) return launch<T, 64, E>(a, w, tiles, units, stream);
+  if (D == 128) return launch<T, 128, E>(a, w, tiles, units, stream);
+  return launch<T, 256, E>(a, w, tiles, units, stream);
 }
 
 int64_t all_units(int64_t seqs, int q_heads, int heads) {
@@ -524,7 +558,7 @@ int64_t all_units(int64_t seqs, int q_heads, int heads) {
 // [parts] [first] [count]
 size_t attn_decode_workspace(int64_t seqs, int q_heads, int heads, int head_dim) {
   const int rows = std::min(q_heads / heads, kRows);
-  return size_t(kWgs) * 2 * partial_floats(rows, head_dim) * 4 + size_t(all_units(seqs, q_heads, heads)) * 8;
+  return size_t(kMaxWgs) * 2 * partial_floats(rows, head_dim) * 4 + size_t(all_units(seqs, q_heads, heads)) * 8;
 }
 
 hipError_t launch_attn_decode(const AttnArgs& a, int cache_dtype, int dtype, int head_dim, void* workspace,
@@ -533,17 +567,16 @@ hipError_t launch_attn_decode(const AttnArgs& a, int cache_dtype, int dtype, int
   Work w;
   w.rows = std::min(a.group, kRows);
   w.parts = static_cast<float*>(workspace);
-  w.first = reinterpret_cast<int32_t*>(w.parts + size_t(kWgs) * 2 * partial_floats(w.rows, head_dim));
+  w.first = reinterpret_cast<int32_t*>(w.parts + size_t(kMaxWgs) * 2 * partial_floats(w.rows, head_dim));
   w.count = w.first + units;
   // no more workgroups than tiles that the tables can hold
-  const int64_t tiles = (int64_t(a.kv.max_pages) * a.kv.page.d + kTile - 1) / kTile + 2;
-  const unsigned grid = unsigned(std::min<int64_t>(kWgs, units * tiles));
+  const int64_t tiles = units * ((int64_t(a.kv.max_pages) * a.kv.page.d + kTile - 1) / kTile + 2);
   const bool e4m3 = cache_dtype == W4A4_E4M3;
   if (dtype == W4A4_BF16)
-    return e4m3 ? launch_dim<Bf16, 1>(a, w, head_dim, grid, units, stream)
-                : launch_dim<Bf16, 2>(a, w, head_dim, grid, units, stream);
-  return e4m3 ? launch_dim<F16, 1>(a, w, head_dim, grid, units, stream)
-              : launch_dim<F16, 2>(a, w, head_dim, grid, units, stream);
+    return e4m3 ? launch_dim<Bf16, 1>(a, w, head_dim, tiles, units, stream)
+                : launch_dim<Bf16, 2>(a, w, head_dim, tiles, units, stream);
+  return e4m3 ? launch_dim<F16, 1>(a, w, head_dim, tiles, units, stream)
+              : launch_dim<F16, 2>(a, w, head_dim, tiles, units, stream);
 }
 
 }  // namespace w4a4
