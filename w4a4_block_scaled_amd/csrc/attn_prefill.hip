@@ -81,27 +81,35 @@ __device__ __forceinline__ int key_swz(int r) { return D == 64 ? (r >> 1) & 7 : 
 template <int D>
 __device__ __forceinline__ int value_swz(int r) { return D == 64 ? ((r >> 1) & 3) << 1 : (r & 7) << 1; }
 
+typedef LDS_AS uint16_t Lds16;
+
 // 16 bytes per lane from `src` to LDS, lane l writing `dst` + 16 l (dst is
 // wave-uniform).
-__device__ __forceinline__ void copy_to_lds(const uint8_t* src, uint16_t* dst) {
+__device__ __forceinline__ void copy_to_lds(const uint8_t* src, Lds16* dst) {
   __builtin_amdgcn_global_load_lds(src, (LDS_AS void*)dst, 16, 0, 0);
 }
+__device__ __forceinline__ at_u32x4 read16(const Lds16* p) { return *reinterpret_cast<const LDS_AS at_u32x4*>(p); }
 // Two dwords (4 elements) of column l % 16 of 4 rows x 16 columns, from the
 // 8 bytes that each of 16 lanes points at.
-__device__ __forceinline__ at_u32x2 transpose_from_lds(const uint16_t* src) {
+__device__ __forceinline__ at_u32x2 transpose_from_lds(const Lds16* src) {
   typedef short s4 __attribute__((ext_vector_type(4)));
   return __builtin_bit_cast(at_u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS s4*)src));
 }
 
-template <class T, int D, int E>
+// ONE: the page size is a multiple of 16, so that 16 tokens from a multiple of
+// 16 lie on one page, and one lookup serves the wave that stages them.
+template <class T, int D, int E, bool ONE>
 __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs a, PrefillWork w) {
   constexpr int kChunks = D / 8;                  // 16-byte chunks of a row of 16-bit elements
   constexpr int kLoads = kChunks * E / 8;         // 16-byte loads per thread and tensor: 64 rows x D x E bytes
   constexpr int kSteps = D / 16;                  // score MFMAs per 32 tokens
   constexpr int kBlocks = D / 32;                 // value blocks
-  __shared__ __align__(16) uint16_t lds_k[2][kBN * D];
-  __shared__ __align__(16) uint16_t lds_v[2][kBN * D];
-  __shared__ int lds_bad;
+  // Two tiles of keys, two of values, and three words.  One object: with several,
+  // the compiler no longer sees that copies into one tile leave the others alone,
+  // and waits for them before every read.
+  __shared__ __align__(16) uint16_t smem[4 * kBN * D + 8];
+  volatile LDS_AS int* const flags = (volatile LDS_AS int*)((Lds16*)smem + 4 * kBN * D);
+  constexpr int kBad = 2;                         // [0], [1]: the tile with Inf or NaN among its values
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
@@ -111,7 +119,10 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   const int ti = (blockIdx.x / a.kv.heads) % w.row_tiles, split = blockIdx.x / a.kv.heads / w.row_tiles;
   RowTile rt;
   if (!find_tile(a, w, ti, &rt)) return;
-  if (threadIdx.x == 0) lds_bad = rt.over;
+  if (threadIdx.x == 0) {
+    flags[kBad] = rt.over;
+    flags[0] = flags[1] = -1;
+  }
 
   // this lane's row
   const int all_rows = rt.count * a.group;        // at most tokens * q_heads < 2^31
@@ -155,56 +166,109 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
     *stop = sink ? sink_end : hi;
     return sink ? t * kBN : start + (t - sink_tiles) * kBN;
   };
-  // Staging.  Load j of a thread takes 16 bytes of row load_row(j); 16-bit
-  // caches are copied to LDS directly (lane l of a wave writes 16 bytes at 16 l,
-  // so the lane picks the chunk that belongs there), E4M3 goes through registers.
-  constexpr int kRowLoads = D * E / 16;           // 16-byte pieces of a cache row
-  auto load_index = [&](int j) { return E == 2 ? (wave * kLoads + j) * 64 + lane : j * 256 + int(threadIdx.x); };
-  int64_t off[kLoads];
-  bool bad = false;
-  auto find = [&](int t) {
-    int stop;
-    const int base = tile_at(t, &stop);
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int tk = base + load_index(j) / kRowLoads;
-      int slot;
-      const int p = kv_page(a.kv, table, min(tk, stop - 1), &slot);
-      bad |= p < 0 && tk < stop && (tk >= low || tk < a.sinks);
-      off[j] = (int64_t(max(p, 0)) * a.kv.page_stride + slot * a.kv.token_stride) * E;
-    }
+  // Staging.  A wave takes 16 tokens of a tile: its load j brings 64 pieces of 16
+  // bytes, kRowLoads of a cache row.  16-bit caches are copied to LDS directly
+  // (lane l of a wave writes 16 bytes at 16 l, so the lane picks the chunk that
+  // belongs there), E4M3 goes through registers.
+  constexpr int kRowLoads = D * E / 16, kRows = 64 / kRowLoads;      // rows of one load
+  auto load_row = [&](int j) { return j * kRows + lane / kRowLoads; };           // of the wave's 16
+  auto chunk = [&](int j, bool v) {
+    const int r = 16 * wave + load_row(j), c = lane % kRowLoads;
+    return E == 1 ? c : c ^ (v ? value_swz<D>(r) : key_swz<D>(r));
   };
+  // Where the rows are.  Lane l looks up one page for the tiles ahead: the wave's
+  // 16 tokens of tile t + l if they lie on one page (ONE), or its token l % 16 of
+  // tile t + l / 16.  So one load of the table serves 64 or 4 tiles.  Tokens past
+  // the end take the last one's place, and an entry outside the cache is read as
+  // page 0 and spoils the workgroup's rows if any of them may see a token there.
+  constexpr int kAhead = ONE ? 64 : 4;
+  bool bad = false;
+  int64_t where = 0;          // byte offset of the lane's row
+  auto look_ahead = [&](int t) {
+    const int tl = min(t + (ONE ? lane : lane >> 4), t1 - 1);
+    int stop;
+    const int tk = tile_at(tl, &stop) + 16 * wave + (ONE ? 0 : lane & 15);
+    const int u = min(tk, ONE ? (stop - 1) & ~15 : stop - 1), i = a.kv.page.div(u);
+    const int slot = u - i * int(a.kv.page.d), p = table[i];
+    const bool good = uint32_t(p) < uint32_t(a.kv.pages);
+    bad |= !good && tk < stop && (min(tk + (ONE ? 16 : 1), stop) > low || tk < a.sinks);
+    where = (int64_t(good ? p : 0) * a.kv.page_stride + int64_t(slot) * a.kv.token_stride) * E;
+  };
+  // ONE: what a lane reads is at a fixed offset from the first token's row.
+  uint32_t koff[kLoads], voff[kLoads];
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const uint32_t row = ONE ? uint32_t(load_row(j)) * uint32_t(a.kv.token_stride * E) : 0;
+    koff[j] = row + 16 * chunk(j, false);
+    voff[j] = row + 16 * chunk(j, true);
+  }
   at_u32x4 raw_k[E == 1 ? kLoads : 1], raw_v[E == 1 ? kLoads : 1];
-  auto load = [&](int buf) {
+  auto load = [&](Lds16* kt, Lds16* vt, int t) {
+    const int n = (t - t0) % kAhead;
+    if (n == 0) look_ahead(t);
+    const int lo = int(where), hi32 = int(where >> 32);
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      const int i = load_index(j), r = i / kRowLoads, c = i % kRowLoads;
-      if constexpr (E == 2) {
-        const int at = (wave * kLoads + j) * 64 * 8;      // elements
-        copy_to_lds(kbase + off[j] + 16 * (c ^ key_swz<D>(r)), &lds_k[buf][at]);
-        copy_to_lds(vbase + off[j] + 16 * (c ^ value_swz<D>(r)), &lds_v[buf][at]);
+      int64_t at;
+      if constexpr (ONE) {
+        at = int64_t(uint32_t(__builtin_amdgcn_readlane(lo, n))) | int64_t(__builtin_amdgcn_readlane(hi32, n)) << 32;
       } else {
-        raw_k[j] = *reinterpret_cast<const at_u32x4*>(kbase + off[j] + 16 * c);
-        raw_v[j] = *reinterpret_cast<const at_u32x4*>(vbase + off[j] + 16 * c);
+        const int from = 16 * n + load_row(j);
+        at = int64_t(uint32_t(__shfl(lo, from))) | int64_t(__shfl(hi32, from)) << 32;
+      }
+      const uint8_t* k = kbase + at + koff[j];
+      const uint8_t* v = vbase + at + voff[j];
+      if constexpr (E == 2) {
+        copy_to_lds(k, kt + (wave * kLoads + j) * 64 * 8);
+        copy_to_lds(v, vt + (wave * kLoads + j) * 64 * 8);
+      } else {
+        raw_k[j] = *reinterpret_cast<const at_u32x4*>(k);
+        raw_v[j] = *reinterpret_cast<const at_u32x4*>(v);
       }
     }
   };
-  auto arrive = [&](int buf) {
+  // A tile that every row sees whole needs no masks.
+  auto whole = [&](int t) {
+    int stop;
+    const int base = tile_at(t, &stop);
+    return base + kBN <= stop && base + kBN - 1 <= pos_min &&
+           (!a.window || base > pos_max - a.window || base + kBN <= a.sinks);
+  };
+  // Completes a tile.  In one that some row does not see whole, the wave that
+  // staged the values clears those past the end (whatever the page holds there)
+  // and looks for Inf and NaN among the others.
+  auto arrive = [&](Lds16* kt, Lds16* vt, int buf, int t) {
     if constexpr (E == 2) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt(0)
     } else {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        const int i = load_index(j), r = i / kRowLoads, c = i % kRowLoads;
+        const int r = 16 * wave + load_row(j), c = chunk(j, false);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const uint32_t k0 = raw_k[j][2 * s], k1 = raw_k[j][2 * s + 1], v0 = raw_v[j][2 * s], v1 = raw_v[j][2 * s + 1];
-          *reinterpret_cast<at_u32x4*>(&lds_k[buf][r * D + 8 * ((2 * c + s) ^ key_swz<D>(r))]) =
+          *reinterpret_cast<LDS_AS at_u32x4*>(kt + r * D + 8 * ((2 * c + s) ^ key_swz<D>(r))) =
               (at_u32x4){e4m3_pair<T, false>(k0), e4m3_pair<T, true>(k0), e4m3_pair<T, false>(k1), e4m3_pair<T, true>(k1)};
-          *reinterpret_cast<at_u32x4*>(&lds_v[buf][r * D + 8 * ((2 * c + s) ^ value_swz<D>(r))]) =
+          *reinterpret_cast<LDS_AS at_u32x4*>(vt + r * D + 8 * ((2 * c + s) ^ value_swz<D>(r))) =
               (at_u32x4){e4m3_pair<T, false>(v0), e4m3_pair<T, true>(v0), e4m3_pair<T, false>(v1), e4m3_pair<T, true>(v1)};
         }
       }
+    }
+    if (!whole(t)) {
+      bool odd = false;
+#pragma unroll
+      for (int j = 0; j < kChunks / 4; ++j) {
+        const int i = (wave * (kChunks / 4) + j) * 64 + lane;        // 16-byte piece of the tile
+        int stop;
+        if (tile_at(t, &stop) + i / kChunks < stop) {
+          const at_u32x4 x = read16(vt + 8 * i);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) odd |= T::not_finite(x[k]);
+        } else {
+          *reinterpret_cast<LDS_AS at_u32x4*>(vt + 8 * i) = (at_u32x4){0, 0, 0, 0};
+        }
+      }
+      if (odd) flags[buf] = t;
     }
     __syncthreads();
   };
@@ -219,26 +283,23 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   auto sees = [&](int t, int stop) {
     return t < stop && t <= pos && (!a.window || t > pos - a.window || t < a.sinks);
   };
-  // token of score register e of block b, relative to the tile
-  auto token_of = [&](int b, int e) { return 32 * b + 8 * (e >> 2) + 4 * half + (e & 3); };
   // value operand: block n (32 d's), 16 tokens from tb: two transposing reads of
   // 4 tokens x 16 d's per 16 lanes
-  auto value = [&](int buf, int n, int tb) {
+  auto value = [&](const Lds16* vt, int n, int tb) {
     const int i = lane & 15, d = 32 * n + 16 * ((lane >> 4) & 1) + 4 * (i & 3);
     at_u32x4 x;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int r = tb + 8 * s + 4 * half + (i >> 2);
-      const at_u32x2 y = transpose_from_lds(&lds_v[buf][r * D + 8 * ((d >> 3) ^ value_swz<D>(r)) + (d & 4)]);
+      const at_u32x2 y = transpose_from_lds(vt + r * D + 8 * ((d >> 3) ^ value_swz<D>(r)) + (d & 4));
       x[2 * s] = y.x;
       x[2 * s + 1] = y.y;
     }
     return x;
   };
-  auto compute = [&](int buf, int t) {
-    int stop;
-    const int base = tile_at(t, &stop);
-    at_f32x16 s[2];
+  // Scores of tile t: register e of block b is the token 32 b + 8 (e / 4) + 4
+  // half + e % 4 of the tile.
+  auto scores = [&](const Lds16* kt, int t, at_f32x16 (&s)[2]) {
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -248,27 +309,39 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int r = 32 * b + col;
-        const at_u32x4 k = *reinterpret_cast<const at_u32x4*>(&lds_k[buf][r * D + 8 * ((2 * j + half) ^ key_swz<D>(r))]);
-        s[b] = T::mfma32(k, q[j], s[b]);
+        s[b] = T::mfma32(read16(kt + r * D + 8 * ((2 * j + half) ^ key_swz<D>(r))), q[j], s[b]);
       }
-    // a tile that every row sees whole needs no masks
-    const bool full = base + kBN <= stop && base + kBN - 1 <= pos_min &&
-                      (!a.window || base > pos_max - a.window || base + kBN <= a.sinks);
-    if (!full) {
+    if (!whole(t)) {
+      // A bit for each of the 64 tokens, counted from this half's first one: from
+      // <= token < to, or a sink.
+      int stop;
+      const int base = tile_at(t, &stop) + 4 * half;
+      const int to = min(stop, pos + 1) - base, sinks = min(a.sinks - base, to);
+      const int from = a.window ? pos - a.window + 1 - base : 0;
+      auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t seen = (below(to - 32 * b) & ~below(from - 32 * b)) | below(sinks - 32 * b);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          if (!sees(base + token_of(b, e), stop)) s[b][e] = kNegInf;
+          const uint32_t keep = uint32_t(int32_t(seen << (31 - (8 * (e >> 2) + (e & 3)))) >> 31);
+          const float x = s[b][e];
+          s[b][e] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & keep) | (0xff800000u & ~keep));
         }
+      }
     }
+  };
+  // Scores to weights, with the running maximum and sum.
+  auto weights = [&](at_f32x16 (&s)[2]) {
     float mx = s[0][0];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[b][e]);
     mx = max_xor32(mx) * cs;
-    if (__any(mx > m)) {
+    // The sums are rebased only where a maximum has grown by more than 2^8: until
+    // then weights go up to 2^8, which costs neither type any accuracy.
+    if (__any(mx > m + 8.0f)) {
       const float mn = fmaxf(m, mx), f = rebase(m, mn);
 #pragma unroll
       for (int n = 0; n < kBlocks; ++n) o[n] *= f;
@@ -283,69 +356,72 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
         s[b][e] = exp2_fast(__builtin_fmaf(s[b][e], cs, -mm));
         l += s[b][e];
       }
-    if (!full) {
-      // Inf or NaN among the values of a tile that some row does not see whole:
-      // 0 x Inf would reach the row's sum.  The rows that see such a value get it
-      // added, then it is cleared in the tile.  (The same test of the same tile
-      // in every wave, so all of them meet at the barriers.)
-      bool odd = false;
-#pragma unroll 2
-      for (int i = lane; i < kBN * D / 8; i += 64) {
-        const at_u32x4 x = *reinterpret_cast<const at_u32x4*>(&lds_v[buf][8 * i]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) odd |= T::not_finite(x[k]);
-      }
-      if (__any(odd)) {
+  };
+  // Inf or NaN in a tile that some row does not see whole: 0 x Inf would reach
+  // the row's sum.  The rows that see such a value get it added, then it is
+  // cleared in the tile.  (All waves get here together: the flag is the tile's.)
+  auto settle_odd = [&](Lds16* vt, int t) {
+    int stop;
+    const int base = tile_at(t, &stop);
 #pragma unroll 1
-        for (int r = 0; r < kBN; ++r) {
-          const bool see = sees(base + r, stop);
+    for (int r = 0; r < kBN; ++r) {
+      const bool see = sees(base + r, stop);
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            const at_u32x2 x = *reinterpret_cast<const at_u32x2*>(&lds_v[buf][r * D + 8 * (c ^ value_swz<D>(r)) + 4 * half]);
+      for (int c = 0; c < kChunks; ++c) {
+        const at_u32x2 x = *reinterpret_cast<const LDS_AS at_u32x2*>(vt + r * D + 8 * (c ^ value_swz<D>(r)) + 4 * half);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float v = k & 1 ? T::high(x[k >> 1]) : T::low(x[k >> 1]);
-              if (see && !(fabsf(v) < -kNegInf)) o[c >> 2][4 * (c & 3) + k] += v;
-            }
-          }
+        for (int k = 0; k < 4; ++k) {
+          const float v = k & 1 ? T::high(x[k >> 1]) : T::low(x[k >> 1]);
+          if (see && !(fabsf(v) < -kNegInf)) o[c >> 2][4 * (c & 3) + k] += v;
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < kBN * D / 2; i += 256) {
-          uint32_t* u = reinterpret_cast<uint32_t*>(&lds_v[buf][0]) + i;
-          if (T::not_finite(*u)) *u = T::finite(*u);
-        }
-        __syncthreads();
       }
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBN * D / 2; i += 256) {
+      LDS_AS uint32_t* u = reinterpret_cast<LDS_AS uint32_t*>(vt) + i;
+      if (T::not_finite(*u)) *u = T::finite(*u);
+    }
+    __syncthreads();
+  };
+  auto values = [&](const Lds16* vt, const at_f32x16 (&s)[2]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       at_u32x4 p;        // weights of the tokens 16 i .. 16 i + 15
 #pragma unroll
       for (int k = 0; k < 4; ++k) p[k] = T::pack(s[i >> 1][8 * (i & 1) + 2 * k], s[i >> 1][8 * (i & 1) + 2 * k + 1]);
 #pragma unroll
-      for (int n = 0; n < kBlocks; ++n) o[n] = T::mfma32(value(buf, n, 16 * i), p, o[n]);
+      for (int n = 0; n < kBlocks; ++n) o[n] = T::mfma32(value(vt, n, 16 * i), p, o[n]);
     }
   };
 
+  // One step: start the copies of tile t + 1 into `nk`, `nv`, and take tile t from
+  // `ck`, `cv`.  That they are different memory is what lets the reads go on while
+  // the copies are in flight.
+  auto tile_step = [&](Lds16* __restrict__ ck, Lds16* __restrict__ cv, Lds16* __restrict__ nk, Lds16* __restrict__ nv,
+                       int t, int buf) {
+    if (t + 1 < t1) load(nk, nv, t + 1);
+    at_f32x16 s[2];
+    scores(ck, t, s);
+    weights(s);
+    if (flags[buf] == t) settle_odd(cv, t);
+    values(cv, s);
+  };
+
+  Lds16* const lk = (Lds16*)smem;
+  Lds16* const lv = lk + 2 * kBN * D;
   if (t0 < t1) {
-    find(t0);
-    load(0);
-    if (t0 + 1 < t1) find(t0 + 1);
-    arrive(0);
+    load(lk, lv, t0);
+    arrive(lk, lv, 0, t0);
     for (int t = t0; t < t1; ++t) {
-      const int buf = (t - t0) & 1;
-      if (t + 1 < t1) {
-        load(buf ^ 1);
-        if (t + 2 < t1) find(t + 2);
-      }
-      compute(buf, t);
-      if (t + 1 < t1) arrive(buf ^ 1);
+      const int buf = (t - t0) & 1, cur = buf * kBN * D, nxt = kBN * D - cur;
+      tile_step(lk + cur, lv + cur, lk + nxt, lv + nxt, t, buf);
+      if (t + 1 < t1) arrive(lk + nxt, lv + nxt, buf ^ 1, t + 1);
     }
   }
-  if (bad) lds_bad = 1;
+  if (bad) flags[kBad] = 1;
   __syncthreads();
   l = sum_xor32(l);
-  if (lds_bad) l = __builtin_nanf("");
+  if (flags[kBad]) l = __builtin_nanf("");
 
   if (w.splits > 1 && used > 1) {
     float* part = w.parts + (int64_t(ti * a.kv.heads + head) * w.splits + split) * kBM * (D + 2);
@@ -432,7 +508,11 @@ int key_splits(int64_t tiles, int heads) {
 template <class T, int D, int E>
 hipError_t launch(const AttnArgs& a, const PrefillWork& w, hipStream_t stream) {
   const unsigned tiles = unsigned(w.row_tiles * a.kv.heads);
-  prefill_kernel<T, D, E><<<tiles * unsigned(w.splits), 256, 0, stream>>>(a, w);
+  // (a lane's offset from the first of 16 tokens is kept in 32 bits)
+  if (a.kv.page.d % 16 == 0 && a.kv.token_stride < (1 << 26))
+    prefill_kernel<T, D, E, true><<<tiles * unsigned(w.splits), 256, 0, stream>>>(a, w);
+  else
+    prefill_kernel<T, D, E, false><<<tiles * unsigned(w.splits), 256, 0, stream>>>(a, w);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || w.splits == 1) return e;
   prefill_join_kernel<T, D, E><<<dim3(tiles, kBM / 8), 256, 0, stream>>>(a, w);
