@@ -16,6 +16,7 @@
 //
 // The matrix cores bound it: 4 D operations per visible pair.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_common.h"
 
@@ -26,6 +27,7 @@ namespace {
 
 constexpr int kBM = 128;      // rows per workgroup
 constexpr int kBN = 64;       // tokens per step
+constexpr int kMaxSplits = 64;  // of the keys of a row tile: two per lane of the join
 
 struct PrefillWork {
   const int32_t* cu;
@@ -36,7 +38,9 @@ struct PrefillWork {
 };
 
 // The sequence and tile of the sequence that row tile `ti` is; false past the end.
-// Tiles of a sequence are handed out from its end, where rows see most keys.
+// Tiles of a sequence are handed out from its end, where rows see most keys, and
+// up to 64 sequences by length, the longest first: the last workgroups to start
+// are short ones.
 struct RowTile {
   int seq, tile, first_token, count, len;
   bool over;
@@ -45,9 +49,19 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, const PrefillWork& 
   const int lane = threadIdx.x & 63;
   int before = 0;
   for (int base = 0; base < a.kv.seqs; base += 64) {
-    const int s = base + lane;
-    int n = 0;
+    int s = base + lane, n = 0;
     if (s < a.kv.seqs) n = min(max(w.cu[s + 1] - w.cu[s], 0), w.tokens);
+    if (a.kv.seqs <= 64 && a.kv.seqs > 1) {
+      const int len = s < a.kv.seqs ? a.kv.lens[s] : INT32_MIN;
+      int rank = 0;
+      for (int i = 0; i < a.kv.seqs; ++i) {
+        const int other = __builtin_amdgcn_readlane(len, i);
+        rank += other > len || (other == len && i < lane);
+      }
+      if (s >= a.kv.seqs) rank = lane;               // behind all sequences, each at its own place
+      s = __builtin_amdgcn_ds_permute(rank << 2, s);
+      n = __builtin_amdgcn_ds_permute(rank << 2, n);
+    }
     const int t = int((int64_t(n) * a.group + kBM - 1) / kBM);
     int in = t;
 #pragma unroll
@@ -58,12 +72,12 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, const PrefillWork& 
     const uint64_t past = __ballot(before + in > ti);
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
-      out->seq = base + l;
+      out->seq = __builtin_amdgcn_readlane(s, l);
       out->count = __builtin_amdgcn_readlane(n, l);
       out->tile = before + __builtin_amdgcn_readlane(in, l) - 1 - ti;
-      out->first_token = w.cu[base + l];
+      out->first_token = w.cu[out->seq];
       const int cap = int(min(int64_t(a.kv.max_pages) * a.kv.page.d, int64_t(1) << 30));
-      const int len = a.kv.lens[base + l];
+      const int len = a.kv.lens[out->seq];
       out->over = len > cap;
       out->len = min(len, cap);
       return true;
@@ -75,18 +89,29 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, const PrefillWork& 
 
 // 16-byte chunk swizzles of the LDS tiles (row r, chunk c at slot c ^ swz(r)).
 // Keys: 16 consecutive rows of one chunk fall on 16 different 16-byte bank
-// groups; values: so do 4 consecutive rows of two chunks.
+// groups; values: so do 4 consecutive rows of four chunks (32 lanes' pieces).
 template <int D>
 __device__ __forceinline__ int key_swz(int r) { return D == 64 ? (r >> 1) & 7 : r & 15; }
 template <int D>
-__device__ __forceinline__ int value_swz(int r) { return D == 64 ? ((r >> 1) & 3) << 1 : (r & 7) << 1; }
+__device__ __forceinline__ int value_swz(int r) { return D == 64 ? (r & 2) << 1 : (r & 3) << 2; }
 
 typedef LDS_AS uint16_t Lds16;
+
+// s_waitcnt vmcnt(n) alone: vmcnt in bits 3:0 and 15:14, expcnt 6:4 and lgkmcnt
+// 11:8 at their maxima.
+constexpr int wait_vmcnt(int n) { return (n & 15) | (n >> 4) << 14 | 0x0f70; }
 
 // 16 bytes per lane from `src` to LDS, lane l writing `dst` + 16 l (dst is
 // wave-uniform).
 __device__ __forceinline__ void copy_to_lds(const uint8_t* src, Lds16* dst) {
   __builtin_amdgcn_global_load_lds(src, (LDS_AS void*)dst, 16, 0, 0);
+}
+// The same from `base` (uniform) + `off`.  A buffer load: the compiler counts a
+// global load to LDS as an access of both kinds that may come back in any order,
+// and then waits for every LDS read before the first one's use.
+__device__ __forceinline__ void copy_to_lds(const uint8_t* base, uint32_t off, Lds16* dst) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, -1, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LDS_AS void*)dst, 16, int(off), 0, 0, 0);
 }
 __device__ __forceinline__ at_u32x4 read16(const Lds16* p) { return *reinterpret_cast<const LDS_AS at_u32x4*>(p); }
 // Two dwords (4 elements) of column l % 16 of 4 rows x 16 columns, from the
@@ -98,7 +123,10 @@ __device__ __forceinline__ at_u32x2 transpose_from_lds(const Lds16* src) {
 
 // ONE: the page size is a multiple of 16, so that 16 tokens from a multiple of
 // 16 lie on one page, and one lookup serves the wave that stages them.
-template <class T, int D, int E, bool ONE>
+// SPLIT: the keys are split over workgroups.  The matrix cores then have time to
+// spare, and the weights enter as two 16-bit parts, as in decoding (0 x Inf has
+// to be kept out of every tile, since the second part may be 0).
+template <class T, int D, int E, bool ONE, bool SPLIT>
 __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs a, PrefillWork w) {
   constexpr int kChunks = D / 8;                  // 16-byte chunks of a row of 16-bit elements
   constexpr int kLoads = kChunks * E / 8;         // 16-byte loads per thread and tensor: 64 rows x D x E bytes
@@ -143,9 +171,9 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   const int sink_end = min(a.sinks, start);
   const int sink_tiles = (sink_end + kBN - 1) / kBN;
   const int tiles = sink_tiles + (hi - start + kBN - 1) / kBN;
-  const int used = min(w.splits, max(tiles / 4, 1));      // a split has at least 4 tiles
+  const int used = SPLIT ? min(w.splits, max(tiles / 4, 1)) : 1;      // a split has at least 4 tiles
   if (split >= used) return;
-  if (w.splits > 1 && split == 0 && threadIdx.x == 0) w.used[ti * a.kv.heads + head] = used;
+  if (SPLIT && split == 0 && threadIdx.x == 0) w.used[ti * a.kv.heads + head] = used;
   const int t0 = int(int64_t(tiles) * split / used), t1 = int(int64_t(tiles) * (split + 1) / used);
 
   const float cs = a.scale_log2 * (E == 1 && a.kv.k_scale ? a.kv.k_scale[head] : 1.0f);
@@ -203,58 +231,61 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
     voff[j] = row + 16 * chunk(j, true);
   }
   at_u32x4 raw_k[E == 1 ? kLoads : 1], raw_v[E == 1 ? kLoads : 1];
-  auto load = [&](Lds16* kt, Lds16* vt, int t) {
+  struct Place {
+    int64_t at[ONE ? 1 : kLoads];
+  };
+  auto place_of = [&](int t) {
     const int n = (t - t0) % kAhead;
     if (n == 0) look_ahead(t);
     const int lo = int(where), hi32 = int(where >> 32);
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      int64_t at;
-      if constexpr (ONE) {
-        at = int64_t(uint32_t(__builtin_amdgcn_readlane(lo, n))) | int64_t(__builtin_amdgcn_readlane(hi32, n)) << 32;
-      } else {
-        const int from = 16 * n + load_row(j);
-        at = int64_t(uint32_t(__shfl(lo, from))) | int64_t(__shfl(hi32, from)) << 32;
-      }
-      const uint8_t* k = kbase + at + koff[j];
-      const uint8_t* v = vbase + at + voff[j];
-      if constexpr (E == 2) {
-        copy_to_lds(k, kt + (wave * kLoads + j) * 64 * 8);
-        copy_to_lds(v, vt + (wave * kLoads + j) * 64 * 8);
-      } else {
-        raw_k[j] = *reinterpret_cast<const at_u32x4*>(k);
-        raw_v[j] = *reinterpret_cast<const at_u32x4*>(v);
-      }
-    }
-  };
-  // A tile that every row sees whole needs no masks.
-  auto whole = [&](int t) {
-    int stop;
-    const int base = tile_at(t, &stop);
-    return base + kBN <= stop && base + kBN - 1 <= pos_min &&
-           (!a.window || base > pos_max - a.window || base + kBN <= a.sinks);
-  };
-  // Completes a tile.  In one that some row does not see whole, the wave that
-  // staged the values clears those past the end (whatever the page holds there)
-  // and looks for Inf and NaN among the others.
-  auto arrive = [&](Lds16* kt, Lds16* vt, int buf, int t) {
-    if constexpr (E == 2) {
-      __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt(0)
+    Place x;
+    if constexpr (ONE) {
+      x.at[0] = int64_t(uint32_t(__builtin_amdgcn_readlane(lo, n))) | int64_t(__builtin_amdgcn_readlane(hi32, n)) << 32;
     } else {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        const int r = 16 * wave + load_row(j), c = chunk(j, false);
+        const int from = 16 * n + load_row(j);
+        x.at[j] = int64_t(uint32_t(__shfl(lo, from))) | int64_t(__shfl(hi32, from)) << 32;
+      }
+    }
+    return x;
+  };
+  auto load = [&](Lds16* tile, const uint8_t* base, const Place& x, const uint32_t* offset, at_u32x4* raw) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const uint8_t* p = base + x.at[ONE ? 0 : j];
+      Lds16* const to = tile + (wave * kLoads + j) * 64 * 8;
+      if constexpr (E == 1) raw[j] = *reinterpret_cast<const at_u32x4*>(p + offset[j]);
+      else if constexpr (ONE) copy_to_lds(p, offset[j], to);
+      else copy_to_lds(p + offset[j], to);
+    }
+  };
+  // E4M3: the pieces that have come go to LDS as 16-bit elements.
+  auto put = [&](Lds16* tile, const at_u32x4* raw, bool v) {
+    if constexpr (E == 1) {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int r = 16 * wave + load_row(j), c = chunk(j, v), z = v ? value_swz<D>(r) : key_swz<D>(r);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const uint32_t k0 = raw_k[j][2 * s], k1 = raw_k[j][2 * s + 1], v0 = raw_v[j][2 * s], v1 = raw_v[j][2 * s + 1];
-          *reinterpret_cast<LDS_AS at_u32x4*>(kt + r * D + 8 * ((2 * c + s) ^ key_swz<D>(r))) =
-              (at_u32x4){e4m3_pair<T, false>(k0), e4m3_pair<T, true>(k0), e4m3_pair<T, false>(k1), e4m3_pair<T, true>(k1)};
-          *reinterpret_cast<LDS_AS at_u32x4*>(vt + r * D + 8 * ((2 * c + s) ^ value_swz<D>(r))) =
-              (at_u32x4){e4m3_pair<T, false>(v0), e4m3_pair<T, true>(v0), e4m3_pair<T, false>(v1), e4m3_pair<T, true>(v1)};
+          const uint32_t x = raw[j][2 * s], y = raw[j][2 * s + 1];
+          *reinterpret_cast<LDS_AS at_u32x4*>(tile + r * D + 8 * ((2 * c + s) ^ z)) =
+              (at_u32x4){e4m3_pair<T, false>(x), e4m3_pair<T, true>(x), e4m3_pair<T, false>(y), e4m3_pair<T, true>(y)};
         }
       }
     }
-    if (!whole(t)) {
+  };
+  // Tiles that every row sees whole need no masks: full sink tiles, and those
+  // from where the last row's window begins to the first row's position.
+  const int whole_sinks = sink_end / kBN;
+  const int whole_from = sink_tiles + (a.window ? (max(pos_max - a.window + 1 - start, 0) + kBN - 1) / kBN : 0);
+  const int whole_to = sink_tiles + max(min(pos_min + 1, hi) - start, 0) / kBN;
+  auto whole = [&](int t) { return t < whole_sinks || (t >= whole_from && t < whole_to); };
+  // Looks over the values of a tile that has come.  In one that some row does not
+  // see whole, the wave that staged them clears those past the end (whatever the
+  // page holds there) and looks for Inf and NaN among the others.
+  auto look_over = [&](Lds16* vt, int buf, int t) {
+    if (SPLIT || !whole(t)) {
       bool odd = false;
 #pragma unroll
       for (int j = 0; j < kChunks / 4; ++j) {
@@ -270,7 +301,9 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
       }
       if (odd) flags[buf] = t;
     }
-    __syncthreads();
+  };
+  auto arrived = [] {
+    if constexpr (E == 2) __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
   };
 
   at_f32x16 o[kBlocks];
@@ -283,64 +316,51 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   auto sees = [&](int t, int stop) {
     return t < stop && t <= pos && (!a.window || t > pos - a.window || t < a.sinks);
   };
-  // value operand: block n (32 d's), 16 tokens from tb: two transposing reads of
-  // 4 tokens x 16 d's per 16 lanes
+  // Operands.  A lane's element offsets in a tile, apart from constants: of the key
+  // operand of step j (32 tokens: row lane % 32, chunk 2 j + lane / 32), and of the
+  // value operand of block n (32 d's, by two transposing reads of 4 tokens x 16
+  // d's per 16 lanes; a multiple of 8 tokens does not change the swizzle).
+  int k_at[kSteps], v_at[kBlocks];
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) k_at[j] = col * D + 8 * ((2 * j + half) ^ key_swz<D>(col));
+#pragma unroll
+  for (int n = 0; n < kBlocks; ++n) {
+    const int i = lane & 15, d = 32 * n + 16 * ((lane >> 4) & 1) + 4 * (i & 3), r = 4 * half + (i >> 2);
+    v_at[n] = r * D + 8 * ((d >> 3) ^ value_swz<D>(r)) + (d & 4);
+  }
+  // Key operand of MFMA i of a tile's scores (block i % 2 of 32 tokens, step i / 2).
+  // Register e of the block's scores is the token 8 (e / 4) + 4 half + e % 4.
+  auto key = [&](const Lds16* kt, int i) { return read16(kt + k_at[i >> 1] + 32 * D * (i & 1)); };
+  // Value operand of block n, 16 tokens from tb.
   auto value = [&](const Lds16* vt, int n, int tb) {
-    const int i = lane & 15, d = 32 * n + 16 * ((lane >> 4) & 1) + 4 * (i & 3);
-    at_u32x4 x;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int r = tb + 8 * s + 4 * half + (i >> 2);
-      const at_u32x2 y = transpose_from_lds(vt + r * D + 8 * ((d >> 3) ^ value_swz<D>(r)) + (d & 4));
-      x[2 * s] = y.x;
-      x[2 * s + 1] = y.y;
-    }
-    return x;
+    const at_u32x2 x = transpose_from_lds(vt + v_at[n] + tb * D), y = transpose_from_lds(vt + v_at[n] + (tb + 8) * D);
+    return (at_u32x4){x.x, x.y, y.x, y.y};
   };
-  // Scores of tile t: register e of block b is the token 32 b + 8 (e / 4) + 4
-  // half + e % 4 of the tile.
-  auto scores = [&](const Lds16* kt, int t, at_f32x16 (&s)[2]) {
+  // Masks the scores of tile t.
+  auto mask = [&](int t, at_f32x16 (&s)[2]) {
+    // A bit for each of the 64 tokens, counted from this half's first one: from <=
+    // token < to, or a sink.
+    int stop;
+    const int base = tile_at(t, &stop) + 4 * half;
+    const int to = min(stop, pos + 1) - base, sinks = min(a.sinks - base, to);
+    const int from = a.window ? pos - a.window + 1 - base : 0;
+    auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t seen = (below(to - 32 * b) & ~below(from - 32 * b)) | below(sinks - 32 * b);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s[b][e] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int r = 32 * b + col;
-        s[b] = T::mfma32(read16(kt + r * D + 8 * ((2 * j + half) ^ key_swz<D>(r))), q[j], s[b]);
-      }
-    if (!whole(t)) {
-      // A bit for each of the 64 tokens, counted from this half's first one: from
-      // <= token < to, or a sink.
-      int stop;
-      const int base = tile_at(t, &stop) + 4 * half;
-      const int to = min(stop, pos + 1) - base, sinks = min(a.sinks - base, to);
-      const int from = a.window ? pos - a.window + 1 - base : 0;
-      auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint32_t seen = (below(to - 32 * b) & ~below(from - 32 * b)) | below(sinks - 32 * b);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint32_t keep = uint32_t(int32_t(seen << (31 - (8 * (e >> 2) + (e & 3)))) >> 31);
-          const float x = s[b][e];
-          s[b][e] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & keep) | (0xff800000u & ~keep));
-        }
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t keep = uint32_t(int32_t(seen << (31 - (8 * (e >> 2) + (e & 3)))) >> 31);
+        const float x = s[b][e];
+        s[b][e] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & keep) | (0xff800000u & ~keep));
       }
     }
   };
-  // Scores to weights, with the running maximum and sum.
-  auto weights = [&](at_f32x16 (&s)[2]) {
-    float mx = s[0][0];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[b][e]);
+  // Takes a tile's largest score into the running maximum.  The sums are rebased
+  // only where a maximum has grown by more than 2^8: until then weights go up to
+  // 2^8, which costs neither type any accuracy.
+  auto rebase_sums = [&](float mx) {
     mx = max_xor32(mx) * cs;
-    // The sums are rebased only where a maximum has grown by more than 2^8: until
-    // then weights go up to 2^8, which costs neither type any accuracy.
     if (__any(mx > m + 8.0f)) {
       const float mn = fmaxf(m, mx), f = rebase(m, mn);
 #pragma unroll
@@ -348,14 +368,6 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
       l *= f;
       m = mn;
     }
-    const float mm = m == kNegInf ? 0.0f : m;
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        s[b][e] = exp2_fast(__builtin_fmaf(s[b][e], cs, -mm));
-        l += s[b][e];
-      }
   };
   // Inf or NaN in a tile that some row does not see whole: 0 x Inf would reach
   // the row's sum.  The rows that see such a value get it added, then it is
@@ -383,47 +395,208 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
     }
     __syncthreads();
   };
-  auto values = [&](const Lds16* vt, const at_f32x16 (&s)[2]) {
+  // The scores are a tile ahead: the matrix cores take those of tile t + 1 (NEXT),
+  // then the values of tile t.  A wave's instructions issue in order, so MFMAs in
+  // a row would leave the vector units idle, and the other way round: behind every
+  // MFMA comes a share of the vector work.  That is the weights of t, the first
+  // kFirst of 16 pairs behind the scores of t + 1, the others behind the values of
+  // the first 32 tokens, and behind those of the last 32 the maximum of t + 1.
+  // Operands are read kDepth MFMAs ahead.
+  auto compute = [&](const Lds16* k_next, const Lds16* v_cur, int t, const at_f32x16 (&s)[2], at_f32x16 (&ahead)[2], auto next) {
+    constexpr bool NEXT = decltype(next)::value;
+    constexpr int kScores = 2 * kSteps, kValues = 4 * kBlocks, kDepth = D == 256 ? 2 : 4, kFirst = 10;
+    const float mm = m == kNegInf ? 0.0f : m;
+    at_u32x4 p[4], rest[SPLIT ? 4 : 1];      // weights of 16 tokens as operands (SPLIT: in two parts)
+    auto pair = [&](int u) {
+      const int i = u >> 2, k = u & 3, e = 8 * (i & 1) + 2 * k;
+      const float x = exp2_fast(__builtin_fmaf(s[i >> 1][e], cs, -mm)), y = exp2_fast(__builtin_fmaf(s[i >> 1][e + 1], cs, -mm));
+      l += x;
+      l += y;
+      uint32_t z = T::pack(x, y);
+      asm volatile("" : "+v"(z), "+v"(l));      // here, and not where they are used
+      p[i][k] = z;
+      if constexpr (SPLIT) rest[i][k] = T::pack(x - T::low(z), y - T::high(z));
+    };
+    auto v_operand = [&](int v) { return value(v_cur, v % kBlocks, 16 * (v / kBlocks)); };
+    at_u32x4 f[kDepth];
+    if constexpr (NEXT) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      at_u32x4 p;        // weights of the tokens 16 i .. 16 i + 15
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) p[k] = T::pack(s[i >> 1][8 * (i & 1) + 2 * k], s[i >> 1][8 * (i & 1) + 2 * k + 1]);
+        for (int e = 0; e < 16; ++e) ahead[b][e] = 0.0f;
 #pragma unroll
-      for (int n = 0; n < kBlocks; ++n) o[n] = T::mfma32(value(vt, n, 16 * i), p, o[n]);
+      for (int i = 0; i < kDepth; ++i) f[i] = key(k_next, i);
+#pragma unroll
+      for (int i = 0; i < kScores; ++i) {
+        ahead[i & 1] = T::mfma32(f[i % kDepth], q[i >> 1], ahead[i & 1]);
+        f[i % kDepth] = i + kDepth < kScores ? key(k_next, i + kDepth) : v_operand(i + kDepth - kScores);
+#pragma unroll
+        for (int u = i * kFirst / kScores; u < (i + 1) * kFirst / kScores; ++u) pair(u);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (!whole(t + 1)) mask(t + 1, ahead);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) f[i] = v_operand(i);
+#pragma unroll
+      for (int u = 0; u < kFirst; ++u) pair(u);
+    }
+    float mx = kNegInf;
+#pragma unroll
+    for (int v = 0; v < kValues; ++v) {
+      const int n = v % kBlocks, i = v / kBlocks;
+      o[n] = T::mfma32(f[v % kDepth], p[i], o[n]);
+      if constexpr (SPLIT) o[n] = T::mfma32(f[v % kDepth], rest[i], o[n]);
+      if (v + kDepth < kValues) f[v % kDepth] = v_operand(v + kDepth);
+      if (v < kValues / 2) {
+#pragma unroll
+        for (int u = kFirst + v * (16 - kFirst) / (kValues / 2); u < kFirst + (v + 1) * (16 - kFirst) / (kValues / 2); ++u) pair(u);
+      } else if constexpr (NEXT) {
+        constexpr int kShare = 64 / kValues;
+#pragma unroll
+        for (int e = (v - kValues / 2) * kShare; e < (v - kValues / 2 + 1) * kShare; ++e) mx = fmaxf(mx, ahead[e >> 4][e & 15]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (NEXT) {
+      rebase_sums(mx);
     }
   };
-
-  // One step: start the copies of tile t + 1 into `nk`, `nv`, and take tile t from
-  // `ck`, `cv`.  That they are different memory is what lets the reads go on while
-  // the copies are in flight.
-  auto tile_step = [&](Lds16* __restrict__ ck, Lds16* __restrict__ cv, Lds16* __restrict__ nk, Lds16* __restrict__ nv,
-                       int t, int buf) {
-    if (t + 1 < t1) load(nk, nv, t + 1);
-    at_f32x16 s[2];
-    scores(ck, t, s);
-    weights(s);
-    if (flags[buf] == t) settle_odd(cv, t);
-    values(cv, s);
+  // The scores of a tile by themselves, masked and taken into the maximum.
+  auto scores = [&](const Lds16* kt, int t, at_f32x16 (&s)[2]) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[b][e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2 * kSteps; ++i) s[i & 1] = T::mfma32(key(kt, i), q[i >> 1], s[i & 1]);
+    if (!whole(t)) mask(t, s);
+    float mx = kNegInf;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[b][e]);
+    rebase_sums(mx);
+  };
+  // SPLIT: a wave whose rows are all past the sequence's end only stages.
+  const bool busy = rt.tile * kBM + wave * 32 < all_rows;
+  // One step: copies start of the keys of t + 2 into the buffer that t's were in,
+  // and of the values of t + 1.  That the four tiles are different memory is what
+  // lets the reads go on meanwhile.
+  Place here;                   // of tile t + 1
+  auto settle = [&](Lds16* v_cur, int t, int buf) {
+    if ((SPLIT || !whole(t)) && flags[buf] == t) settle_odd(v_cur, t);
+  };
+  auto tile_step = [&](Lds16* __restrict__ k_in, Lds16* __restrict__ k_next, Lds16* __restrict__ v_cur,
+                       Lds16* __restrict__ v_in, int t, int buf, const at_f32x16 (&s)[2], at_f32x16 (&ahead)[2]) {
+    load(v_in, vbase, here, voff, raw_v);
+    if (t + 2 < t1) {
+      here = place_of(t + 2);
+      load(k_in, kbase, here, koff, raw_k);
+    }
+    settle(v_cur, t, buf);
+    compute(k_next, v_cur, t, s, ahead, std::true_type());
+    arrived();
+    put(v_in, raw_v, true);
+    if (t + 2 < t1) put(k_in, raw_k, false);
+    look_over(v_in, buf ^ 1, t + 1);
+    __syncthreads();
   };
 
   Lds16* const lk = (Lds16*)smem;
   Lds16* const lv = lk + 2 * kBN * D;
-  if (t0 < t1) {
-    load(lk, lv, t0);
-    arrive(lk, lv, 0, t0);
+  if constexpr (SPLIT) {
+    // A share of the keys: what counts is how soon they come, so a tile's copies
+    // start a whole step ahead, keys and values, and the step is plain.
+    auto split_step = [&](Lds16* __restrict__ k_cur, Lds16* __restrict__ v_cur, Lds16* __restrict__ k_in,
+                          Lds16* __restrict__ v_in, int t, int buf) {
+      const bool more = t + 1 < t1;
+      if (more) {
+        here = place_of(t + 1);
+        load(k_in, kbase, here, koff, raw_k);
+        load(v_in, vbase, here, voff, raw_v);
+      }
+      settle(v_cur, t, buf);
+      if (busy) {
+        at_f32x16 s[2], none[2];
+        scores(k_cur, t, s);
+        compute(k_cur, v_cur, t, s, none, std::false_type());
+      }
+      if (more) {
+        arrived();
+        put(k_in, raw_k, false);
+        put(v_in, raw_v, true);
+        look_over(v_in, buf ^ 1, t + 1);
+      }
+      __syncthreads();
+    };
+    if (t0 < t1) {
+      here = place_of(t0);
+      load(lk, kbase, here, koff, raw_k);
+      load(lv, vbase, here, voff, raw_v);
+      arrived();
+      put(lk, raw_k, false);
+      put(lv, raw_v, true);
+      look_over(lv, 0, t0);
+      __syncthreads();
+    }
     for (int t = t0; t < t1; ++t) {
       const int buf = (t - t0) & 1, cur = buf * kBN * D, nxt = kBN * D - cur;
-      tile_step(lk + cur, lv + cur, lk + nxt, lv + nxt, t, buf);
-      if (t + 1 < t1) arrive(lk + nxt, lv + nxt, buf ^ 1, t + 1);
+      split_step(lk + cur, lv + cur, lk + nxt, lv + nxt, t, buf);
     }
+  } else if (t0 < t1) {
+    // the keys of t0, its values, and the keys of t0 + 1; the scores of t0 wait
+    // for the first only
+    here = place_of(t0);
+    load(lk, kbase, here, koff, raw_k);
+    put(lk, raw_k, false);
+    load(lv, vbase, here, voff, raw_v);
+    put(lv, raw_v, true);
+    if (t0 + 1 < t1) {
+      here = place_of(t0 + 1);
+      load(lk + kBN * D, kbase, here, koff, raw_k);
+      put(lk + kBN * D, raw_k, false);
+      if constexpr (E == 2) __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * kLoads));
+    } else if constexpr (E == 2) {
+      __builtin_amdgcn_s_waitcnt(wait_vmcnt(kLoads));
+    }
+    __syncthreads();
+    at_f32x16 s[2], s2[2];
+    scores(lk, t0, s);
+    arrived();
+    look_over(lv, 0, t0);
+    __syncthreads();            // also: the keys of t0 have been read by all, theirs is the buffer of t0 + 2
+    Lds16 *const k0 = lk, *const k1 = lk + kBN * D, *const v0 = lv, *const v1 = lv + kBN * D;
+    int t = t0;
+    if constexpr (D == 256) {           // two steps' code would not fit the registers
+      for (; t + 1 < t1; ++t) {
+        const int cur = ((t - t0) & 1) * kBN * D, nxt = kBN * D - cur;
+        tile_step(lk + cur, lk + nxt, lv + cur, lv + nxt, t, (t - t0) & 1, s, s2);
+        s[0] = s2[0];
+        s[1] = s2[1];
+      }
+    } else {
+      for (; t + 2 < t1; t += 2) {
+        tile_step(k0, k1, v0, v1, t, 0, s, s2);
+        tile_step(k1, k0, v1, v0, t + 1, 1, s2, s);
+      }
+      if (t + 1 < t1) {
+        tile_step(k0, k1, v0, v1, t, 0, s, s2);
+        s[0] = s2[0];
+        s[1] = s2[1];
+        ++t;
+      }
+    }
+    Lds16* const last = (t - t0) & 1 ? v1 : v0;
+    settle(last, t, (t - t0) & 1);
+    compute(lk, last, t, s, s2, std::false_type());
   }
   if (bad) flags[kBad] = 1;
   __syncthreads();
   l = sum_xor32(l);
   if (flags[kBad]) l = __builtin_nanf("");
 
-  if (w.splits > 1 && used > 1) {
+  if (SPLIT && used > 1) {
     float* part = w.parts + (int64_t(ti * a.kv.heads + head) * w.splits + split) * kBM * (D + 2);
     const int r = wave * 32 + col;
 #pragma unroll
@@ -469,21 +642,34 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(AttnArgs a, PrefillWo
   const int tok = w.group.div(row), qi = rt.first_token + tok;
   if (qi < 0 || qi >= w.tokens) return;
   const float* base = w.parts + int64_t(blockIdx.x) * w.splits * kBM * (D + 2);
-  float M = kNegInf;
-  for (int i = 0; i < used; ++i) M = fmaxf(M, base[int64_t(i) * kBM * (D + 2) + kBM * D + r]);
-  float L = 0.0f, O[D / 32];
+  // lane i looks after the splits i, i + 32: their maxima and sums of weights
+  float f0 = kNegInf, f1 = kNegInf, L = 0.0f;
+  const int64_t part = int64_t(kBM) * (D + 2);
+  if (lane < used) f0 = base[lane * part + kBM * D + r];
+  if (lane + 32 < used) f1 = base[(lane + 32) * part + kBM * D + r];
+  float M = fmaxf(f0, f1);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor(M, d));
+  f0 = rebase(f0, M);
+  f1 = rebase(f1, M);
+  if (lane < used) L = f0 * base[lane * part + kBM * (D + 1) + r];
+  if (lane + 32 < used) L += f1 * base[(lane + 32) * part + kBM * (D + 1) + r];
+#pragma unroll
+  for (int d = 16; d; d >>= 1) L += __shfl_xor(L, d);
+  float O[D / 32];
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) O[j] = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < used; ++i) {
-    const float* p = base + int64_t(i) * kBM * (D + 2);
-    const float f = rebase(p[kBM * D + r], M);
-    L += f * p[kBM * (D + 1) + r];
+  for (int i0 = 0; i0 < used; i0 += 8) {
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      const at_f32x2 x = *reinterpret_cast<const at_f32x2*>(p + r * D + 64 * j + 2 * lane);
-      O[2 * j] += f * x.x;
-      O[2 * j + 1] += f * x.y;
+    for (int k = 0; k < 8; ++k) {                     // 8 splits' loads in flight
+      const int i = min(i0 + k, used - 1);
+      const float f = __shfl(i < 32 ? f0 : f1, (threadIdx.x & 32) + (i & 31));
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const at_f32x2 x = *reinterpret_cast<const at_f32x2*>(base + i * part + r * D + 64 * j + 2 * lane);
+        O[2 * j] += i0 + k < used ? f * x.x : 0.0f;
+        O[2 * j + 1] += i0 + k < used ? f * x.y : 0.0f;
+      }
     }
   }
   const int h = head * a.group + (row - tok * a.group);
@@ -502,21 +688,26 @@ int64_t row_tiles(int64_t seqs, int64_t tokens, int group) { return tokens * gro
 // row tiles alone leave CUs without work.
 int key_splits(int64_t tiles, int heads) {
   const int64_t wgs = tiles * heads;
-  return wgs >= 256 ? 1 : int(std::min<int64_t>((512 + wgs - 1) / wgs, 64));
+  return wgs >= 256 ? 1 : int(std::min<int64_t>((512 + wgs - 1) / wgs, kMaxSplits));
+}
+
+template <class T, int D, int E, bool SPLIT>
+hipError_t launch_split(const AttnArgs& a, const PrefillWork& w, hipStream_t stream) {
+  const unsigned tiles = unsigned(w.row_tiles * a.kv.heads);
+  // (a lane's offset from the first of 16 tokens is kept in 32 bits)
+  if (a.kv.page.d % 16 == 0 && a.kv.token_stride < (1 << 26))
+    prefill_kernel<T, D, E, true, SPLIT><<<tiles * unsigned(w.splits), 256, 0, stream>>>(a, w);
+  else
+    prefill_kernel<T, D, E, false, SPLIT><<<tiles * unsigned(w.splits), 256, 0, stream>>>(a, w);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !SPLIT) return e;
+  prefill_join_kernel<T, D, E><<<dim3(tiles, kBM / 8), 256, 0, stream>>>(a, w);
+  return hipGetLastError();
 }
 
 template <class T, int D, int E>
 hipError_t launch(const AttnArgs& a, const PrefillWork& w, hipStream_t stream) {
-  const unsigned tiles = unsigned(w.row_tiles * a.kv.heads);
-  // (a lane's offset from the first of 16 tokens is kept in 32 bits)
-  if (a.kv.page.d % 16 == 0 && a.kv.token_stride < (1 << 26))
-    prefill_kernel<T, D, E, true><<<tiles * unsigned(w.splits), 256, 0, stream>>>(a, w);
-  else
-    prefill_kernel<T, D, E, false><<<tiles * unsigned(w.splits), 256, 0, stream>>>(a, w);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || w.splits == 1) return e;
-  prefill_join_kernel<T, D, E><<<dim3(tiles, kBM / 8), 256, 0, stream>>>(a, w);
-  return hipGetLastError();
+  return w.splits > 1 ? launch_split<T, D, E, true>(a, w, stream) : launch_split<T, D, E, false>(a, w, stream);
 }
 
 template <class T, int E>
