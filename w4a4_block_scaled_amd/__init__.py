@@ -551,37 +551,46 @@ def attn_prefill(q: torch.Tensor, cu_seqlens: torch.Tensor, k_cache: torch.Tenso
                  out, return_lse, workspace)
 
 
+def _kv_page_layout(what: str, t: torch.Tensor):
+    """(shape of pages, page stride in bytes, page bytes) of [..., pages, page_size, heads, head_dim]."""
+    if t.dim() < 4:
+        raise W4A4Error(2, f"{what}: a cache is [..., pages, page_size, heads, head_dim], got {tuple(t.shape)}")
+    elt, size, stride = t.element_size(), t.shape[-4:], t.stride()[-4:]
+    dense = 1
+    for st, n in sorted(zip(stride[1:], size[1:])):
+        if n > 1:
+            if st != dense:
+                raise W4A4Error(2, f"{what}: a page's {tuple(size[1:])} values must lie densely in memory")
+            dense *= n
+    return size, stride[0] * elt if size[0] > 1 else dense * elt, dense * elt
+
+
 def _kv_arrays(what: str, caches):
     """(n, host array of base pointers, page stride, page bytes, pages, page_size, device)."""
-    tensors = [caches] if isinstance(caches, torch.Tensor) else list(caches)
-    ptrs, first = [], None
-    for t in tensors:
-        if t.dim() < 4:
-            raise W4A4Error(2, f"{what}: a cache is [..., pages, page_size, heads, head_dim], got {tuple(t.shape)}")
-        size, elt = tuple(t.shape[-4:]), t.element_size()
-        stride = tuple(n * elt for n in t.stride()[-4:])
-        dense = elt
-        for st, n in sorted(zip(stride[1:], size[1:])):
-            if n > 1 and st != dense:
-                raise W4A4Error(2, f"{what}: a page's {size[1:]} values must lie densely in memory")
-            dense *= n
-        key = (size, stride[0], dense, t.device)
+    ptrs, first, dev = [], None, None
+    for t in ((caches,) if isinstance(caches, torch.Tensor) else caches):
+        layout = _kv_page_layout(what, t)
         if first is None:
-            first = key
-        elif key != first:
+            first, dev = layout, t.device
+        elif layout != first or t.device != dev:
             raise W4A4Error(2, f"{what}: the caches must be alike")
-        at = [t.data_ptr()]
+        at, elt = [t.data_ptr()], t.element_size()
         for n, st in zip(t.shape[:-4], t.stride()[:-4]):
-            at = [a + i * st * elt for a in at for i in range(n)]
+            at = [x + y for x in at for y in range(0, n * st * elt, st * elt)] if n > 1 and st > 0 else at * n
         ptrs += at
     if first is None:
         raise W4A4Error(2, f"{what}: no caches")
-    (pages, page, _, _), stride, dense, dev = first
-    return len(ptrs), (ctypes.c_void_p * max(len(ptrs), 1))(*ptrs), stride if pages > 1 else dense, dense, pages, page, dev
+    size, stride, dense = first
+    return len(ptrs), (ctypes.c_void_p * max(len(ptrs), 1))(*ptrs), stride, dense, size[0], size[1], dev
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv_workspace_bytes(rows: int, pages: int) -> int:
+    return lib().w4a4_kv_workspace_bytes(rows, pages)
 
 
 def _kv_workspace(rows: int, pages: int, device) -> torch.Tensor:
-    return torch.empty(lib().w4a4_kv_workspace_bytes(rows, pages), dtype=torch.uint8, device=device)
+    return torch.empty(_kv_workspace_bytes(rows, pages), dtype=torch.uint8, device=device)
 
 
 def _same_length(what: str, a: torch.Tensor, b: torch.Tensor) -> int:

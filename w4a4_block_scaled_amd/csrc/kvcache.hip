@@ -45,16 +45,19 @@ __device__ __forceinline__ float e4m3_range(float x) {
   return x != x ? x : fminf(fmaxf(x, -448.0f), 448.0f);
 }
 
-// kTok tokens per workgroup: their cache rows are looked up once by the first
-// kTok threads, then all 256 threads copy 16-byte chunks (8 elements) of K and
-// V, consecutive threads on consecutive chunks of a head.  MODE 0 copies 16-bit
+// A workgroup takes `per_wg` tokens: their cache rows are looked up by its first
+// threads, then `lanes` threads copy a token's 16-byte chunks (8 elements) of K
+// and V, consecutive threads on consecutive chunks of a head, 256 / lanes tokens
+// at a time and kFlight of them in flight per thread.  MODE 0 copies 16-bit
 // elements, 1 / 2 convert BF16 / FP16 to E4M3 (one IEEE division by the head's
 // scale, one RNE conversion per element).
-template <int MODE, int kTok>
-__global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
-  __shared__ int64_t base[kTok];
-  const int64_t first = int64_t(blockIdx.x) * kTok;
-  if (threadIdx.x < kTok) {
+constexpr int kMaxTok = 32, kFlight = 4;
+
+template <int MODE>
+__global__ void __launch_bounds__(256) append_kernel(AppendArgs a, int lanes, int per_wg) {
+  __shared__ int64_t base[kMaxTok];
+  const int64_t first = int64_t(blockIdx.x) * per_wg;
+  if (int(threadIdx.x) < per_wg) {
     const int64_t i = first + threadIdx.x;
     int64_t b = -1;
     if (i < a.tokens) {
@@ -78,34 +81,48 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
   }
   __syncthreads();
   const int per_side = a.kv.heads * a.head_chunks;
-  for (int c = threadIdx.x; c < kTok * 2 * per_side; c += 256) {
-    const int t = c / (2 * per_side), r = c - t * 2 * per_side;
-    const int side = r >= per_side;
-    const int h = (r - side * per_side) / a.head_chunks, d = 8 * ((r - side * per_side) - h * a.head_chunks);
-    if (base[t] < 0) continue;
-    const uint16_t* src = static_cast<const uint16_t*>(a.src[side]) + (first + t) * a.row[side] + h * a.head[side] + d;
-    const kv_u32x4 x = *reinterpret_cast<const kv_u32x4*>(src);
-    const int64_t at = base[t] + h * a.kv.head_stride + d;
+  const int t0 = threadIdx.x / lanes, step = 256 / lanes;
+  for (int c = threadIdx.x % lanes; c < 2 * per_side; c += lanes) {
+    const int side = c >= per_side, r = c - side * per_side;
+    const int h = r / a.head_chunks, d = 8 * (r - h * a.head_chunks);
+    const uint16_t* src = static_cast<const uint16_t*>(a.src[side]) + first * a.row[side] + h * a.head[side] + d;
+    const int64_t at = h * a.kv.head_stride + d;
     void* dst = const_cast<void*>(side ? a.kv.v : a.kv.k);
-    if (MODE == 0) {
-      *reinterpret_cast<kv_u32x4*>(static_cast<uint16_t*>(dst) + at) = x;
-    } else {
+    float sc = 1.0f;
+    if (MODE) {
       const float* scales = side ? a.kv.v_scale : a.kv.k_scale;
-      const float sc = scales ? scales[h] : 1.0f;
-      kv_u32x2 o;
+      if (scales) sc = scales[h];
+    }
+    for (int tt = t0; tt < per_wg; tt += kFlight * step) {
+      kv_u32x4 x[kFlight];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        float f[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t u = x[2 * w + j / 2];
-          f[j] = e4m3_range(bits_to_f32(uint16_t(j & 1 ? u >> 16 : u), MODE == 2) / sc);
-        }
-        int p = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
-        p = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], p, true);
-        o[w] = uint32_t(p);
+      for (int j = 0; j < kFlight; ++j) {
+        const int t = tt + j * step;
+        if (t < per_wg && base[t] >= 0) x[j] = *reinterpret_cast<const kv_u32x4*>(src + t * a.row[side]);
       }
-      *reinterpret_cast<kv_u32x2*>(static_cast<uint8_t*>(dst) + at) = o;
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j) {
+        const int t = tt + j * step;
+        if (t >= per_wg || base[t] < 0) continue;
+        if (MODE == 0) {
+          *reinterpret_cast<kv_u32x4*>(static_cast<uint16_t*>(dst) + base[t] + at) = x[j];
+        } else {
+          kv_u32x2 o;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            float f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t u = x[j][2 * w + k / 2];
+              f[k] = e4m3_range(bits_to_f32(uint16_t(k & 1 ? u >> 16 : u), MODE == 2) / sc);
+            }
+            int p = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+            p = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], p, true);
+            o[w] = uint32_t(p);
+          }
+          *reinterpret_cast<kv_u32x2*>(static_cast<uint8_t*>(dst) + base[t] + at) = o;
+        }
+      }
     }
   }
 }
@@ -117,19 +134,81 @@ struct Arrays {
   uint8_t* p[kMaxArrays];
 };
 
+// The tables' share of an operation that moves pages: its first `blocks`
+// workgroups, so that it takes no launch of its own.
+struct NoBook {
+  int blocks = 0;
+  __device__ void operator()() const {}
+};
+// The children's tables, one workgroup each; whole pages get one more reference.
+struct ForkBook {
+  int32_t* tables;
+  int64_t table_stride;
+  const int32_t* lens;
+  int seqs, max_pages;
+  int32_t* refs;
+  int pages, page_size;
+  const int32_t *parents, *children, *own;
+  int blocks;
+  __device__ void operator()() const {
+    const int p = parents[blockIdx.x], c = children[blockIdx.x];
+    if (p < 0 || p >= seqs || c < 0 || c >= seqs || p == c) return;
+    const int full = max(lens[p], 0) / page_size;
+    const int last = own[blockIdx.x];
+    for (int j = threadIdx.x; j < max_pages; j += 256) {
+      int e = -1;
+      if (j < full) {
+        e = tables[p * table_stride + j];
+        if (e >= 0 && e < pages) atomicAdd(&refs[e], 1);
+        else e = -1;
+      } else if (j == full) {
+        e = last;
+      }
+      tables[c * table_stride + j] = e;
+    }
+  }
+};
+// Every table entry to its page's new place; the references move along.
+struct CompactBook {
+  int32_t* tables;
+  int64_t table_stride, entries;
+  int max_pages;
+  int32_t* refs;
+  int pages;
+  const int32_t *remap, *src, *dst, *count;
+  int blocks;
+  __device__ void operator()() const {
+    const int64_t stride = int64_t(blocks) * 256, at = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    for (int64_t i = at; i < entries; i += stride) {
+      int32_t* e = tables + (i / max_pages) * table_stride + i % max_pages;
+      const int32_t p = *e;
+      if (p >= 0) *e = p < pages ? remap[p] : -1;
+    }
+    const int n = *count;
+    for (int64_t i = at; i < n; i += stride) {
+      refs[dst[i]] = refs[src[i]];
+      refs[src[i]] = 0;
+    }
+  }
+};
+
 // Moves page src[i] to dst[i], i < pairs (or *count if given), in n arrays.
 // Work items are 16 KiB pieces of a page (4 units of 16 bytes per thread, all
 // loaded before the first store), handed out in a grid-stride loop, since the
 // number of pairs may only be known on the device.
-template <typename UNIT>
+template <typename UNIT, class BOOK>
 __global__ void __launch_bounds__(256) copy_pages_kernel(Arrays arrays, int n, int64_t stride, int64_t units, int pages,
                                                          const int32_t* __restrict__ src,
                                                          const int32_t* __restrict__ dst, int64_t pairs,
-                                                         const int32_t* __restrict__ count) {
+                                                         const int32_t* __restrict__ count, BOOK book) {
+  if (int(blockIdx.x) < book.blocks) {
+    book();
+    return;
+  }
   if (count) pairs = min(pairs, int64_t(*count));
   const int64_t pieces = (units + 1023) / 1024;
   const int64_t items = pairs * n * pieces;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+  for (int64_t it = blockIdx.x - book.blocks; it < items; it += gridDim.x - book.blocks) {
     const int64_t piece = it % pieces, rest = it / pieces;
     const int64_t i = rest / n;
     const int s = src[i], d = dst[i];
@@ -148,22 +227,23 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(Arrays arrays, int n, i
   }
 }
 
+template <class BOOK>
 hipError_t copy_pairs(const PageMove& mv, int pages, const int32_t* src, const int32_t* dst, int64_t pairs,
-                      const int32_t* count, hipStream_t stream) {
-  if (pairs <= 0 || mv.page_bytes <= 0) return hipSuccess;
+                      const int32_t* count, BOOK book, hipStream_t stream) {
   const bool wide = mv.page_bytes % 16 == 0 && mv.stride_bytes % 16 == 0;   // array bases are 16-byte aligned
   const int64_t units = wide ? mv.page_bytes / 16 : mv.page_bytes;
-  for (int at = 0; at < mv.n; at += kMaxArrays) {
+  for (int at = 0; at < std::max(mv.n, 1); at += kMaxArrays) {
     const int n = std::min(mv.n - at, kMaxArrays);
     Arrays a;
-    for (int i = 0; i < n; ++i) a.p[i] = static_cast<uint8_t*>(mv.arrays[at + i]);
-    for (int i = n; i < kMaxArrays; ++i) a.p[i] = nullptr;
+    for (int i = 0; i < kMaxArrays; ++i) a.p[i] = i < n ? static_cast<uint8_t*>(mv.arrays[at + i]) : nullptr;
+    if (at) book.blocks = 0;
     const int64_t items = pairs * n * ((units + 1023) / 1024);
-    const unsigned grid = unsigned(std::min<int64_t>(items, 4096));
+    const unsigned grid = unsigned(std::min<int64_t>(items, 4096) + book.blocks);
+    if (grid == 0) continue;
     if (wide)
-      copy_pages_kernel<kv_u32x4><<<grid, 256, 0, stream>>>(a, n, mv.stride_bytes, units, pages, src, dst, pairs, count);
+      copy_pages_kernel<kv_u32x4><<<grid, 256, 0, stream>>>(a, n, mv.stride_bytes, units, pages, src, dst, pairs, count, book);
     else
-      copy_pages_kernel<uint8_t><<<grid, 256, 0, stream>>>(a, n, mv.stride_bytes, units, pages, src, dst, pairs, count);
+      copy_pages_kernel<uint8_t><<<grid, 256, 0, stream>>>(a, n, mv.stride_bytes, units, pages, src, dst, pairs, count, book);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -330,30 +410,6 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const int32_t* __restr
   if (lacking && threadIdx.x == 0) *lacking = int32_t(want - got);
 }
 
-// The children's tables, one workgroup each; whole pages get one more reference.
-__global__ void __launch_bounds__(256) fork_tables_kernel(int32_t* tables, int64_t table_stride,
-                                                          const int32_t* __restrict__ lens, int seqs, int max_pages,
-                                                          int32_t* refs, int pages, int page_size,
-                                                          const int32_t* __restrict__ parents,
-                                                          const int32_t* __restrict__ children,
-                                                          const int32_t* __restrict__ dst) {
-  const int p = parents[blockIdx.x], c = children[blockIdx.x];
-  if (p < 0 || p >= seqs || c < 0 || c >= seqs || p == c) return;
-  const int full = max(lens[p], 0) / page_size;
-  const int own = dst[blockIdx.x];
-  for (int j = threadIdx.x; j < max_pages; j += 256) {
-    int e = -1;
-    if (j < full) {
-      e = tables[p * table_stride + j];
-      if (e >= 0 && e < pages) atomicAdd(&refs[e], 1);
-      else e = -1;
-    } else if (j == full) {
-      e = own;
-    }
-    tables[c * table_stride + j] = e;
-  }
-}
-
 // One workgroup per sequence.  An entry is taken out of the table with an
 // atomic exchange, and only who got it drops the reference, so an id that is
 // listed twice is freed once.
@@ -420,36 +476,20 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const int32_t* __re
   if (threadIdx.x == 0) *count = int32_t(movers);
 }
 
-__global__ void __launch_bounds__(256) compact_tables_kernel(int32_t* tables, int64_t table_stride, int64_t entries,
-                                                             int max_pages, int32_t* refs, int pages,
-                                                             const int32_t* __restrict__ remap,
-                                                             const int32_t* __restrict__ src,
-                                                             const int32_t* __restrict__ dst,
-                                                             const int32_t* __restrict__ count) {
-  const int64_t stride = int64_t(gridDim.x) * 256, at = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  for (int64_t i = at; i < entries; i += stride) {
-    int32_t* e = tables + (i / max_pages) * table_stride + i % max_pages;
-    const int32_t p = *e;
-    if (p >= 0) *e = p < pages ? remap[p] : -1;
-  }
-  const int n = *count;
-  for (int64_t i = at; i < n; i += stride) {
-    refs[dst[i]] = refs[src[i]];
-    refs[src[i]] = 0;
-  }
-}
-
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
 
 template <int MODE>
 static void append_mode(const AppendArgs& a, hipStream_t stream) {
-  // one token per workgroup until the card is full, then 4
-  if (a.tokens <= 1024)
-    append_kernel<MODE, 1><<<unsigned(a.tokens), 256, 0, stream>>>(a);
-  else
-    append_kernel<MODE, 4><<<unsigned((a.tokens + 3) / 4), 256, 0, stream>>>(a);
+  int lanes = 16;                                      // a power of two that holds a token's chunks, at most 256
+  while (lanes < 256 && lanes < 2 * a.kv.heads * a.head_chunks) lanes *= 2;
+  // one pass of the threads per workgroup until there are four of them per CU,
+  // then up to kFlight passes
+  const int step = 256 / lanes;
+  const int64_t passes = std::min<int64_t>(kFlight, std::max<int64_t>(1, a.tokens / (1024 * step)));
+  const int per_wg = int(std::min<int64_t>(kMaxTok, step * passes));
+  append_kernel<MODE><<<unsigned((a.tokens + per_wg - 1) / per_wg), 256, 0, stream>>>(a, lanes, per_wg);
 }
 
 hipError_t launch_kv_append(const KvView& kv, int dtype, int head_dim, const int32_t* cu, int64_t tokens, int in_dtype,
@@ -464,7 +504,7 @@ hipError_t launch_kv_append(const KvView& kv, int dtype, int head_dim, const int
 
 hipError_t launch_kv_copy_pages(const PageMove& mv, int pages, const int32_t* src, const int32_t* dst, int64_t pairs,
                                 hipStream_t stream) {
-  return copy_pairs(mv, pages, src, dst, pairs, nullptr, stream);
+  return copy_pairs(mv, pages, src, dst, pairs, nullptr, NoBook(), stream);
 }
 
 // [off int64 x (seqs + 1)] [first int32 x seqs] [list int32 x pages]
@@ -500,11 +540,9 @@ hipError_t launch_kv_fork(const PageMove& mv, int32_t* tables, int64_t table_str
                                             parents, children, n, lacking, src, dst, reinterpret_cast<int32_t*>(w));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || n == 0) return e;
-  fork_tables_kernel<<<unsigned(n), 256, 0, stream>>>(tables, table_stride, lens, seqs, max_pages, refs, pages,
-                                                      page_size, parents, children, dst);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return copy_pairs(mv, pages, src, dst, n, nullptr, stream);
+  return copy_pairs(mv, pages, src, dst, n, nullptr,
+                    ForkBook{tables, table_stride, lens, seqs, max_pages, refs, pages, page_size, parents, children, dst, n},
+                    stream);
 }
 
 hipError_t launch_kv_free(int32_t* tables, int64_t table_stride, int32_t* lens, int seqs, int max_pages, int32_t* refs,
@@ -530,13 +568,11 @@ hipError_t launch_kv_compact(const PageMove& mv, int32_t* tables, int64_t table_
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // at most half of the pages move: as many holes lie below them
-  e = copy_pairs(mv, pages, src, dst, pages / 2 + 1, count, stream);
-  if (e != hipSuccess) return e;
   const int64_t entries = int64_t(seqs) * max_pages;
-  const unsigned grid = unsigned(std::min<int64_t>(1024, (std::max<int64_t>(entries, pages / 2 + 1) + 255) / 256));
-  compact_tables_kernel<<<grid, 256, 0, stream>>>(tables, table_stride, entries, max_pages, refs, pages, remap, src,
-                                                  dst, count);
-  return hipGetLastError();
+  const int blocks = int(std::min<int64_t>(256, (std::max<int64_t>(entries, pages / 2 + 1) + 255) / 256));
+  return copy_pairs(mv, pages, src, dst, pages / 2 + 1, count,
+                    CompactBook{tables, table_stride, entries, max_pages, refs, pages, remap, src, dst, count, blocks},
+                    stream);
 }
 
 }  // namespace w4a4
