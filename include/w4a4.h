@@ -406,10 +406,10 @@ w4a4_status w4a4_dualquant_solve(w4a4_format fmt, int64_t N, int64_t K,
  *
  * tables, lens and the other index arrays are device memory that the host
  * never reads, so their contents cannot be refused by a status.  Nothing is
- * ever read or written outside the buffers for any contents: a sequence whose
- * table lacks a valid page (an entry outside 0..pages-1, or a length beyond
- * max_pages * page_size) for a token that a query sees gets BF16 / FP16 NaN
- * for that query's kv head, and tokens without a page are not stored.
+ * ever read or written outside the buffers for any contents: a query that sees
+ * a token without a valid page (an entry outside 0..pages-1), or whose sequence
+ * is longer than max_pages * page_size, gets BF16 / FP16 NaN, and so may other
+ * queries of the sequence; tokens without a page are not stored.
  */
 typedef enum { W4A4_BF16 = 0, W4A4_F16 = 1, W4A4_E4M3 = 2 } w4a4_dtype;
 

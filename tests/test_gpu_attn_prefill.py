@@ -205,3 +205,76 @@ def test_prefill_nothing_to_do():
     q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=dev)
     y = w4.attn_prefill(q, ints([0, 0], dev), k, k, ints([[0, 1]], dev), ints([5], dev))
     assert y.shape == (0, 4, 64)
+
+
+# Few queries per sequence go another way than many (and pages that are no
+# multiple of 8 tokens always go the way of many): the cases below cross both.
+
+@pytest.mark.parametrize("kind,kv,group,dim,page,past,new", [
+    ("bf16", 2, 4, 128, 16, [3000, 7, 0], [4, 3, 1]),            # up to 16 rows
+    ("fp16", 4, 7, 64, 32, [500, 2100], [4, 3]),                 # up to 32
+    ("fp8", 2, 4, 128, 64, [5000, 0, 77], [9, 16, 0]),           # up to 64
+    ("bf16", 1, 20, 256, 8, [300], [3]),
+    ("fp8", 3, 1, 64, 16, [100, 900, 40], [40, 2, 1]),           # uneven: 40 rows in blocks of 16
+    ("bf16", 2, 4, 128, 16, [4000, 3000], [40, 33]),             # many rows, the keys split
+    ("fp16", 1, 8, 64, 16, [6000], [30]),
+    ("fp8", 2, 7, 128, 32, [2500], [25]),
+    ("bf16", 1, 4, 256, 16, [2000], [50]),
+    ("bf16", 2, 4, 128, 11, [3000, 7], [4, 3]),
+])
+def test_prefill_few_and_split(kind, kv, group, dim, page, past, new):
+    say(f"[prefill] few / split: {kind} {kv} x {group} heads of {dim}, page {page}, past {past}, new {new}")
+    c = chunks(kind, kv, group, dim, page, past, new, seed=sum(past) + dim)
+    for window, sinks in ((0, 0), (70, 5), (1500, 0)):
+        y, lse = run(c, window, sinks)
+        check(c, y, lse, window, sinks, label=f"window {window} sinks {sinks}", most=8)
+
+
+@pytest.mark.parametrize("new", [[3, 2], [8, 8], [16, 12], [60, 50]])
+def test_prefill_few_edges(new):
+    """Rows that see nothing, pages that are missing, and values in masked places,
+    for every way that few rows go."""
+    say(f"[prefill] few, edges: new {new}")
+    c = chunks("bf16", 2, 4, 128, 16, [600, 600], new, seed=sum(new))
+    clean, lse = run(c, 90, 3)
+    check(c, clean, lse, 90, 3, label="window", most=8)
+    n0 = new[0]
+    # a length below the number of queries
+    lens = [2, c["lens"][1]]
+    y, l2 = run(c, 90, 3, lens=lens)
+    assert torch.all(y[:n0 - 2] == 0) and torch.all(l2[:n0 - 2] == float("-inf")) and torch.isfinite(y[n0 - 2:n0]).all()
+    assert torch.equal(y[n0:], clean[n0:])
+    # missing pages: of a seen token, and of one before every window
+    t = c["tables"].copy()
+    t[0, c["lens"][0] // 16 - 1] = -1
+    t[1, 5:20] = c["kd"].shape[0]
+    y, _ = run(c, 90, 3, tables=t)
+    first = max(0, 16 * (c["lens"][0] // 16 - 1) - 600)          # the first query that sees a token of the missing page
+    assert torch.isnan(y[first:n0]).all() and torch.equal(y[n0:], clean[n0:])
+    # Inf and NaN in the last token's values: only the last query sees them
+    last = c["lens"][0] - 1
+    at = (c["tables"][0, last // 16], last % 16)
+    c["vd"][at[0], at[1], 0, 5] = float("inf")
+    c["vd"][at[0], at[1], 0, 6] = float("nan")
+    c["kd"][at[0], at[1], 1, 3] = float("nan")
+    y, _ = run(c, 90, 3)
+    row = n0 - 1
+    keep = [i for i in range(len(clean)) if i != row]
+    assert torch.all(y[row, :4, 5] == float("inf")) and torch.isnan(y[row, :4, 6]).all() and torch.isnan(y[row, 4:]).all()
+    assert torch.isfinite(y[keep]).all() and (y[keep].float() - clean[keep].float()).abs().max() <= 2.0 ** -6
+    # uninitialised rows past the end
+    held = -(-c["lens"][1] // 16) * 16
+    if held > c["lens"][1]:
+        c["vd"][c["tables"][1, held // 16 - 1], c["lens"][1] % 16:] = float("nan")
+        z, _ = run(c, 90, 3)
+        assert torch.equal(z, y) or torch.equal(torch.nan_to_num(z), torch.nan_to_num(y))
+
+
+def test_prefill_row_counts_that_do_not_fit():
+    """cu_seqlens that point outside the rows: nothing outside is touched."""
+    say("[prefill] few rows, stray cu_seqlens")
+    c = chunks("bf16", 2, 4, 128, 16, [60, 60, 60], [4, 4, 4], seed=9)
+    dev = c["dev"]
+    for cu in ([0, 4, 20, 12], [0, -4, 8, 12], [5, 5, 5, 10 ** 9], [7, 7, 7, 7]):
+        w4.attn_prefill(c["q"].to(dev), ints(cu, dev), c["kd"], c["vd"], ints(c["tables"], dev), ints(c["lens"], dev))
+    torch.cuda.synchronize()

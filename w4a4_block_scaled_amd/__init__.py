@@ -459,9 +459,10 @@ def _kv_stream(device: torch.device) -> int:
 
 
 @functools.lru_cache(maxsize=4096)
-def _attn_workspace_bytes(prefill: bool, dtype: int, heads: int, dim: int, seqs: int, tokens: int, q_heads: int) -> int:
+def _attn_workspace_bytes(prefill: bool, dtype: int, page: int, heads: int, dim: int, seqs: int, tokens: int,
+                          q_heads: int) -> int:
     """w4a4_attn_*_workspace_bytes: depends on these numbers alone."""
-    c = _KvCache(16, 16, None, None, 0, 0, 0, dtype, 1, 1, heads, dim)
+    c = _KvCache(16, 16, None, None, 0, 0, 0, dtype, 1, page, heads, dim)
     return (lib().w4a4_attn_prefill_workspace_bytes(c, seqs, tokens, q_heads) if prefill else
             lib().w4a4_attn_decode_workspace_bytes(c, seqs, q_heads))
 
@@ -512,7 +513,7 @@ def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, sc
             raise W4A4Error(4, f"{name}: out is {out.dtype}, q is {q.dtype}")
     lse = torch.empty((rows, q_heads), dtype=torch.float32, device=dev) if return_lse else None
     if workspace is None:
-        size = _attn_workspace_bytes(cu is not None, c.dtype, c.heads, dim, s.seqs, rows, q_heads)
+        size = _attn_workspace_bytes(cu is not None, c.dtype, c.page_size, c.heads, dim, s.seqs, rows, q_heads)
         if size:
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     else:

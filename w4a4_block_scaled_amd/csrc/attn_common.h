@@ -28,21 +28,42 @@ __device__ __forceinline__ uint32_t without_odd(uint32_t u) {
   return ((u & EXP) == EXP ? 0 : u & 0xffffu) | ((u >> 16 & EXP) == EXP ? 0 : u & 0xffff0000u);
 }
 
+// u with 0 in the place of the halves that are Inf or NaN; *plus gets ONE for +Inf
+// and NaN, *minus for -Inf and NaN, 0 elsewhere.
+template <uint32_t EXP, uint32_t ONE>
+__device__ __forceinline__ uint32_t split_odd16(uint32_t u, uint32_t* plus, uint32_t* minus) {
+  uint32_t keep = 0, p = 0, n = 0;
+#pragma unroll
+  for (int s = 0; s < 32; s += 16) {
+    const uint32_t x = u >> s & 0xffffu;
+    const bool odd = (x & EXP) == EXP, nan = odd && (x & 0x7fffu) != EXP;
+    keep |= odd ? 0 : x << s;
+    p |= odd && (nan || x < 0x8000u) ? ONE << s : 0;
+    n |= odd && (nan || x >= 0x8000u) ? ONE << s : 0;
+  }
+  *plus = p;
+  *minus = n;
+  return keep;
+}
+
 // 16-bit element types.  pack(a, b): two fp32 to two elements, RNE, a in the
 // low half.  mfma16: 16 x 16 x 32, mfma32: 32 x 32 x 16; operands 8 elements
 // per lane.
 struct Bf16 {
-  static constexpr uint32_t kExp = 0x7f80u;      // the exponent of Inf and NaN
+  static constexpr uint32_t kExp = 0x7f80u, kOne = 0x3f80u;      // the exponent of Inf and NaN; 1.0
   static __device__ __forceinline__ bool not_finite(uint32_t u) { return has_odd<kExp>(u); }
   static __device__ __forceinline__ uint32_t finite(uint32_t u) { return without_odd<kExp>(u); }
+  static __device__ __forceinline__ uint32_t split_odd(uint32_t u, uint32_t* plus, uint32_t* minus) {
+    return split_odd16<kExp, kOne>(u, plus, minus);
+  }
   typedef __bf16 x8 __attribute__((ext_vector_type(8)));
   typedef __bf16 x2 __attribute__((ext_vector_type(2)));
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((at_f32x2){a, b}, x2));
   }
-  // pack() of values that the type holds exactly (E4M3 values): the upper halves
-  static __device__ __forceinline__ uint32_t pack_exact(float a, float b) {
-    return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302);
+  template <bool HI>
+  static __device__ __forceinline__ x2 from_e4m3(uint32_t u) {
+    return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u, 1.0f, HI);
   }
   static __device__ __forceinline__ float low(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
   static __device__ __forceinline__ float high(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
@@ -54,16 +75,20 @@ struct Bf16 {
   }
 };
 struct F16 {
-  static constexpr uint32_t kExp = 0x7c00u;      // the exponent of Inf and NaN
+  static constexpr uint32_t kExp = 0x7c00u, kOne = 0x3c00u;      // the exponent of Inf and NaN; 1.0
   static __device__ __forceinline__ bool not_finite(uint32_t u) { return has_odd<kExp>(u); }
   static __device__ __forceinline__ uint32_t finite(uint32_t u) { return without_odd<kExp>(u); }
+  static __device__ __forceinline__ uint32_t split_odd(uint32_t u, uint32_t* plus, uint32_t* minus) {
+    return split_odd16<kExp, kOne>(u, plus, minus);
+  }
   typedef _Float16 x8 __attribute__((ext_vector_type(8)));
   typedef _Float16 x2 __attribute__((ext_vector_type(2)));
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((at_f32x2){a, b}, x2));
   }
-  static __device__ __forceinline__ uint32_t pack_exact(float a, float b) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+  template <bool HI>
+  static __device__ __forceinline__ x2 from_e4m3(uint32_t u) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, HI);
   }
   static __device__ __forceinline__ float low(uint32_t u) {
     return float(__builtin_bit_cast(x2, u).x);
@@ -82,8 +107,7 @@ struct F16 {
 // Two E4M3 codes (the low or the high half of u) as two elements of T, exact.
 template <class T, bool HI>
 __device__ __forceinline__ uint32_t e4m3_pair(uint32_t u) {
-  const at_f32x2 f = __builtin_amdgcn_cvt_pk_f32_fp8(int(u), HI);
-  return T::pack_exact(f.x, f.y);
+  return __builtin_bit_cast(uint32_t, T::template from_e4m3<HI>(u));
 }
 
 // x of the lanes l and l ^ 32 (l ^ 16), in either order: halves (odd and even

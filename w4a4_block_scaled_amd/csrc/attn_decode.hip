@@ -1,8 +1,8 @@
-// Attention of one new token per sequence over the paged cache.
+// Attention of one new token per sequence, or a few, over the paged cache.
 //
-// Each kv head of each sequence is a unit with `rows` query rows (the group's
-// heads, in blocks of 16), and reads its visible keys and values once: 4 to 16
-// fp operations per byte, so HBM bandwidth bounds it.  The units' visible
+// Each kv head of each sequence is a unit with the group's heads as query rows,
+// in blocks of 16 (FEW: the heads of its few tokens), and reads its visible keys and values once: 4 to 16 fp operations per
+// byte, so HBM bandwidth bounds it.  The units' visible
 // tokens, in tiles of 128, form one list over all sequences, of which every
 // workgroup takes an equal contiguous piece, whatever the lengths are.  A
 // workgroup that holds a unit whole writes its output; a unit cut by the
@@ -20,6 +20,7 @@
 // (high and rest, about 16 bits together): the matrix cores idle here, so the
 // second product is free and only the output is rounded to 16 bits.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_common.h"
 
@@ -27,7 +28,7 @@ namespace w4a4 {
 namespace {
 
 constexpr int kTile = 128;       // tokens per workgroup step: 4 waves x 32
-constexpr int kRows = 16;
+constexpr int kRows = 16;        // of a unit
 
 // The list of work: per sequence, tiles over [0, sink_end) and [start, len).
 // A length beyond the table's capacity is cut to it and marked (`over`).
@@ -36,13 +37,14 @@ struct SeqSpan {
   bool over;
 };
 
-__device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, int length) {
+// `count`: the sequence's queries, its last tokens.
+__device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, int length, int count) {
   SeqSpan z;
   const int cap = int(min(int64_t(a.kv.max_pages) * a.kv.page.d, int64_t(1) << 30));
   const int len = max(length, 0);
   z.over = len > cap;
   z.len = min(len, cap);
-  z.low = a.window ? max(z.len - a.window, 0) : 0;   // first token of the window
+  z.low = a.window ? max(z.len - count + 1 - a.window, 0) : 0;   // first token of the first query's window
   z.start = z.low & ~7;
   z.sink_end = min(a.sinks, z.start);
   z.sink_tiles = (z.sink_end + kTile - 1) / kTile;
@@ -57,11 +59,18 @@ struct Partial {
   float *o, *m, *l;
 };
 
+// A cut unit: written by the workgroup that begins it.
+struct Cut {
+  int32_t seq, unit, count, unused;      // count: workgroups that hold parts of it
+};
+
 struct Work {
-  int32_t* first;   // [seqs x units]: workgroup that begins the unit
-  int32_t* count;   // [seqs x units]: workgroups that hold parts of it
-  float* parts;     // [workgroups x 2] partial results
-  int rows;         // min(group, 16)
+  float* parts;       // [workgroups x 2] partial results
+  Cut* cuts;          // [workgroups]
+  int rows;           // of a partial result
+  const int32_t* cu;  // FEW: rows of q
+  int tokens;
+  FastDiv group;
 };
 
 __host__ __device__ constexpr int partial_floats(int rows, int D) { return (rows * (D + 2) + 3) / 4 * 4; }
@@ -139,11 +148,10 @@ struct Tile {
         (*lo)[t] = __builtin_amdgcn_perm(y, x, 0x05040100);
         (*hi)[t] = __builtin_amdgcn_perm(y, x, 0x07060302);
       } else {
-        const int x = int(v[2 * t][r][j / 4]), y = int(v[2 * t + 1][r][j / 4]);
-        const at_f32x2 a = j % 4 ? __builtin_amdgcn_cvt_pk_f32_fp8(x, true) : __builtin_amdgcn_cvt_pk_f32_fp8(x, false);
-        const at_f32x2 b = j % 4 ? __builtin_amdgcn_cvt_pk_f32_fp8(y, true) : __builtin_amdgcn_cvt_pk_f32_fp8(y, false);
-        (*lo)[t] = T::pack_exact(a.x, b.x);
-        (*hi)[t] = T::pack_exact(a.y, b.y);
+        const uint32_t x = v[2 * t][r][j / 4], y = v[2 * t + 1][r][j / 4];
+        const uint32_t z = __builtin_amdgcn_perm(y, x, j % 4 ? 0x07030602 : 0x05010400);      // codes x_j y_j x_j+1 y_j+1
+        (*lo)[t] = e4m3_pair<T, false>(z);
+        (*hi)[t] = e4m3_pair<T, true>(z);
       }
     }
   }
@@ -160,65 +168,128 @@ struct Rows {
 // Workgroups that share a CU: what the registers of two tiles leave room for.
 constexpr int wgs_per_cu(int D, int E, bool oct) { return D == 256 ? 1 : oct && D == 64 ? 3 : 2; }
 
+// A sequence's queries: the rows of one kv head are count * group, token by token.
+struct Queries {
+  int count, first;
+};
+template <bool FEW>
+__device__ __forceinline__ Queries queries_of(const Work& w, int s) {
+  if (!FEW) return {1, s};
+  const int first = w.cu[s];
+  return {min(max(w.cu[s + 1] - first, 0), w.tokens), first};
+}
+
+__device__ __forceinline__ int readlane(int x, int l) { return __builtin_amdgcn_readlane(x, l); }
+__device__ __forceinline__ int64_t readlane(int64_t x, int l) {
+  return int64_t(uint32_t(__builtin_amdgcn_readlane(int(x), l))) | int64_t(__builtin_amdgcn_readlane(int(x >> 32), l)) << 32;
+}
+
+// Output columns d .. d + 3 of row `row` of a kv head from its maximum, sum of
+// weights and unnormalised sum.
+template <class T, int D, int E, bool FEW>
+__device__ __forceinline__ void finish(const AttnArgs& a, const Work& w, int head, const Queries& qs, const SeqSpan& sp,
+                                       int row, int d, float M, float L, at_f32x4 O) {
+  const int tok = FEW ? w.group.div(row) : 0, h = head * a.group + row - tok * a.group;
+  const int64_t at = int64_t(qs.first) + tok;
+  if (FEW && (at < 0 || at >= w.tokens)) return;
+  const bool none = sp.len - qs.count + tok < 0 && !sp.over;       // a query before position 0
+  const float inv = (E == 1 && a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / L;
+  at_u32x2 y = {T::pack(O[0] * inv, O[1] * inv), T::pack(O[2] * inv, O[3] * inv)};
+  if (none) y = (at_u32x2){0, 0};
+  *reinterpret_cast<at_u32x2*>(static_cast<uint16_t*>(a.out) + at * a.o_row + h * a.o_head + d) = y;
+  if (a.lse && d == 0) a.lse[at * a.q_heads + h] = none ? kNegInf : (M + __log2f(L)) * 0.693147180559945f;
+}
+
+// Adds the Inf and NaN of a value operand to the sums of the rows that see them
+// (`see`: 1.0 or 0 per token and row), and returns it with zeros in their place.
+template <class T>
+__device__ __forceinline__ at_u32x4 add_odd(at_u32x4 v, at_u32x4 see, at_f32x4* o) {
+  at_u32x4 plus, minus;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t p, n;
+    v[k] = T::split_odd(v[k], &p, &n);
+    plus[k] = p;
+    minus[k] = n;
+  }
+  const at_f32x4 zero = {0, 0, 0, 0}, up = T::mfma16(plus, see, zero), down = T::mfma16(minus, see, zero);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (up[i] > 0.0f) (*o)[i] -= kNegInf;
+    if (down[i] > 0.0f) (*o)[i] += kNegInf;
+  }
+  return v;
+}
+
 // OCT: the page size is a multiple of 8, so 8 tokens from a multiple of 8 lie
 // on one page and one lookup serves them; otherwise every row is looked up.
-template <class T, int D, int E, bool OCT>
+// FEW: the sequences have any number of queries (a few, if it is to be fast).
+template <class T, int D, int E, bool OCT, bool FEW>
 __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(AttnArgs a, Work work) {
   typedef Tile<T, D, E> TileT;
   constexpr int kSteps = TileT::kSteps, kRun = TileT::kRun, kRuns = TileT::kRuns;
   constexpr int kBlocks = D / 16;                        // MFMAs of the value product
+  typedef std::conditional_t<FEW, int64_t, int> Sum;     // of tiles (FEW: times units) of 64 sequences
   __shared__ float lds_o[4][kRows][D + 4];
   __shared__ float lds_m[4][kRows], lds_l[4][kRows];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
-  const int blocks_per_head = (a.group + kRows - 1) / kRows;
-  const int units = a.kv.heads * blocks_per_head;
+  const int64_t wg = blockIdx.x;
+  if (threadIdx.x == 0) work.cuts[wg].count = 0;
 
   // This workgroup's piece [item, end) of the list of (sequence, unit, tile),
   // and the sequence that `item` falls in, with the place where that begins.
   // Lane l looks after the sequences l, l + 64, ...; up to 64 sequences take one
   // load of the lengths.
+  auto units_of = [&](int count) { return a.kv.heads * ((count * a.group + kRows - 1) / kRows); };
+  const int64_t units1 = FEW ? 1 : units_of(1);
   auto length = [&](int s) { return s < a.kv.seqs ? a.kv.lens[s] : 0; };
-  auto tiles_of = [&](int s, int len) { return s < a.kv.seqs ? seq_span(a, len).tiles : 0; };
-  auto scan = [&](int t) {
+  auto share_of = [&](int s, int len) -> Sum {
+    if (s >= a.kv.seqs) return 0;
+    const int count = queries_of<FEW>(work, s).count;
+    const Sum tiles = seq_span(a, len, count).tiles;
+    return FEW ? tiles * units_of(count) : tiles;
+  };
+  auto scan = [&](Sum t) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int y = __shfl_up(t, d);
+      const Sum y = __shfl_up(t, d);
       if (lane >= d) t += y;
     }
     return t;
   };
-  const int len0 = length(lane), mine0 = tiles_of(lane, len0), in0 = scan(mine0);
-  int64_t total = __builtin_amdgcn_readlane(in0, 63);
-  for (int base = 64; base < a.kv.seqs; base += 64)
-    total += __builtin_amdgcn_readlane(scan(tiles_of(base + lane, length(base + lane))), 63);
-  total *= units;
+  const int len0 = length(lane);
+  const Sum mine0 = share_of(lane, len0), in0 = scan(mine0);
+  int64_t total = readlane(in0, 63);
+  for (int base = 64; base < a.kv.seqs; base += 64) total += readlane(scan(share_of(base + lane, length(base + lane))), 63);
+  total *= units1;
   const int64_t wgs = min(int64_t(gridDim.x), total);
-  const int64_t wg = blockIdx.x;
   if (wg >= wgs) return;
   int64_t item = wg * total / wgs;
   const int64_t end = (wg + 1) * total / wgs;
   int seq = 0;
   int64_t seq_begin = 0;
   for (int base = 0; base < a.kv.seqs; base += 64) {
-    int mine = mine0, in = in0;
+    Sum mine = mine0, in = in0;
     if (base) {
-      mine = tiles_of(base + lane, length(base + lane));
+      mine = share_of(base + lane, length(base + lane));
       in = scan(mine);
     }
-    const uint64_t past = __ballot(seq_begin + int64_t(in) * units > item);
+    const uint64_t past = __ballot(seq_begin + int64_t(in) * units1 > item);
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
       seq = base + l;
-      seq_begin += int64_t(__builtin_amdgcn_readlane(in - mine, l)) * units;
+      seq_begin += int64_t(readlane(Sum(in - mine), l)) * units1;
       break;
     }
-    seq_begin += int64_t(__builtin_amdgcn_readlane(in, 63)) * units;
+    seq_begin += int64_t(readlane(in, 63)) * units1;
   }
 
   while (item < end && seq < a.kv.seqs) {
-    const SeqSpan sp = seq_span(a, seq < 64 ? __builtin_amdgcn_readlane(len0, seq) : a.kv.lens[seq]);
+    const Queries qs = queries_of<FEW>(work, seq);
+    const SeqSpan sp = seq_span(a, seq < 64 ? __builtin_amdgcn_readlane(len0, seq) : a.kv.lens[seq], qs.count);
+    const int units = units_of(qs.count);
     const int64_t in_seq = item - seq_begin;
     if (in_seq >= int64_t(sp.tiles) * units) {
       seq_begin += int64_t(sp.tiles) * units;
@@ -231,9 +302,19 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
     const int t1 = int(min(int64_t(sp.tiles), end - unit_begin));
     item += t1 - t0;
 
+    const int blocks_per_head = units / a.kv.heads;
     const int head = unit / blocks_per_head;
-    const int row0 = (unit % blocks_per_head) * kRows;
-    const int rows = min(a.group - row0, kRows);
+    const int unit_row = (unit % blocks_per_head) * kRows;
+    const int rows = min(qs.count * a.group - unit_row, kRows);
+    // this lane's row: its token and head of the group, and its position
+    const int row = unit_row + min(c, rows - 1);
+    const int tok = FEW ? work.group.div(row) : 0;
+    const int in_group = row - tok * a.group;
+    const int past = sp.len - qs.count;
+    const int pos = past + tok;
+    // positions of the unit's first and last row
+    const int pos_min = past + (FEW ? work.group.div(unit_row) : 0);
+    const int pos_max = past + (FEW ? work.group.div(unit_row + rows - 1) : 0);
     const float cs = a.scale_log2 * (E == 1 && a.kv.k_scale ? a.kv.k_scale[head] : 1.0f);
     const int32_t* table = a.kv.tables + seq * a.kv.table_stride;
     const uint8_t* kbase = static_cast<const uint8_t*>(a.kv.k) + head * a.kv.head_stride * E;
@@ -243,8 +324,8 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
     // query operand: row c, zero past the unit's rows
     at_u32x4 q[kSteps];
     {
-      const uint16_t* qp = static_cast<const uint16_t*>(a.q) + seq * a.q_row +
-                           (int64_t(head) * a.group + row0 + min(c, rows - 1)) * a.q_head;
+      const int at = FEW ? min(max(qs.first + tok, 0), work.tokens - 1) : seq;
+      const uint16_t* qp = static_cast<const uint16_t*>(a.q) + at * a.q_row + (int64_t(head) * a.group + in_group) * a.q_head;
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) {
         q[j] = *reinterpret_cast<const at_u32x4*>(qp + TileT::key_dim(j, g));
@@ -254,7 +335,7 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
 
     at_f32x4 o[kBlocks];
     float m, l;
-    bool bad = sp.over, both = true;      // both: the weights' second parts are used
+    bool bad = sp.over, odd = false;      // odd: the second time, for Inf and NaN among the values
 
     // first token of this wave's part of tile t, and the end of its range
     auto tile_at = [&](int t, int* stop) {
@@ -262,7 +343,12 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
       *stop = sink ? sp.sink_end : sp.len;
       return (sink ? t * kTile : sp.start + (t - sp.sink_tiles) * kTile) + wave * 32;
     };
+    // whether any row of the sequence sees token t, and whether this lane's does
     auto seen = [&](int t, int stop) { return t < stop && (t >= sp.low || t < a.sinks); };
+    auto sees = [&](int t, int stop) {
+      if (!FEW) return seen(t, stop);
+      return t < stop && t <= pos && (!a.window || t > pos - a.window || t < a.sinks);
+    };
     // Tokens past the end of the range take the place of its last one (last 8
     // tokens).  Only reads the table: what it gave is looked at in load(), an
     // iteration later.
@@ -321,19 +407,23 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
       float p[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = s[i >> 2][i & 3] * cs;
-      if (!(base + 32 <= stop && (base >= sp.low || base + 32 <= a.sinks))) {
+      const bool whole = FEW ? base + 32 <= min(stop, pos_min + 1) &&
+                                   (!a.window || base > pos_max - a.window || base + 32 <= a.sinks)
+                             : base + 32 <= stop && (base >= sp.low || base + 32 <= a.sinks);
+      if (!whole) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (!seen(base + 8 * g + i, stop)) {
-            p[i] = kNegInf;
-            x.clear_v(i);      // 0 x Inf and 0 x NaN would reach the sum
-          }
+        for (int i = 0; i < 8; ++i) {
+          if (!sees(base + 8 * g + i, stop)) p[i] = kNegInf;
+          if (!seen(base + 8 * g + i, stop)) x.clear_v(i);      // 0 x Inf and 0 x NaN would reach the sum
+        }
       }
       float mx = p[0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) mx = fmaxf(mx, p[i]);
       mx = max_xor32(max_xor16(mx));
-      if (__any(mx > m)) {
+      // The sums are rebased only where a maximum has grown by more than 2^8: until
+      // then weights go up to 2^8, which costs neither type any accuracy.
+      if (__any(mx > m + 8.0f)) {
         const float mn = fmaxf(m, mx), f = rebase(m, mn);
 #pragma unroll
         for (int j = 0; j < kBlocks; ++j) o[j] *= f;
@@ -358,19 +448,27 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
         for (int j = 0; j < kRun; j += 2) {
           at_u32x4 v0, v1;
           x.values(r, j, &v0, &v1);
+          if (odd) {
+            at_u32x4 see;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              see[i] = (sees(base + 8 * g + 2 * i, stop) ? T::kOne : 0) | (sees(base + 8 * g + 2 * i + 1, stop) ? T::kOne << 16 : 0);
+            v0 = add_odd<T>(v0, see, &o[r * kRun + j]);
+            v1 = add_odd<T>(v1, see, &o[r * kRun + j + 1]);
+          }
           o[r * kRun + j] = T::mfma16(v0, hi, o[r * kRun + j]);
           o[r * kRun + j + 1] = T::mfma16(v1, hi, o[r * kRun + j + 1]);
-          if (both) {
-            o[r * kRun + j] = T::mfma16(v0, lo, o[r * kRun + j]);
-            o[r * kRun + j + 1] = T::mfma16(v1, lo, o[r * kRun + j + 1]);
-          }
+          o[r * kRun + j] = T::mfma16(v0, lo, o[r * kRun + j]);
+          o[r * kRun + j + 1] = T::mfma16(v1, lo, o[r * kRun + j + 1]);
         }
     };
 
     // Two tiles in registers: one is computed while the next one's loads (and
     // the table lookups of the one after it) are in flight.  A sum that is not
-    // finite is taken again without the weights' second parts, which may be 0 or
-    // negative: times an Inf that the queries see they would give NaN.
+    // finite is taken again: Inf and NaN among the values then do not enter the
+    // products (a weight's second part may be 0 or negative, and a row that does
+    // not see the token has the weight 0: times Inf that is NaN), but are added to
+    // the rows that see them.
     for (;;) {
 #pragma unroll
       for (int j = 0; j < kBlocks; ++j) o[j] = (at_f32x4){0, 0, 0, 0};
@@ -405,14 +503,13 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
       } else {
         compute(x, t);
       }
-      if (!both) break;
-      bool odd = false;
+      if (odd) break;
 #pragma unroll
       for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) odd |= !(fabsf(o[j][i]) < -kNegInf);
-      if (!__any(odd)) break;
-      both = false;
+      odd = __any(odd);
+      if (!odd) break;
     }
 
     // merge the waves
@@ -431,18 +528,16 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
     }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == sp.tiles;
-    const int64_t u = int64_t(seq) * units + unit;
-    if (t0 == 0 && threadIdx.x == 0) {
+    if (t0 == 0 && !whole && threadIdx.x == 0) {
       const int64_t last = unit_begin + sp.tiles - 1;      // the unit's last item is in workgroup ...
-      work.first[u] = int32_t(wg);
-      work.count[u] = int32_t(((last + 1) * wgs - 1) / total - wg + 1);
+      work.cuts[wg] = {seq, unit, int32_t(((last + 1) * wgs - 1) / total - wg + 1), 0};
     }
     const Partial part = partial_at(work, D, wg, t0 == 0);
     for (int e = threadIdx.x; e < rows * (D / 4); e += 256) {
       const int r = e / (D / 4), d = 4 * (e - r * (D / 4));
-      float M = lds_m[0][r];
+      float M = kNegInf;
 #pragma unroll
-      for (int w = 1; w < 4; ++w) M = fmaxf(M, lds_m[w][r]);
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, lds_m[w][r]);
       float L = 0.0f;
       at_f32x4 O = {0, 0, 0, 0};
 #pragma unroll
@@ -452,14 +547,7 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
         O += *reinterpret_cast<const at_f32x4*>(&lds_o[w][r][d]) * f;
       }
       if (whole) {
-        const int h = head * a.group + row0 + r;
-        const float inv = (E == 1 && a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / L;
-        const bool none = sp.len == 0 && !sp.over;
-        at_u32x2 y = {T::pack(O[0] * inv, O[1] * inv), T::pack(O[2] * inv, O[3] * inv)};
-        if (none) y = (at_u32x2){0, 0};
-        *reinterpret_cast<at_u32x2*>(static_cast<uint16_t*>(a.out) + seq * a.o_row + h * a.o_head + d) = y;
-        if (a.lse && d == 0)
-          a.lse[int64_t(seq) * a.q_heads + h] = none ? kNegInf : (M + __log2f(L)) * 0.693147180559945f;
+        finish<T, D, E, FEW>(a, work, head, qs, sp, unit_row + r, d, M, L, O);
       } else {
         *reinterpret_cast<at_f32x4*>(part.o + r * D + d) = O;
         if (d == 0) {
@@ -472,111 +560,146 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
   }
 }
 
-// Joins the partial results of units that were cut: grid (seqs x units, rows).
+// Joins the partial results of units that were cut: grid (workgroups, row
+// shares), each workgroup the unit that the one of its number has begun, if any.
 // D / 4 threads hold a column quad each, the rest of the 256 share the parts.
-template <class T, int D, int E>
+template <class T, int D, int E, bool FEW>
 __global__ void __launch_bounds__(256) decode_join_kernel(AttnArgs a, Work work) {
   constexpr int kQuads = D / 4, kSplits = 256 / kQuads;
   __shared__ at_f32x4 lds_o[kSplits][kQuads];
   __shared__ float lds_m[kSplits], lds_l[kSplits];
-  const int n = work.count[blockIdx.x];
-  if (n <= 1) return;
-  const int blocks_per_head = (a.group + kRows - 1) / kRows;
-  const int units = a.kv.heads * blocks_per_head;
-  const int seq = blockIdx.x / units, unit = blockIdx.x % units;
-  const int head = unit / blocks_per_head, row0 = (unit % blocks_per_head) * kRows;
-  const int r = blockIdx.y;
-  if (r >= min(a.group - row0, kRows)) return;
-  const int first = work.first[blockIdx.x];
+  const Cut cut = work.cuts[blockIdx.x];
+  if (cut.count <= 1) return;
+  const Queries qs = queries_of<FEW>(work, cut.seq);
+  const SeqSpan sp = seq_span(a, a.kv.lens[cut.seq], qs.count);
+  const int blocks_per_head = (qs.count * a.group + kRows - 1) / kRows;
+  const int head = cut.unit / blocks_per_head, unit_row = (cut.unit % blocks_per_head) * kRows;
+  const int rows = min(qs.count * a.group - unit_row, kRows);
   const int quad = threadIdx.x % kQuads, split = threadIdx.x / kQuads;
-  float M = kNegInf, L = 0.0f;
-  at_f32x4 O = {0, 0, 0, 0};
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    float M = kNegInf, L = 0.0f;
+    at_f32x4 O = {0, 0, 0, 0};
 #pragma unroll 4
-  for (int i = split; i < n; i += kSplits) {
-    const Partial p = partial_at(work, D, first + i, i == 0);
-    const float m = p.m[r], l = p.l[r];
-    const at_f32x4 o = *reinterpret_cast<const at_f32x4*>(p.o + r * D + 4 * quad);
-    const float mn = fmaxf(M, m), f = rebase(M, mn), h = rebase(m, mn);
-    L = L * f + l * h;
-    O = O * f + o * h;
-    M = mn;
+    for (int i = split; i < cut.count; i += kSplits) {
+      const Partial p = partial_at(work, D, blockIdx.x + i, i == 0);
+      const float m = p.m[r], l = p.l[r];
+      const at_f32x4 o = *reinterpret_cast<const at_f32x4*>(p.o + r * D + 4 * quad);
+      const float mn = fmaxf(M, m), f = rebase(M, mn), h = rebase(m, mn);
+      L = L * f + l * h;
+      O = O * f + o * h;
+      M = mn;
+    }
+    __syncthreads();              // the row before has been read
+    lds_o[split][quad] = O;
+    if (quad == 0) {
+      lds_m[split] = M;
+      lds_l[split] = L;
+    }
+    __syncthreads();
+    if (split) continue;
+    M = lds_m[0];
+    for (int i = 1; i < kSplits; ++i) M = fmaxf(M, lds_m[i]);
+    L = 0.0f;
+    O = (at_f32x4){0, 0, 0, 0};
+    for (int i = 0; i < kSplits; ++i) {
+      const float f = rebase(lds_m[i], M);
+      L += f * lds_l[i];
+      O += lds_o[i][quad] * f;
+    }
+    finish<T, D, E, FEW>(a, work, head, qs, sp, unit_row + r, 4 * quad, M, L, O);
   }
-  lds_o[split][quad] = O;
-  if (quad == 0) {
-    lds_m[split] = M;
-    lds_l[split] = L;
-  }
-  __syncthreads();
-  if (split) return;
-  M = lds_m[0];
-  for (int i = 1; i < kSplits; ++i) M = fmaxf(M, lds_m[i]);
-  L = 0.0f;
-  O = (at_f32x4){0, 0, 0, 0};
-  for (int i = 0; i < kSplits; ++i) {
-    const float f = rebase(lds_m[i], M);
-    L += f * lds_l[i];
-    O += lds_o[i][quad] * f;
-  }
-  const int h = head * a.group + row0 + r;
-  const float inv = (E == 1 && a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / L;
-  const at_u32x2 y = {T::pack(O[0] * inv, O[1] * inv), T::pack(O[2] * inv, O[3] * inv)};
-  *reinterpret_cast<at_u32x2*>(static_cast<uint16_t*>(a.out) + seq * a.o_row + h * a.o_head + 4 * quad) = y;
-  if (a.lse && quad == 0) a.lse[int64_t(seq) * a.q_heads + h] = (M + __log2f(L)) * 0.693147180559945f;
 }
 
 // Workgroups of a full card.
 int full_card(int D, int E, bool oct) { return 256 * wgs_per_cu(D, E, oct); }
 constexpr int kMaxWgs = 256 * 3;
 
-template <class T, int D, int E>
-hipError_t launch(const AttnArgs& a, const Work& w, int64_t tiles, int64_t units, hipStream_t stream) {
-  const bool oct = a.kv.page.d % 8 == 0;
-  const unsigned grid = unsigned(std::min<int64_t>(full_card(D, E, oct), tiles));
-  if (oct)
-    decode_kernel<T, D, E, true><<<grid, 256, 0, stream>>>(a, w);
-  else
-    decode_kernel<T, D, E, false><<<grid, 256, 0, stream>>>(a, w);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  decode_join_kernel<T, D, E><<<dim3(unsigned(units), unsigned(w.rows)), 256, 0, stream>>>(a, w);
-  return hipGetLastError();
-}
-
-template <class T, int E>
-hipError_t launch_dim(const AttnArgs& a, const Work& w, int D, int64_t tiles, int64_t units, hipStream_t stream) {
-  if (D == 64) return launch<T, 64, E>(a, w, tiles, units, stream);
-  if (D == 128) return launch<T, 128, E>(a, w, tiles, units, stream);
-  return launch<T, 256, E>(a, w, tiles, units, stream);
-}
-
 int64_t all_units(int64_t seqs, int q_heads, int heads) {
   return seqs * heads * ((q_heads / heads + kRows - 1) / kRows);
 }
 
+size_t workspace_bytes(int rows, int D, int wgs) {
+  return size_t(wgs) * (2 * size_t(partial_floats(rows, D)) * 4 + sizeof(Cut));
+}
+
+// [parts] [cuts]
+Work work_at(void* workspace, int rows, int D, int wgs) {
+  Work w;
+  w.rows = rows;
+  w.parts = static_cast<float*>(workspace);
+  w.cuts = reinterpret_cast<Cut*>(w.parts + size_t(wgs) * 2 * partial_floats(rows, D));
+  w.cu = nullptr;
+  w.tokens = 0;
+  w.group = fast_div(1);
+  return w;
+}
+
+template <class T, int D, int E, bool OCT, bool FEW>
+hipError_t launch_kernels(const AttnArgs& a, const Work& w, unsigned grid, hipStream_t stream) {
+  decode_kernel<T, D, E, OCT, FEW><<<grid, 256, 0, stream>>>(a, w);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  decode_join_kernel<T, D, E, FEW><<<dim3(grid, unsigned(w.rows)), 256, 0, stream>>>(a, w);
+  return hipGetLastError();
+}
+
+template <class T, int D, int E>
+hipError_t launch(const AttnArgs& a, const int32_t* cu, int64_t tokens, void* workspace, hipStream_t stream) {
+  const bool oct = a.kv.page.d % 8 == 0;
+  const int wgs = full_card(D, E, oct);
+  Work w = work_at(workspace, cu ? kRows : std::min(a.group, kRows), D, wgs);
+  w.cu = cu;
+  w.tokens = int(tokens);
+  w.group = fast_div(uint32_t(a.group));
+  // no more workgroups than tiles that the tables can hold
+  const int64_t units = cu ? a.kv.heads * (tokens * a.group / kRows + a.kv.seqs) : all_units(a.kv.seqs, a.q_heads, a.kv.heads);
+  const int64_t tiles = (int64_t(a.kv.max_pages) * a.kv.page.d + kTile - 1) / kTile + 2;
+  const unsigned grid = unsigned(std::min<int64_t>(wgs, units * tiles));
+  if (cu) return launch_kernels<T, D, E, true, true>(a, w, grid, stream);
+  return oct ? launch_kernels<T, D, E, true, false>(a, w, grid, stream)
+             : launch_kernels<T, D, E, false, false>(a, w, grid, stream);
+}
+
+template <class T, int E>
+hipError_t launch_dim(const AttnArgs& a, const int32_t* cu, int64_t tokens, int D, void* workspace, hipStream_t stream) {
+  if (D == 64) return launch<T, 64, E>(a, cu, tokens, workspace, stream);
+  if (D == 128) return launch<T, 128, E>(a, cu, tokens, workspace, stream);
+  return launch<T, 256, E>(a, cu, tokens, workspace, stream);
+}
+
+hipError_t launch_any(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype, int D,
+                      void* workspace, hipStream_t stream) {
+  const bool e4m3 = cache_dtype == W4A4_E4M3;
+  if (dtype == W4A4_BF16)
+    return e4m3 ? launch_dim<Bf16, 1>(a, cu, tokens, D, workspace, stream)
+                : launch_dim<Bf16, 2>(a, cu, tokens, D, workspace, stream);
+  return e4m3 ? launch_dim<F16, 1>(a, cu, tokens, D, workspace, stream)
+              : launch_dim<F16, 2>(a, cu, tokens, D, workspace, stream);
+}
+
 }  // namespace
 
-// [parts] [first] [count]
-size_t attn_decode_workspace(int64_t seqs, int q_heads, int heads, int head_dim) {
-  const int rows = std::min(q_heads / heads, kRows);
-  return size_t(kMaxWgs) * 2 * partial_floats(rows, head_dim) * 4 + size_t(all_units(seqs, q_heads, heads)) * 8;
+size_t attn_decode_workspace(int q_heads, int heads, int head_dim) {
+  return workspace_bytes(std::min(q_heads / heads, kRows), head_dim, kMaxWgs);
 }
 
 hipError_t launch_attn_decode(const AttnArgs& a, int cache_dtype, int dtype, int head_dim, void* workspace,
                               hipStream_t stream) {
-  const int64_t units = all_units(a.kv.seqs, a.q_heads, a.kv.heads);
-  Work w;
-  w.rows = std::min(a.group, kRows);
-  w.parts = static_cast<float*>(workspace);
-  w.first = reinterpret_cast<int32_t*>(w.parts + size_t(kMaxWgs) * 2 * partial_floats(w.rows, head_dim));
-  w.count = w.first + units;
-  // no more workgroups than tiles that the tables can hold
-  const int64_t tiles = units * ((int64_t(a.kv.max_pages) * a.kv.page.d + kTile - 1) / kTile + 2);
-  const bool e4m3 = cache_dtype == W4A4_E4M3;
-  if (dtype == W4A4_BF16)
-    return e4m3 ? launch_dim<Bf16, 1>(a, w, head_dim, tiles, units, stream)
-                : launch_dim<Bf16, 2>(a, w, head_dim, tiles, units, stream);
-  return e4m3 ? launch_dim<F16, 1>(a, w, head_dim, tiles, units, stream)
-              : launch_dim<F16, 2>(a, w, head_dim, tiles, units, stream);
+  return launch_any(a, nullptr, a.kv.seqs, cache_dtype, dtype, head_dim, workspace, stream);
+}
+
+// Up to 16 rows of a kv head per sequence, on average: one unit, as in decoding.
+// More rows would read the keys once per 16; the row tiles of attn_prefill read
+// them once.
+bool attn_few_serves(int64_t seqs, int64_t tokens, int group, int page_size) {
+  return page_size % 8 == 0 && tokens * group <= seqs * kRows;
+}
+
+size_t attn_few_workspace(int head_dim) { return workspace_bytes(kRows, head_dim, kMaxWgs); }
+
+hipError_t launch_attn_few(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype,
+                           int head_dim, void* workspace, hipStream_t stream) {
+  return launch_any(a, cu, tokens, cache_dtype, dtype, head_dim, workspace, stream);
 }
 
 }  // namespace w4a4

@@ -720,7 +720,9 @@ hipError_t launch_dim(const AttnArgs& a, const PrefillWork& w, int D, hipStream_
 }  // namespace
 
 // [parts] [used]
-size_t attn_prefill_workspace(int64_t seqs, int64_t tokens, int q_heads, int heads, int head_dim) {
+size_t attn_prefill_workspace(int64_t seqs, int64_t tokens, int q_heads, int heads, int head_dim, int page_size) {
+  if (attn_few_serves(seqs, tokens, q_heads / heads, page_size))
+    return attn_few_workspace(head_dim);
   const int64_t tiles = row_tiles(seqs, tokens, q_heads / heads);
   const int splits = key_splits(tiles, heads);
   if (splits == 1) return 0;
@@ -729,6 +731,8 @@ size_t attn_prefill_workspace(int64_t seqs, int64_t tokens, int q_heads, int hea
 
 hipError_t launch_attn_prefill(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype,
                                int head_dim, void* workspace, hipStream_t stream) {
+  if (attn_few_serves(a.kv.seqs, tokens, a.group, int(a.kv.page.d)))
+    return launch_attn_few(a, cu, tokens, cache_dtype, dtype, head_dim, workspace, stream);
   PrefillWork w;
   w.cu = cu;
   w.tokens = int32_t(tokens);

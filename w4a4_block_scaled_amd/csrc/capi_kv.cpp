@@ -195,7 +195,7 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs,
 
 size_t w4a4_attn_decode_workspace_bytes(const w4a4_kv_cache* cache, int64_t seqs, int q_heads) {
   if (check_cache("attn_decode_workspace_bytes", cache) != W4A4_OK || !heads_ok(cache, q_heads) || seqs <= 0) return 0;
-  return w4a4::attn_decode_workspace(seqs, q_heads, cache->heads, cache->head_dim);
+  return w4a4::attn_decode_workspace(q_heads, cache->heads, cache->head_dim);
 }
 
 w4a4_status w4a4_attn_decode(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, w4a4_dtype dtype, int q_heads,
@@ -207,7 +207,7 @@ w4a4_status w4a4_attn_decode(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seq
   if (st == W4A4_OK) st = check_seqs(what, seqs, true);
   if (st != W4A4_OK) return st;
   const size_t need = seqs->seqs > 0 && heads_ok(cache, q_heads)
-                          ? w4a4::attn_decode_workspace(seqs->seqs, q_heads, cache->heads, cache->head_dim) : 0;
+                          ? w4a4::attn_decode_workspace(q_heads, cache->heads, cache->head_dim) : 0;
   st = check_attn(what, cache, seqs, dtype, q_heads, seqs->seqs, q, q_row, q_head, scale, window, sinks, out, o_row,
                   o_head, lse, workspace, ws_bytes, need);
   if (st != W4A4_OK) return st;
@@ -223,7 +223,7 @@ size_t w4a4_attn_prefill_workspace_bytes(const w4a4_kv_cache* cache, int64_t seq
   if (check_cache("attn_prefill_workspace_bytes", cache) != W4A4_OK || !heads_ok(cache, q_heads) || seqs <= 0 ||
       tokens <= 0 || tokens * q_heads >= kMaxIndex)
     return 0;
-  return w4a4::attn_prefill_workspace(seqs, tokens, q_heads, cache->heads, cache->head_dim);
+  return w4a4::attn_prefill_workspace(seqs, tokens, q_heads, cache->heads, cache->head_dim, cache->page_size);
 }
 
 w4a4_status w4a4_attn_prefill(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, const int32_t* cu, int64_t tokens,

@@ -69,11 +69,17 @@ hipError_t launch_kv_append(const KvView& kv, int dtype, int head_dim, const int
                             const void* k, int64_t k_row, int64_t k_head, const void* v, int64_t v_row, int64_t v_head,
                             hipStream_t stream);
 
-size_t attn_decode_workspace(int64_t seqs, int q_heads, int heads, int head_dim);
+size_t attn_decode_workspace(int q_heads, int heads, int head_dim);
 hipError_t launch_attn_decode(const AttnArgs& a, int cache_dtype, int dtype, int head_dim, void* workspace,
                               hipStream_t stream);
 
-size_t attn_prefill_workspace(int64_t seqs, int64_t tokens, int q_heads, int heads, int head_dim);
+// The same kernel for several queries per sequence, where there are few of them.
+bool attn_few_serves(int64_t seqs, int64_t tokens, int group, int page_size);
+size_t attn_few_workspace(int head_dim);
+hipError_t launch_attn_few(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype,
+                           int head_dim, void* workspace, hipStream_t stream);
+
+size_t attn_prefill_workspace(int64_t seqs, int64_t tokens, int q_heads, int heads, int head_dim, int page_size);
 hipError_t launch_attn_prefill(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype,
                                int head_dim, void* workspace, hipStream_t stream);
 
