@@ -165,8 +165,20 @@ struct Rows {
 
 // ------------------------------------------------------------------ kernel --
 
-// Workgroups that share a CU: what the registers of two tiles leave room for.
-constexpr int wgs_per_cu(int D, int E, bool oct) { return D == 256 ? 1 : oct && D == 64 ? 3 : 2; }
+// Whether a wave holds two tiles in registers or one, and the workgroups that
+// then share a CU.  One tile is enough to keep the memory busy where its bytes
+// are few or the rows' addresses take the registers; two gain where a tile is
+// large.  Microseconds on 4 to 6 thousand cached tokens each of 32 sequences,
+// one tile / two: bf16, D=128 (the ragged batch) 162.3 / 158.2; E4M3, D=128
+// 65.5 / 65.0, D=64 85.3 / 90.6, D=256 115.9 / 120.6; token by token (!OCT),
+// bf16, D=128 90.7 / 175.3, D=64 108.6 / 124.0 (two tiles spill).  Workgroups,
+// for one tile: E4M3, D=64 4 / 3: 79.5 / 85.3, D=256 2 / 1: 94.8 / 115.9,
+// D=128 3 / 2 (the long cache): 87.3 / 76.8.
+constexpr bool two_tiles(int D, int E, bool oct) { return oct && E == 2 && D < 256; }
+constexpr int wgs_per_cu(int D, int E, bool oct) {
+  if (D == 256) return oct && E == 1 ? 2 : 1;
+  return oct && D == 64 ? (E == 1 ? 4 : 3) : 2;
+}
 
 // A sequence's queries: the rows of one kv head are count * group, token by token.
 struct Queries {
@@ -227,6 +239,7 @@ __device__ __forceinline__ at_u32x4 add_odd(at_u32x4 v, at_u32x4 see, at_f32x4* 
 template <class T, int D, int E, bool OCT, bool FEW>
 __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(AttnArgs a, Work work) {
   typedef Tile<T, D, E> TileT;
+  constexpr bool TWO = two_tiles(D, E, OCT);
   constexpr int kSteps = TileT::kSteps, kRun = TileT::kRun, kRuns = TileT::kRuns;
   constexpr int kBlocks = D / 16;                        // MFMAs of the value product
   typedef std::conditional_t<FEW, int64_t, int> Sum;     // of tiles (FEW: times units) of 64 sequences
@@ -373,13 +386,13 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
     };
     // An entry outside the cache is read as page 0, and spoils the result if a
     // query sees a token there (the keys' entries are the values').
-    auto load = [&](TileT& x, const Rows<OCT>& r, int t) {
+    auto row_at = [&](const Rows<OCT>& r, int i) -> int64_t {
+      const int p = uint32_t(r.page[i]) < uint32_t(a.kv.pages) ? r.page[i] : 0;
+      return (int64_t(p) * a.kv.page_stride + int64_t(r.slot[i]) * a.kv.token_stride) * E;
+    };
+    auto load_keys = [&](TileT& x, const Rows<OCT>& r, int t) {
       int stop;
       const int base = tile_at(t, &stop);
-      auto row = [&](int i) -> int64_t {
-        const int p = uint32_t(r.page[i]) < uint32_t(a.kv.pages) ? r.page[i] : 0;
-        return (int64_t(p) * a.kv.page_stride + int64_t(r.slot[i]) * a.kv.token_stride) * E;
-      };
       if constexpr (OCT) {
         const int kt = base + 8 * (c >> 2);
         bad |= uint32_t(r.page[0]) >= uint32_t(a.kv.pages) && kt < stop &&
@@ -389,21 +402,35 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
         for (int b = 0; b < 2; ++b)
           bad |= uint32_t(r.page[b]) >= uint32_t(a.kv.pages) && seen(base + 8 * (c >> 2) + 4 * b + (c & 3), stop);
       }
-      const int64_t k0 = row(0), v0 = row(OCT ? 1 : 2);
+      const int64_t k0 = row_at(r, 0);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) x.load_k(b, kbase + (OCT ? k0 + (4 * b + (c & 3)) * step : b ? row(1) : k0), g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x.load_v(i, vbase + (OCT ? v0 + i * step : i ? row(OCT ? 1 : 2 + i) : v0), c);
+      for (int b = 0; b < 2; ++b) x.load_k(b, kbase + (OCT ? k0 + (4 * b + (c & 3)) * step : b ? row_at(r, 1) : k0), g);
     };
-    auto compute = [&](TileT& x, int t) {
+    auto load_values = [&](TileT& x, const Rows<OCT>& r) {
+      const int64_t v0 = row_at(r, OCT ? 1 : 2);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x.load_v(i, vbase + (OCT ? v0 + i * step : i ? row_at(r, OCT ? 1 : 2 + i) : v0), c);
+    };
+    auto load = [&](TileT& x, const Rows<OCT>& r, int t) {
+      load_keys(x, r, t);
+      load_values(x, r);
+    };
+    // `keys_done` and `values_done` run where the tile's keys and values are no
+    // longer needed.
+    auto compute = [&](TileT& x, int t, auto keys_done, auto values_done) {
       int stop;
       const int base = tile_at(t, &stop);
-      if (base >= stop) return;
+      if (base >= stop) {
+        keys_done();
+        values_done();
+        return;
+      }
       at_f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
       for (int j = 0; j < kSteps; ++j)
 #pragma unroll
         for (int b = 0; b < 2; ++b) s[b] = T::mfma16(x.key(b, j), q[j], s[b]);
+      keys_done();
       float p[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = s[i >> 2][i & 3] * cs;
@@ -461,7 +488,9 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
           o[r * kRun + j] = T::mfma16(v0, lo, o[r * kRun + j]);
           o[r * kRun + j + 1] = T::mfma16(v1, lo, o[r * kRun + j + 1]);
         }
+      values_done();
     };
+    auto nothing = [] {};
 
     // Two tiles in registers: one is computed while the next one's loads (and
     // the table lookups of the one after it) are in flight.  A sum that is not
@@ -477,31 +506,47 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
       // No load depends on a condition inside the loop, and a tile's table
       // entries are read before the loads of the tile ahead of it: loads come
       // back in order, and waiting for either leaves the later ones in flight.
-      TileT x, y;
-      Rows<OCT> r, n;
-      auto at = [&](int t) { return min(t, t1 - 1); };
-      find(r, t0);
-      find(n, at(t0 + 1));
-      load(x, r, t0);
-      int t = t0;
-      for (; t + 2 < t1; t += 2) {
-        find(r, t + 2);
-        load(y, n, t + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(x, t);
-        __builtin_amdgcn_sched_barrier(0);
-        find(n, at(t + 3));
-        load(x, r, t + 2);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(y, t + 1);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (t + 1 < t1) {
-        load(y, n, t + 1);
-        compute(x, t);
-        compute(y, t + 1);
+      if constexpr (TWO) {
+        TileT x, y;
+        Rows<OCT> r, n;
+        auto at = [&](int t) { return min(t, t1 - 1); };
+        find(r, t0);
+        find(n, at(t0 + 1));
+        load(x, r, t0);
+        int t = t0;
+        for (; t + 2 < t1; t += 2) {
+          find(r, t + 2);
+          load(y, n, t + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          compute(x, t, nothing, nothing);
+          __builtin_amdgcn_sched_barrier(0);
+          find(n, at(t + 3));
+          load(x, r, t + 2);
+          __builtin_amdgcn_sched_barrier(0);
+          compute(y, t + 1, nothing, nothing);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (t + 1 < t1) {
+          load(y, n, t + 1);
+          compute(x, t, nothing, nothing);
+          compute(y, t + 1, nothing, nothing);
+        } else {
+          compute(x, t, nothing, nothing);
+        }
       } else {
-        compute(x, t);
+        // one tile: its keys make way for the next one's after the scores, its
+        // values after the sums
+        TileT x;
+        Rows<OCT> r;
+        find(r, t0);
+        load(x, r, t0);
+        for (int t = t0; t + 1 < t1; ++t) {
+          find(r, t + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          compute(x, t, [&] { load_keys(x, r, t + 1); }, [&] { load_values(x, r); });
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        compute(x, t1 - 1, nothing, nothing);
       }
       if (odd) break;
 #pragma unroll
