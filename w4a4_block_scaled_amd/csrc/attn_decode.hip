@@ -179,6 +179,7 @@ constexpr int wgs_per_cu(int D, int E, bool oct) {
   if (D == 256) return oct && E == 1 ? 2 : 1;
   return oct && D == 64 ? (E == 1 ? 4 : 3) : 2;
 }
+constexpr int kMaxPerCu = 4;     // the workspaces' size
 
 // A sequence's queries: the rows of one kv head are count * group, token by token.
 struct Queries {
@@ -240,6 +241,7 @@ template <class T, int D, int E, bool OCT, bool FEW>
 __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(AttnArgs a, Work work) {
   typedef Tile<T, D, E> TileT;
   constexpr bool TWO = two_tiles(D, E, OCT);
+  static_assert(wgs_per_cu(D, E, OCT) <= kMaxPerCu);
   constexpr int kSteps = TileT::kSteps, kRun = TileT::kRun, kRuns = TileT::kRuns;
   constexpr int kBlocks = D / 16;                        // MFMAs of the value product
   typedef std::conditional_t<FEW, int64_t, int> Sum;     // of tiles (FEW: times units) of 64 sequences
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(256) decode_join_kernel(AttnArgs a, Work work)
 
 // Workgroups of a full card.
 int full_card(int D, int E, bool oct) { return 256 * wgs_per_cu(D, E, oct); }
-constexpr int kMaxWgs = 256 * 3;
+constexpr int kMaxWgs = 256 * kMaxPerCu;
 
 int64_t all_units(int64_t seqs, int q_heads, int heads) {
   return seqs * heads * ((q_heads / heads + kRows - 1) / kRows);
