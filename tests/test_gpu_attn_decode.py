@@ -106,6 +106,18 @@ def test_decode_many_sequences():
     check(c, y, lse, label="many", rows=range(0, 150, 7))
 
 
+@pytest.mark.parametrize("kind,kv,dim,page,seqs,high", [("fp16", 24, 64, 16, 140, 500), ("fp8", 32, 64, 16, 150, 600),
+                                                        ("bf16", 8, 256, 11, 100, 800)])
+def test_decode_many_units_per_workgroup(kind, kv, dim, page, seqs, high):
+    """So many units that every workgroup takes several, with empty and short
+    sequences between long ones."""
+    say(f"[decode] {seqs} sequences of up to {high} tokens, {kv} heads of {dim}")
+    lens = [0 if i % 13 == 5 else 1 + (101 * i) % 40 if i % 4 == 1 else (173 * i) % high for i in range(seqs)]
+    c = make(kind, kv, 1, dim, page, lens, seed=seqs)
+    y, lse = run(c)
+    check(c, y, lse, label="many units", rows=range(0, seqs, 5))
+
+
 @pytest.mark.parametrize("order", list(ORDERS))
 def test_decode_memory_orders(order):
     say(f"[decode] cache order {order}")

@@ -179,6 +179,13 @@ constexpr int wgs_per_cu(int D, int E, bool oct) {
   if (D == 256) return oct && E == 1 ? 2 : 1;
   return oct && D == 64 ? (E == 1 ? 4 : 3) : 2;
 }
+
+// Tiles that beginning a unit counts as, where a workgroup has 8 tiles or more:
+// with 0 the pieces of short sequences, of many units each, end last.  0 / 1 / 2
+// on 32 sequences of 100 to 6000 tokens: E4M3, D=128 66.5 / 53.1 / 53.4 us,
+// bf16, D=256 157.9 / 147.2 / 148.7; on equal lengths of 3050, 53.6 / 54.8 for
+// 0 / 2; the ragged batch 158.9 / 157.5 / 160.1.
+constexpr int kStart = 1;
 constexpr int kMaxPerCu = 4;     // the workspaces' size
 
 // A sequence's queries: the rows of one kv head are count * group, token by token.
@@ -278,7 +285,9 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
   const Sum mine0 = share_of(lane, len0), in0 = scan(mine0);
   int64_t total = readlane(in0, 63);
   for (int base = 64; base < a.kv.seqs; base += 64) total += readlane(scan(share_of(base + lane, length(base + lane))), 63);
-  total *= units1;
+  // a unit's first tiles stand for the cost of beginning it, and hold no tokens
+  const int extra = !FEW && total * units1 >= 8 * int64_t(gridDim.x) ? kStart : 0;
+  total = (total + int64_t(extra) * (FEW ? 0 : a.kv.seqs)) * units1;
   const int64_t wgs = min(int64_t(gridDim.x), total);
   if (wg >= wgs) return;
   int64_t item = wg * total / wgs;
@@ -291,14 +300,14 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
       mine = share_of(base + lane, length(base + lane));
       in = scan(mine);
     }
-    const uint64_t past = __ballot(seq_begin + int64_t(in) * units1 > item);
+    const uint64_t past = __ballot(seq_begin + (int64_t(in) + extra * (lane + 1)) * units1 > item);
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
       seq = base + l;
-      seq_begin += int64_t(readlane(Sum(in - mine), l)) * units1;
+      seq_begin += (int64_t(readlane(Sum(in - mine), l)) + extra * l) * units1;
       break;
     }
-    seq_begin += int64_t(readlane(in, 63)) * units1;
+    seq_begin += (int64_t(readlane(in, 63)) + extra * 64) * units1;
   }
 
   while (item < end && seq < a.kv.seqs) {
@@ -306,16 +315,18 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
     const SeqSpan sp = seq_span(a, seq < 64 ? __builtin_amdgcn_readlane(len0, seq) : a.kv.lens[seq], qs.count);
     const int units = units_of(qs.count);
     const int64_t in_seq = item - seq_begin;
-    if (in_seq >= int64_t(sp.tiles) * units) {
-      seq_begin += int64_t(sp.tiles) * units;
+    const int places = sp.tiles + extra;
+    if (in_seq >= int64_t(places) * units) {
+      seq_begin += int64_t(places) * units;
       ++seq;
       continue;
     }
-    const int unit = int(in_seq / sp.tiles);
-    const int64_t unit_begin = seq_begin + int64_t(unit) * sp.tiles;
-    const int t0 = int(item - unit_begin);
+    const int unit = int(in_seq / places);
+    const int64_t unit_begin = seq_begin + int64_t(unit) * places + extra;    // of its tiles
+    const int t0 = int(max(item - unit_begin, int64_t(0)));
     const int t1 = int(min(int64_t(sp.tiles), end - unit_begin));
-    item += t1 - t0;
+    item = unit_begin + t1;
+    if (t1 <= t0) continue;
 
     const int blocks_per_head = units / a.kv.heads;
     const int head = unit / blocks_per_head;
