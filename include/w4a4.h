@@ -497,8 +497,10 @@ w4a4_status w4a4_attn_decode(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seq
  * cu[s+1]-1 of q, at positions lens[s] - count .. lens[s] - 1; cu, tokens as in
  * w4a4_kv_append (cu must not be NULL).  A query at a negative position sees
  * nothing.  lse is fp32 [tokens x q_heads].  Where the rows are too few to fill the
- * card the keys are split as well.  The softmax weights are rounded to `dtype`
- * for the matrix cores; statistics and sums are fp32.
+ * card and the tables can hold long sequences, the keys are split as well.  The
+ * softmax weights are rounded to `dtype` for the matrix cores, in two parts
+ * (about 16 bits) where the keys are split or a kv head has up to 16 rows per
+ * sequence, else in one; statistics and sums are fp32.
  */
 size_t w4a4_attn_prefill_workspace_bytes(const w4a4_kv_cache* cache, int64_t seqs, int64_t tokens, int q_heads);
 w4a4_status w4a4_attn_prefill(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, const int32_t* cu,

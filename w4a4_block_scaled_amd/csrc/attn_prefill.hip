@@ -14,7 +14,25 @@
 // operand comes from the row-major tile by transposing LDS reads, in the token
 // order that the scores' registers have.
 //
-// The matrix cores bound it: 4 D operations per visible pair.
+// The matrix cores bound it: 4 D operations per visible pair.  Beside them the
+// vector unit has some 16 instructions per 32 x 32 x 16 product to place: a step
+// computes the scores of the next tile and the weighted sum of this one, and
+// between any two MFMAs stands a slice of the softmax, of the masks or of the
+// next copies, held there by scheduling barriers (the two in turn, as written
+// without them: 577 us on the ragged chunks; interleaved 507).  Maxima are
+// rebased only where they grew past 2^8, so the sums are rarely touched.
+// Copies go straight to LDS: by buffer loads, which LDS reads do not wait for.
+//
+// The weights are rounded to 16 bits (with the values' own rounding the error
+// stays below the output's two units; a second part would double the second
+// product).  Where the keys are split the matrix cores are idle, and two parts
+// are taken, as in decoding.
+//
+// Measured, 32 / 8 heads, D = 128, causal 8192 bf16: 518 us, 1.06 PFLOP/s (a
+// library product of 8192^3 reaches 1.44 here; the MFMAs are busy about half of
+// the time, at 1.88 GHz), E4M3 548 us, D = 64 327 us, page 11 (!ONE) 571 us;
+// 4096 at D = 256 338 us.  Ragged chunks over 28 / 4 heads, 526 GFLOP: 491 to
+// 509 us.  82 tokens: 11 us of which the launch is most.
 #include <algorithm>
 #include <type_traits>
 
@@ -685,7 +703,14 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(AttnArgs a, PrefillWo
 int64_t row_tiles(int64_t seqs, int64_t tokens, int group) { return tokens * group / kBM + seqs; }
 
 // Splits of the keys: as many as it takes for two workgroups per CU, where the
-// row tiles alone leave CUs without work.
+// row tiles alone leave CUs without work (5 to 9 rows x 4 heads on 33000 E4M3
+// tokens, not split / split: 611.8 / 74.2 us; 16 tokens of each of 8 sequences
+// on 8000 bf16 tokens 151.7 / 92.4).  Workspace is given for this many; tables that
+// hold kNoSplit tokens at most are not split, since the second launch and the
+// partial results cost what 15 steps of 64 tokens do: split / not split, a
+// prompt of 82 tokens 15.3 / 11.0 us, of 800 34.7 / 22.1, 16 tokens after 700
+// 19.5 / 18.8, after 1000 19.3 / 21.8.
+constexpr int kNoSplit = 1000;
 int key_splits(int64_t tiles, int heads) {
   const int64_t wgs = tiles * heads;
   return wgs >= 256 ? 1 : int(std::min<int64_t>((512 + wgs - 1) / wgs, kMaxSplits));
@@ -737,7 +762,7 @@ hipError_t launch_attn_prefill(const AttnArgs& a, const int32_t* cu, int64_t tok
   w.cu = cu;
   w.tokens = int32_t(tokens);
   w.row_tiles = int32_t(row_tiles(a.kv.seqs, tokens, a.group));
-  w.splits = key_splits(w.row_tiles, a.kv.heads);
+  w.splits = int64_t(a.kv.max_pages) * a.kv.page.d <= kNoSplit ? 1 : key_splits(w.row_tiles, a.kv.heads);
   w.group = fast_div(uint32_t(a.group));
   w.parts = static_cast<float*>(workspace);
   w.used = reinterpret_cast<int32_t*>(w.parts + size_t(w.row_tiles) * a.kv.heads * w.splits * kBM * (head_dim + 2));
