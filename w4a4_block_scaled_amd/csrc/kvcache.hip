@@ -51,6 +51,9 @@ __device__ __forceinline__ float e4m3_range(float x) {
 // at a time and kFlight of them in flight per thread.  MODE 0 copies 16-bit
 // elements, 1 / 2 convert BF16 / FP16 to E4M3 (one IEEE division by the head's
 // scale, one RNE conversion per element).
+//
+// One token each of 16 sequences (0.13 MB): 3.7 us of GPU time, 8.3 with the
+// call: latency of the lookups and the copy behind them.  14400 tokens to E4M3, 44 MB: 14.2 us, 3.1 TB/s.
 constexpr int kMaxTok = 32, kFlight = 4;
 
 template <int MODE>
@@ -195,7 +198,10 @@ struct CompactBook {
 // Moves page src[i] to dst[i], i < pairs (or *count if given), in n arrays.
 // Work items are 16 KiB pieces of a page (4 units of 16 bytes per thread, all
 // loaded before the first store), handed out in a grid-stride loop, since the
-// number of pairs may only be known on the device.
+// number of pairs may only be known on the device.  1.07 GB (read and written)
+// in 212 to 219 us, 4.9 TB/s: a large copy's rate.  The copies of a fork of 4
+// sequences into 32 over 16 layers, 67 MB of which 4 MB are read from HBM: 8.5 to
+// 10 us.
 template <typename UNIT, class BOOK>
 __global__ void __launch_bounds__(256) copy_pages_kernel(Arrays arrays, int n, int64_t stride, int64_t units, int pages,
                                                          const int32_t* __restrict__ src,
@@ -306,7 +312,9 @@ __device__ int64_t lowest_free(const int32_t* refs, int pages, int64_t want, int
 // the last entry its row needs; a row whose walk is long, as a new sequence's,
 // is searched by its wave together), then the free pages are listed and dealt
 // out.  first[s] and off[s] (the row's first missing entry and its place among
-// all missing ones) live in the workspace.
+// all missing ones) live in the workspace.  The order of pages is part of the
+// result, so one workgroup counts; its chain of reads and barriers bounds it:
+// 3.5 us at 32 sequences.
 __global__ void __launch_bounds__(kPlan) reserve_kernel(int32_t* tables, int64_t table_stride,
                                                         const int32_t* __restrict__ lens, int seqs, int max_pages,
                                                         int32_t* refs, int pages, int page_size,
@@ -369,7 +377,8 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(int32_t* tables, int64_t
 }
 
 // One workgroup: which children need a page of their own for the parent's last
-// tokens, and which one.  src / dst get the pages to copy (-1: none).
+// tokens, and which one.  src / dst get the pages to copy (-1: none).  6 us, as
+// reserve_kernel a chain of reads and barriers.
 __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const int32_t* __restrict__ tables, int64_t table_stride,
                                                           int32_t* lens, int seqs, int max_pages, int32_t* refs,
                                                           int pages, int page_size,
@@ -412,7 +421,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const int32_t* __restr
 
 // One workgroup per sequence.  An entry is taken out of the table with an
 // atomic exchange, and only who got it drops the reference, so an id that is
-// listed twice is freed once.
+// listed twice is freed once.  3.1 us for 32 sequences, of which launching is most.
 __global__ void __launch_bounds__(256) free_kernel(int32_t* tables, int64_t table_stride, int32_t* lens, int seqs,
                                                    int max_pages, int32_t* refs, int pages, int page_size,
                                                    const int32_t* __restrict__ ids, int trim, int window, int sinks) {
@@ -436,6 +445,7 @@ __global__ void __launch_bounds__(256) free_kernel(int32_t* tables, int64_t tabl
 
 // One workgroup: counts the pages in use, then lists the free pages below that
 // count and the used ones from there on (equally many), in ascending order.
+// 6.9 us beside the copies' 212.
 __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const int32_t* __restrict__ refs, int pages,
                                                              int32_t* remap, int32_t* src, int32_t* dst,
                                                              int32_t* count) {
@@ -484,11 +494,9 @@ template <int MODE>
 static void append_mode(const AppendArgs& a, hipStream_t stream) {
   int lanes = 16;                                      // a power of two that holds a token's chunks, at most 256
   while (lanes < 256 && lanes < 2 * a.kv.heads * a.head_chunks) lanes *= 2;
-  // one pass of the threads per workgroup until there are four of them per CU,
-  // then up to kFlight passes
-  const int step = 256 / lanes;
-  const int64_t passes = std::min<int64_t>(kFlight, std::max<int64_t>(1, a.tokens / (1024 * step)));
-  const int per_wg = int(std::min<int64_t>(kMaxTok, step * passes));
+  // as many passes as a thread has loads in flight (14400 tokens to E4M3: one
+  // pass 19.2 us, four 15.7; 16 tokens 8.4 and 8.3)
+  const int per_wg = std::min(kMaxTok, 256 / lanes * kFlight);
   append_kernel<MODE><<<unsigned((a.tokens + per_wg - 1) / per_wg), 256, 0, stream>>>(a, lanes, per_wg);
 }
 
