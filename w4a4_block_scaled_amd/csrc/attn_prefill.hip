@@ -15,7 +15,7 @@
 // order that the scores' registers have.
 //
 // The matrix cores bound it: 4 D operations per visible pair.  Beside them the
-// vector unit has some 16 instructions per 32 x 32 x 16 product to place: a step
+// vector unit has some 5 instructions per 32 x 32 x 16 product to place: a step
 // computes the scores of the next tile and the weighted sum of this one, and
 // between any two MFMAs stands a slice of the softmax, of the masks or of the
 // next copies, held there by scheduling barriers (the two in turn, as written
@@ -23,16 +23,16 @@
 // rebased only where they grew past 2^8, so the sums are rarely touched.
 // Copies go straight to LDS: by buffer loads, which LDS reads do not wait for.
 //
-// The weights are rounded to 16 bits (with the values' own rounding the error
-// stays below the output's two units; a second part would double the second
-// product).  Where the keys are split the matrix cores are idle, and two parts
-// are taken, as in decoding.
+// The weights are rounded to 16 bits (bf16: the relative error is 1.9e-3 against
+// 64 bits, of which the output's own rounding is 1.6e-3; a second part would
+// double the second product).  Where the keys are split the matrix cores are
+// idle, and two parts are taken, as in decoding.
 //
-// Measured, 32 / 8 heads, D = 128, causal 8192 bf16: 518 us, 1.06 PFLOP/s (a
-// library product of 8192^3 reaches 1.44 here; the MFMAs are busy about half of
-// the time, at 1.88 GHz), E4M3 548 us, D = 64 327 us, page 11 (!ONE) 571 us;
-// 4096 at D = 256 338 us.  Ragged chunks over 28 / 4 heads, 526 GFLOP: 491 to
-// 509 us.  82 tokens: 11 us of which the launch is most.
+// Measured, 32 / 8 heads, D = 128, causal 8192 bf16: 512 to 518 us, 1.07 PFLOP/s (a
+// library product of 8192^3 reaches 1.44 here; the MFMAs are busy 56% of the
+// time on the ragged chunks, at 1.65 GHz), E4M3 537 to 548 us, D = 64 320 to 327;
+// 4096 at D = 256 333 to 338 us.  Ragged chunks over 28 / 4 heads, 526 GFLOP:
+// 491 to 509 us.  82 tokens: 10.5 us, 8.4 of them the kernel's.
 #include <algorithm>
 #include <type_traits>
 
