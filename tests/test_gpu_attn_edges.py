@@ -1,0 +1,58 @@
+"""Attention over the paged cache where values or lengths are extreme: Inf and
+NaN in places that the kernels treat apart, lengths far below zero, softmax
+weights that span the types' range.  Every way that the entry points go is
+taken: decoding, few rows per sequence, row tiles whole and with the keys split
+(tables that hold more than 1000 tokens, few row tiles)."""
+import numpy as np
+import pytest
+import torch
+
+import w4a4_block_scaled_amd as w4
+from gpu_common import device, say
+from kv_common import ints
+from test_gpu_attn_prefill import check, chunks, run
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+
+
+def place(c, s, t):
+    """Page and row of token t of sequence s."""
+    page = c["kd"].shape[1]
+    return int(c["tables"][s, t // page]), t % page
+
+
+# ------------------------------------------------- masked values, keys split --
+
+@pytest.mark.parametrize("kind,dim,page", [("bf16", 128, 16), ("bf16", 64, 24), ("fp16", 256, 16), ("fp16", 128, 11),
+                                           ("bf16", 128, 1), ("fp8", 128, 32), ("fp8", 256, 8)])
+def test_split_keys_ignore_masked_values_in_their_first_tiles(kind, dim, page):
+    """The keys are split, and the first tile of the shares holds Inf and NaN that
+    some or all rows do not see (before their windows, between sinks and window):
+    the rows that do not see them are those of clean caches, bit for bit, each time."""
+    say(f"[split] masked values, {kind}, D = {dim}, page {page}")
+    window, sinks, past, new = 1100, 2, 1500, 40
+    c = chunks(kind, 1, 4, dim, page, [past], [new], seed=dim + page)
+    clean, lse = run(c, window, sinks)
+    check(c, clean, lse, window, sinks, label="clean", most=4)
+    # the first query's window begins at past - window + 1: tokens below are seen by none (sinks apart), the
+    # next ones by ever fewer of the 40 queries
+    low = past - window + 1
+    hidden = [t for t in range(sinks, low)]
+    part = [low + i for i in range(0, 12, 5)]             # token low + i: seen by queries 0 .. i
+    for t in hidden + part:
+        p, r = place(c, 0, t)
+        if kind == "fp8":
+            c["vd"].view(torch.uint8)[p, r] = 0x7f
+            if t in hidden:
+                c["kd"].view(torch.uint8)[p, r] = 0xff
+        else:
+            c["vd"][p, r] = INF if t % 2 else NAN
+            if t in hidden:
+                c["kd"][p, r] = NAN
+    first = part[-1] - low + 1                            # the first query that sees none of them
+    for _ in range(5):
+        y, l2 = run(c, window, sinks)
+        assert torch.equal(y[first:], clean[first:]) and torch.equal(l2, lse)
+        assert not torch.isfinite(y[0]).any()

@@ -553,6 +553,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
       here = place_of(t0);
       load(lk, kbase, here, koff, raw_k);
       load(lv, vbase, here, voff, raw_v);
+      __syncthreads();          // the flags are set before a wave marks its tile in them
       arrived();
       put(lk, raw_k, false);
       put(lv, raw_v, true);
