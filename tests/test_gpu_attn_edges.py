@@ -56,3 +56,28 @@ def test_split_keys_ignore_masked_values_in_their_first_tiles(kind, dim, page):
         y, l2 = run(c, window, sinks)
         assert torch.equal(y[first:], clean[first:]) and torch.equal(l2, lse)
         assert not torch.isfinite(y[0]).any()
+
+
+# -------------------------------------------------------- lengths below zero --
+
+@pytest.mark.parametrize("past,new,group,page", [
+    ([0, 20], [300, 50], 4, 16),                # row tiles, the tables hold few tokens: keys whole
+    ([2000, 30], [300, 50], 4, 16),             # keys split
+    ([2000, 30], [300, 50], 4, 11),
+    ([0] * 40, [300] * 40, 4, 16),              # more row tiles than the keys would be split for
+    ([600, 30], [3, 2], 4, 16),                 # few rows
+    ([600, 30], [8, 8], 1, 16),
+])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 3)])
+def test_lengths_below_zero(past, new, group, page, window, sinks):
+    """A negative length, the lowest of its type among them, puts every query
+    before position 0: zeros and -inf, and the other sequences as before."""
+    say(f"[lengths] past {past[:2]} new {new[:2]} x {len(new)}, group {group}, page {page}, window {window}")
+    c = chunks("bf16", 2, group, 128, page, past, new, seed=new[0])
+    good, lse = run(c, window, sinks)
+    n = int(c["cu"][1])
+    for length in (-1, -5, -299, -2 ** 31, -2 ** 31 + 1, -2 ** 31 + 299, -2 ** 31 + 301):
+        lens = [length] + list(c["lens"][1:])
+        y, l2 = run(c, window, sinks, lens=lens)
+        assert torch.all(y[:n] == 0) and torch.all(l2[:n] == -INF), length
+        assert torch.equal(y[n:], good[n:]) and torch.equal(l2[n:], lse[n:]), length

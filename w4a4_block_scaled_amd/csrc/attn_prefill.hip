@@ -97,7 +97,7 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, const PrefillWork& 
       const int cap = int(min(int64_t(a.kv.max_pages) * a.kv.page.d, int64_t(1) << 30));
       const int len = a.kv.lens[out->seq];
       out->over = len > cap;
-      out->len = min(len, cap);
+      out->len = max(min(len, cap), 0);      // so that len - count does not wrap
       return true;
     }
     before += __builtin_amdgcn_readlane(in, 63);
