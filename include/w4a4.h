@@ -410,6 +410,9 @@ w4a4_status w4a4_dualquant_solve(w4a4_format fmt, int64_t N, int64_t K,
  * a token without a valid page (an entry outside 0..pages-1), or whose sequence
  * is longer than max_pages * page_size, gets BF16 / FP16 NaN, and so may other
  * queries of the sequence; tokens without a page are not stored.
+ *
+ * Counts are int32 on the device: at most 2^30 sequences and list entries, and
+ * fewer than 2^31 - 256 rows times query heads (W4A4_ERR_SHAPE beyond).
  */
 typedef enum { W4A4_BF16 = 0, W4A4_F16 = 1, W4A4_E4M3 = 2 } w4a4_dtype;
 

@@ -758,6 +758,13 @@ size_t attn_prefill_workspace(int64_t seqs, int64_t tokens, int q_heads, int hea
   return size_t(tiles * heads) * (size_t(splits) * kBM * (head_dim + 2) * 4 + 4);
 }
 
+// Of the row tiles' launch (few rows have no more than fill the card: 0).
+int64_t attn_prefill_workgroups(int64_t seqs, int64_t tokens, int q_heads, int heads, int page_size) {
+  if (attn_few_serves(seqs, tokens, q_heads / heads, page_size)) return 0;
+  const int64_t tiles = row_tiles(seqs, tokens, q_heads / heads);
+  return tiles * heads * key_splits(tiles, heads);
+}
+
 hipError_t launch_attn_prefill(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype,
                                int head_dim, void* workspace, hipStream_t stream) {
   if (attn_few_serves(a.kv.seqs, tokens, a.group, int(a.kv.page.d)))

@@ -16,7 +16,11 @@ using w4a4::fail;
 using w4a4::hip_status;
 using w4a4::ok;
 
-const int64_t kMaxIndex = int64_t(1) << 31;     // int32 counts
+// The kernels count in int32: rows in tiles of up to 128 (kMaxRows leaves room for
+// the last one), sequences and list entries in steps of up to 1024, and a launch
+// has fewer than 2^32 threads.
+const int64_t kMaxIndex = int64_t(1) << 31, kMaxRows = kMaxIndex - 256, kMaxCount = int64_t(1) << 30;
+const int64_t kMaxGrid = int64_t(1) << 24;      // workgroups of 256
 
 w4a4_status check_cache(const char* what, const w4a4_kv_cache* c) {
   if (!c) return fail(W4A4_ERR_NULL, "%s: cache must be non-NULL", what);
@@ -41,8 +45,9 @@ w4a4_status check_cache(const char* what, const w4a4_kv_cache* c) {
 
 w4a4_status check_seqs(const char* what, const w4a4_kv_seqs* s, bool lens) {
   if (!s) return fail(W4A4_ERR_NULL, "%s: seqs must be non-NULL", what);
-  if (s->seqs < 0 || s->max_pages < 1 || s->table_stride < s->max_pages)
-    return fail(W4A4_ERR_SHAPE, "%s: seqs=%d max_pages=%d table_stride=%lld (need seqs >= 0, 1 <= max_pages <= table_stride)",
+  if (s->seqs < 0 || s->seqs > kMaxCount || s->max_pages < 1 || s->table_stride < s->max_pages)
+    return fail(W4A4_ERR_SHAPE,
+                "%s: seqs=%d max_pages=%d table_stride=%lld (need 0 <= seqs <= 2^30, 1 <= max_pages <= table_stride)",
                 what, int(s->seqs), int(s->max_pages), (long long)s->table_stride);
   if (s->seqs > 0 && (!s->tables || (lens && !s->lens)))
     return fail(W4A4_ERR_NULL, "%s: tables and lens must be non-NULL", what);
@@ -97,7 +102,7 @@ w4a4_status check_attn(const char* what, const w4a4_kv_cache* c, const w4a4_kv_s
                        size_t ws_bytes, size_t need) {
   w4a4_status st = check_type(what, c, dtype);
   if (st != W4A4_OK) return st;
-  if (!heads_ok(c, q_heads) || rows * q_heads >= kMaxIndex)
+  if (!heads_ok(c, q_heads) || rows * q_heads >= kMaxRows)
     return fail(W4A4_ERR_SHAPE, "%s: %d query heads for %d kv heads, %lld rows", what, q_heads, int(c->heads),
                 (long long)rows);
   if (window < 0 || sinks < 0)
@@ -163,7 +168,7 @@ w4a4_status check_ws(const char* what, const void* ws, size_t bytes, size_t need
 }
 
 w4a4_status check_list(const char* what, const void* a, const void* b, int64_t n) {
-  if (n < 0 || n >= kMaxIndex) return fail(W4A4_ERR_SHAPE, "%s: %lld entries", what, (long long)n);
+  if (n < 0 || n > kMaxCount) return fail(W4A4_ERR_SHAPE, "%s: %lld entries", what, (long long)n);
   if (n > 0 && (!a || !b)) return fail(W4A4_ERR_NULL, "%s: the index lists must be non-NULL", what);
   if (!aligned(a, 4) || !aligned(b, 4)) return fail(W4A4_ERR_ALIGN, "%s: index lists need 4-byte alignment", what);
   return W4A4_OK;
@@ -221,7 +226,7 @@ w4a4_status w4a4_attn_decode(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seq
 
 size_t w4a4_attn_prefill_workspace_bytes(const w4a4_kv_cache* cache, int64_t seqs, int64_t tokens, int q_heads) {
   if (check_cache("attn_prefill_workspace_bytes", cache) != W4A4_OK || !heads_ok(cache, q_heads) || seqs <= 0 ||
-      tokens <= 0 || tokens * q_heads >= kMaxIndex)
+      tokens <= 0 || tokens * q_heads >= kMaxRows)
     return 0;
   return w4a4::attn_prefill_workspace(seqs, tokens, q_heads, cache->heads, cache->head_dim, cache->page_size);
 }
@@ -241,6 +246,9 @@ w4a4_status w4a4_attn_prefill(const w4a4_kv_cache* cache, const w4a4_kv_seqs* se
                   lse, workspace, ws_bytes, need);
   if (st != W4A4_OK) return st;
   if (tokens == 0) return ok();
+  if (w4a4::attn_prefill_workgroups(seqs->seqs, tokens, q_heads, cache->heads, cache->page_size) >= kMaxGrid)
+    return fail(W4A4_ERR_SHAPE, "%s: %lld tokens of %d sequences are too many for one call", what, (long long)tokens,
+                int(seqs->seqs));
   if (!cu) return fail(W4A4_ERR_NULL, "%s: cu must be non-NULL", what);
   if (!aligned(cu, 4)) return fail(W4A4_ERR_ALIGN, "%s: cu needs 4-byte alignment", what);
   return hip_status(w4a4::launch_attn_prefill(attn_args(cache, seqs, q_heads, q, q_row, q_head, scale, window, sinks,

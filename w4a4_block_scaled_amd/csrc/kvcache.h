@@ -80,6 +80,7 @@ hipError_t launch_attn_few(const AttnArgs& a, const int32_t* cu, int64_t tokens,
                            int head_dim, void* workspace, hipStream_t stream);
 
 size_t attn_prefill_workspace(int64_t seqs, int64_t tokens, int q_heads, int heads, int head_dim, int page_size);
+int64_t attn_prefill_workgroups(int64_t seqs, int64_t tokens, int q_heads, int heads, int page_size);
 hipError_t launch_attn_prefill(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype,
                                int head_dim, void* workspace, hipStream_t stream);
 
