@@ -1,0 +1,48 @@
+"""What the binding of the paged cache and its attention refuses beyond the C
+ABI: tensors that are not on a GPU, index tensors and workspaces whose memory is
+not what the kernels would take it for.  (On CPU tensors throughout: each
+refusal comes before anything is enqueued.)"""
+import pytest
+import torch
+
+import os
+
+import w4a4_block_scaled_amd as w4
+
+pytestmark = pytest.mark.skipif(not os.path.exists(w4.library_path()),
+                                reason="libw4a4.so not built (python -m w4a4_block_scaled_amd.build)")
+
+
+def ints(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+def calls(**over):
+    """Every entry point with tensors that fit each other; `over` replaces some."""
+    t = {"rows": torch.zeros(3, 2, 64, dtype=torch.bfloat16), "q": torch.zeros(3, 4, 64, dtype=torch.bfloat16),
+         "k": torch.zeros(6, 16, 2, 64, dtype=torch.bfloat16), "tables": ints(3, 4), "lens": ints(3), "refs": ints(6),
+         "cu": ints(4), "a": ints(2), "b": ints(2), "lacking": ints(1), "workspace": None}
+    t.update(over)
+    v = t["k"].clone()
+    cache, where = (t["k"], v), (t["tables"], t["lens"])
+    return {
+        "kv_append": lambda: w4.kv_append(t["rows"], t["rows"], *cache, *where, cu_seqlens=t["cu"]),
+        "attn_decode": lambda: w4.attn_decode(t["q"], *cache, *where, workspace=t["workspace"]),
+        "attn_prefill": lambda: w4.attn_prefill(t["q"], t["cu"], *cache, *where, workspace=t["workspace"]),
+        "kv_copy_pages": lambda: w4.kv_copy_pages(cache, t["a"], t["b"]),
+        "kv_reserve": lambda: w4.kv_reserve(*where, t["refs"], 16, lacking=t["lacking"]),
+        "kv_fork": lambda: w4.kv_fork(cache, *where, t["refs"], t["a"], t["b"], lacking=t["lacking"]),
+        "kv_free": lambda: w4.kv_free(*where, t["refs"], t["a"]),
+        "kv_trim": lambda: w4.kv_trim(*where, t["refs"], 16, 5, 0, t["a"]),
+        "kv_compact": lambda: w4.kv_compact(cache, t["tables"], t["refs"]),
+    }
+
+
+@pytest.mark.parametrize("name", list(calls()))
+def test_tensors_on_the_cpu(name, monkeypatch):
+    """Their addresses mean nothing to a kernel, whatever GPU is current."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: pytest.fail("asked for a stream"), raising=False)
+    with pytest.raises(w4.W4A4Error, match="GPU") as e:
+        calls()[name]()
+    assert e.value.status == 2

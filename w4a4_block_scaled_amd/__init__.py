@@ -454,8 +454,10 @@ def _kv_rows(what: str, x: torch.Tensor, rows: int, heads, dim: int, device) -> 
 
 
 def _kv_stream(device: torch.device) -> int:
-    """Handle of the current stream of `device` (_stream without the torch.cuda.Stream object)."""
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
+    """Handle of the current stream of `device`, which has to be a GPU (_stream without the torch.cuda.Stream object)."""
+    if device.type != "cuda":
+        raise W4A4Error(2, f"the cache and everything with it must be on a GPU, not on {device}")
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 @functools.lru_cache(maxsize=4096)
