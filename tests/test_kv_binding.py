@@ -46,3 +46,29 @@ def test_tensors_on_the_cpu(name, monkeypatch):
     with pytest.raises(w4.W4A4Error, match="GPU") as e:
         calls()[name]()
     assert e.value.status == 2
+
+
+def spread(*shape):
+    """int32, two-dimensional, its entries not side by side."""
+    return torch.zeros(shape[0], shape[1] * 2, dtype=torch.int32)[:, ::2]
+
+
+@pytest.mark.parametrize("name,over", [
+    ("kv_append", dict(cu=spread(2, 2))), ("attn_prefill", dict(cu=spread(2, 2))),
+    ("kv_reserve", dict(refs=spread(2, 3))), ("kv_fork", dict(refs=spread(2, 3))), ("kv_free", dict(refs=spread(2, 3))),
+    ("kv_free", dict(a=spread(1, 2))), ("kv_trim", dict(a=spread(1, 2))), ("kv_trim", dict(refs=spread(2, 3))),
+    ("kv_compact", dict(refs=spread(2, 3))), ("kv_copy_pages", dict(a=ints(2, 2)[:, 0]))])
+def test_index_tensors_with_gaps(name, over):
+    with pytest.raises(w4.W4A4Error, match="contiguous") as e:
+        calls(**over)[name]()
+    assert e.value.status == 2
+
+
+@pytest.mark.parametrize("name", ["attn_decode", "attn_prefill"])
+@pytest.mark.parametrize("workspace", [torch.zeros(1 << 12, 2, dtype=torch.float32)[:, 0], torch.zeros(1).expand(1 << 24),
+                                       torch.empty(1 << 24, dtype=torch.uint8, device="meta")])
+def test_workspaces(name, workspace):
+    """A workspace with gaps is shorter than it says, one elsewhere is not the device's."""
+    with pytest.raises(w4.W4A4Error, match="workspace") as e:
+        calls(workspace=workspace)[name]()
+    assert e.value.status == 2

@@ -408,7 +408,7 @@ def _kv_type(t: torch.Tensor, what: str) -> int:
 
 def _int32(what: str, device, *tensors) -> None:
     for t in tensors:
-        if t is not None and (t.dtype != torch.int32 or t.device != device or (t.dim() == 1 and not t.is_contiguous())):
+        if t is not None and (t.dtype != torch.int32 or t.device != device or not t.is_contiguous()):
             raise W4A4Error(2, f"{what}: index tensors are int32, on {device}, with contiguous entries")
 
 
@@ -434,10 +434,11 @@ def _kv_cache(what: str, k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> 
 
 def _kv_seqs(what: str, tables: torch.Tensor, lens: Optional[torch.Tensor], device) -> _KvSeqs:
     shape = tables.shape
-    if len(shape) != 2 or (shape[1] > 1 and tables.stride(1) != 1) or \
-            (lens is not None and (lens.dim() != 1 or lens.shape[0] != shape[0])):
-        raise W4A4Error(2, f"{what}: tables {tuple(tables.shape)} must be [seqs, max_pages] with contiguous rows, lens [seqs]")
-    _int32(what, device, tables, lens)
+    if len(shape) != 2 or (shape[1] > 1 and tables.stride(1) != 1) or tables.dtype != torch.int32 or \
+            tables.device != device or (lens is not None and (lens.dim() != 1 or lens.shape[0] != shape[0])):
+        raise W4A4Error(2, f"{what}: tables {tuple(tables.shape)} must be int32 [seqs, max_pages] on {device} with "
+                           "contiguous rows, lens [seqs]")
+    _int32(what, device, lens)
     seqs, width = shape
     return _KvSeqs(tables.data_ptr(), None if lens is None else lens.data_ptr(),
                    tables.stride(0) if seqs > 1 else width, seqs, width)
@@ -519,6 +520,8 @@ def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, sc
         if size:
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise W4A4Error(2, f"{name}: the workspace must be contiguous, on {dev}")
         size = workspace.numel() * workspace.element_size()
     tail = (_kv_type(q, name), q_heads, *q_at, dim ** -0.5 if scale is None else scale, window, sinks, *out_at,
             None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), size,
