@@ -72,3 +72,24 @@ def test_workspaces(name, workspace):
     with pytest.raises(w4.W4A4Error, match="workspace") as e:
         calls(workspace=workspace)[name]()
     assert e.value.status == 2
+
+
+BIG = [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 40 + 1, -2 ** 31 - 1]
+
+
+@pytest.mark.parametrize("value", BIG)
+@pytest.mark.parametrize("call", [
+    lambda t, x: w4.attn_decode(t["q"], t["k"], t["k"].clone(), t["tables"], t["lens"], window=x),
+    lambda t, x: w4.attn_decode(t["q"], t["k"], t["k"].clone(), t["tables"], t["lens"], window=5, sinks=x),
+    lambda t, x: w4.attn_prefill(t["q"], t["cu"], t["k"], t["k"].clone(), t["tables"], t["lens"], window=x),
+    lambda t, x: w4.kv_trim(t["tables"], t["lens"], t["refs"], 16, x),
+    lambda t, x: w4.kv_trim(t["tables"], t["lens"], t["refs"], 16, 5, x),
+    lambda t, x: w4.kv_trim(t["tables"], t["lens"], t["refs"], x, 5),
+    lambda t, x: w4.kv_reserve(t["tables"], t["lens"], t["refs"], x)])
+def test_numbers_past_32_bits(call, value):
+    """A C int would take their low 32 bits: a window of 2^32 + 5 as one of 5."""
+    t = {"q": torch.zeros(3, 4, 64, dtype=torch.bfloat16), "k": torch.zeros(6, 16, 2, 64, dtype=torch.bfloat16),
+         "tables": ints(3, 4), "lens": ints(3), "refs": ints(6), "cu": ints(4)}
+    with pytest.raises(w4.W4A4Error, match="32 bits") as e:
+        call(t, value)
+    assert e.value.status == 2

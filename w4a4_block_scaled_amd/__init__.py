@@ -412,6 +412,13 @@ def _int32(what: str, device, *tensors) -> None:
             raise W4A4Error(2, f"{what}: index tensors are int32, on {device}, with contiguous entries")
 
 
+def _c_ints(what: str, *numbers) -> None:
+    """Refuses what a C int would cut to its low 32 bits."""
+    for x in numbers:
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise W4A4Error(2, f"{what}: {x} does not fit 32 bits")
+
+
 def _kv_cache(what: str, k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> _KvCache:
     shape, stride = k.shape, k.stride()
     if len(shape) != 4 or shape != v.shape or stride != v.stride() or stride[3] != 1 or k.dtype != v.dtype or \
@@ -499,6 +506,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
 def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, scale, window, sinks, out, return_lse,
           workspace):
     dev = k_cache.device
+    _c_ints(name, window, sinks)
     c = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
     s = _kv_seqs(name, tables, lens, dev)
     rows, q_heads, dim = q.shape[0], q.shape[1], c.head_dim
@@ -617,6 +625,7 @@ def kv_reserve(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, pag
                lacking: Optional[torch.Tensor] = None) -> None:
     """w4a4_kv_reserve: pages for lens[s] tokens of every sequence, the lowest
     free ones first; lacking int32 [1]: the number that was not to be had."""
+    _c_ints("kv_reserve", page_size)
     s = _kv_seqs("kv_reserve", tables, lens, refs.device)
     _int32("kv_reserve", refs.device, refs, lacking)
     ws = _kv_workspace(s.seqs, refs.numel(), refs.device)
@@ -657,6 +666,7 @@ def kv_trim(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_s
             seqs: Optional[torch.Tensor] = None) -> None:
     """w4a4_kv_trim: let go of the pages that no later token of the sequences
     `seqs` (None: all) sees under a window with sinks."""
+    _c_ints("kv_trim", page_size, window, sinks)
     s = _kv_seqs("kv_trim", tables, lens, refs.device)
     _int32("kv_trim", refs.device, refs, seqs)
     _check(lib().w4a4_kv_trim(s, page_size, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
