@@ -81,3 +81,24 @@ def test_lengths_below_zero(past, new, group, page, window, sinks):
         y, l2 = run(c, window, sinks, lens=lens)
         assert torch.all(y[:n] == 0) and torch.all(l2[:n] == -INF), length
         assert torch.equal(y[n:], good[n:]) and torch.equal(l2[n:], lse[n:]), length
+
+
+# -------------------------------------------------------- Inf that rows see --
+
+@pytest.mark.parametrize("kind,dim,page,past,new", [("bf16", 128, 16, 2500, 40), ("fp16", 64, 8, 2500, 40),
+                                                    ("bf16", 256, 11, 1400, 9), ("fp16", 128, 24, 3000, 5)])
+def test_split_keys_with_inf_in_the_first_tile_of_a_share(kind, dim, page, past, new):
+    """An Inf among the values of any tile of the split keys, the first one of a
+    share among them, comes out as Inf in the rows that see it (its weight is
+    positive), and elsewhere nothing changes."""
+    say(f"[split] Inf, {kind}, D = {dim}, page {page}, past {past}")
+    c = chunks(kind, 2, 4, dim, page, [past], [new], seed=dim + past)
+    clean, _ = run(c)
+    # a token of every tile of 64, its own column each: some of the tiles begin a share
+    tiles = list(range(0, past, 64))[:dim - 1]
+    for i, t in enumerate(tiles):
+        c["vd"][(*place(c, 0, t + i % 7), 0, i)] = INF if i % 2 else -INF
+    y, _ = run(c)
+    for i in range(len(tiles)):
+        assert torch.all(y[:, :4, i] == (INF if i % 2 else -INF)), f"tile {i}"
+    assert torch.equal(y[:, 4:], clean[:, 4:]) and torch.equal(y[:, :4, len(tiles):], clean[:, :4, len(tiles):])

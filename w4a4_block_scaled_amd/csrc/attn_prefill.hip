@@ -535,12 +535,10 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
         load(k_in, kbase, here, koff, raw_k);
         load(v_in, vbase, here, voff, raw_v);
       }
-      settle(v_cur, t, buf);
-      if (busy) {
-        at_f32x16 s[2], none[2];
-        scores(k_cur, t, s);
-        compute(k_cur, v_cur, t, s, none, std::false_type());
-      }
+      at_f32x16 s[2], none[2];
+      if (busy) scores(k_cur, t, s);
+      settle(v_cur, t, buf);    // after the rebase by this tile's maximum: the first one's is by 0
+      if (busy) compute(k_cur, v_cur, t, s, none, std::false_type());
       if (more) {
         arrived();
         put(k_in, raw_k, false);
