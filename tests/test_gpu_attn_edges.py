@@ -102,3 +102,67 @@ def test_split_keys_with_inf_in_the_first_tile_of_a_share(kind, dim, page, past,
     for i in range(len(tiles)):
         assert torch.all(y[:, :4, i] == (INF if i % 2 else -INF)), f"tile {i}"
     assert torch.equal(y[:, 4:], clean[:, 4:]) and torch.equal(y[:, :4, len(tiles):], clean[:, :4, len(tiles):])
+
+
+WAYS = {
+    # past, new, page: what the table holds and the number of rows choose the way
+    "decode": ([900, 40], [1, 1], 16), "decode, page 11": ([900, 40], [1, 1], 11), "decode, long": ([30000, 40], [1, 1], 16),
+    "few": ([900, 40], [3, 2], 16), "few, long": ([30000, 40], [3, 2], 16),
+    "whole": ([700, 40], [150, 60], 16), "whole, page 11": ([700, 40], [150, 60], 11), "split": ([3000, 40], [30, 20], 16),
+}
+
+
+def attend(c, way, window=0, sinks=0):
+    """(out, lse) of the new tokens, in their order, by the entry point of the way."""
+    if not way.startswith("decode"):
+        return run(c, window, sinks)
+    dev = c["dev"]
+    return w4.attn_decode(c["q"].to(dev), c["kd"], c["vd"], ints(c["tables"], dev), ints(c["lens"], dev),
+                          k_scale=c["scales"][0], v_scale=c["scales"][1], window=window, sinks=sinks, return_lse=True)
+
+
+def steep(kind, dim, way, seed, gaps, group=4):
+    """A case whose queries and keys are zero but in the first element, so that the
+    weight of token t of sequence 0 is 2^-gaps(t) of the largest, exactly up to the
+    rounding of the scale."""
+    past, new, page = WAYS[way]
+    c = chunks(kind, 1, group, dim, page, past, new, seed=seed)
+    c["q"].zero_()
+    c["q"][:, :, 0] = 1.0
+    n = c["lens"][0]
+    k = torch.zeros_like(c["kd"])
+    # score in the exponent of 2: dim^-0.5 / ln 2 * key
+    x = torch.tensor([-g * dim ** 0.5 * np.log(2.0) for g in (gaps(t) for t in range(n))]).to(c["kd"].dtype).to(c["dev"])
+    for t0 in range(0, n, page):
+        m = min(page, n - t0)
+        k[int(c["tables"][0, t0 // page]), :m, 0, 0] = x[t0:t0 + m]
+    c["kd"].copy_(k)
+    c["f64"][0] = k.cpu().float().numpy().astype(np.float64)
+    return c
+
+
+SMALL = [w for w in WAYS if not w.startswith("whole")]
+
+
+@pytest.mark.parametrize("way", SMALL)
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("gap", [30, 110, 200])
+@pytest.mark.parametrize("rest", ["all as small", "others large"])
+@pytest.mark.parametrize("first", [True, False])
+def test_inf_of_a_small_weight(way, kind, gap, rest, first):
+    """A value of Inf whose weight is far below the largest, before the largest and
+    behind it, where the running maximum takes one long step and where it does not:
+    every positive weight makes it Inf."""
+    say(f"[inf] {way}, {kind}, 2^-{gap}, {'before' if first else 'behind'} the largest, {rest}")
+    past = WAYS[way][0][0]
+    top, at = (past - 5, 3) if first else (3, past - 200)
+    c = steep(kind, 64, way, 11, lambda t: 0 if t == top else gap if t == at or rest == "all as small" else 4)
+    clean, _ = attend(c, way)
+    c["vd"][(*place(c, 0, at), 0, 5)] = INF
+    c["vd"][(*place(c, 0, at), 0, 6)] = -INF
+    y, _ = attend(c, way)
+    n = int(c["cu"][1])
+    assert torch.all(y[:n, :, 5] == INF) and torch.all(y[:n, :, 6] == -INF)
+    keep = [i for i in range(64) if i not in (5, 6)]
+    assert torch.isfinite(y[:n][:, :, keep]).all() and torch.equal(y[n:], clean[n:])
+    assert (y[:n][:, :, keep].float() - clean[:n][:, :, keep].float()).abs().max() <= 2.0 ** -6

@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
       // The sums are rebased only where a maximum has grown by more than 2^8: until
       // then weights go up to 2^8, which costs neither type any accuracy.
       if (__any(mx > m + 8.0f)) {
-        const float mn = fmaxf(m, mx), f = rebase(m, mn);
+        const float mn = fmaxf(m, mx), f = fmaxf(rebase(m, mn), odd ? kLeast : 0.0f);
 #pragma unroll
         for (int j = 0; j < kBlocks; ++j) o[j] *= f;
         l *= f;
@@ -609,9 +609,9 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
       at_f32x4 O = {0, 0, 0, 0};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float f = rebase(lds_m[w][r], M);
+        const float m1 = lds_m[w][r], f = rebase(m1, M);
         L += f * lds_l[w][r];
-        O += *reinterpret_cast<const at_f32x4*>(&lds_o[w][r][d]) * f;
+        O += rebased<E>(*reinterpret_cast<const at_f32x4*>(&lds_o[w][r][d]), m1, f);
       }
       if (whole) {
         finish<T, D, E, FEW>(a, work, head, qs, sp, unit_row + r, d, M, L, O);
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(256) decode_join_kernel(AttnArgs a, Work work)
       const at_f32x4 o = *reinterpret_cast<const at_f32x4*>(p.o + r * D + 4 * quad);
       const float mn = fmaxf(M, m), f = rebase(M, mn), h = rebase(m, mn);
       L = L * f + l * h;
-      O = O * f + o * h;
+      O = rebased<E>(O, M, f) + rebased<E>(o, m, h);
       M = mn;
     }
     __syncthreads();              // the row before has been read
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(256) decode_join_kernel(AttnArgs a, Work work)
     for (int i = 0; i < kSplits; ++i) {
       const float f = rebase(lds_m[i], M);
       L += f * lds_l[i];
-      O += lds_o[i][quad] * f;
+      O += rebased<E>(lds_o[i][quad], lds_m[i], f);
     }
     finish<T, D, E, FEW>(a, work, head, qs, sp, unit_row + r, 4 * quad, M, L, O);
   }

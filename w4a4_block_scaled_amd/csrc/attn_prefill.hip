@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[n][e] = 0.0f;
   float m = kNegInf, l = 0.0f;
+  float least = 0.0f;         // of the factors that the sums are rebased by: kLeast from the first Inf or NaN on
 
   auto sees = [&](int t, int stop) {
     return t < stop && t <= pos && (!a.window || t > pos - a.window || t < a.sinks);
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   auto rebase_sums = [&](float mx) {
     mx = max_xor32(mx) * cs;
     if (__any(mx > m + 8.0f)) {
-      const float mn = fmaxf(m, mx), f = rebase(m, mn);
+      const float mn = fmaxf(m, mx), f = fmaxf(rebase(m, mn), least);
 #pragma unroll
       for (int n = 0; n < kBlocks; ++n) o[n] *= f;
       l *= f;
@@ -392,6 +393,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   // the row's sum.  The rows that see such a value get it added, then it is
   // cleared in the tile.  (All waves get here together: the flag is the tile's.)
   auto settle_odd = [&](Lds16* vt, int t) {
+    if (SPLIT) least = kLeast;
     int stop;
     const int base = tile_at(t, &stop);
 #pragma unroll 1
@@ -670,8 +672,9 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(AttnArgs a, PrefillWo
   float M = fmaxf(f0, f1);
 #pragma unroll
   for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor(M, d));
-  f0 = rebase(f0, M);
-  f1 = rebase(f1, M);
+  const float m0 = f0, m1 = f1;
+  f0 = rebase(m0, M);
+  f1 = rebase(m1, M);
   if (lane < used) L = f0 * base[lane * part + kBM * (D + 1) + r];
   if (lane + 32 < used) L += f1 * base[(lane + 32) * part + kBM * (D + 1) + r];
 #pragma unroll
@@ -684,11 +687,12 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(AttnArgs a, PrefillWo
     for (int k = 0; k < 8; ++k) {                     // 8 splits' loads in flight
       const int i = min(i0 + k, used - 1);
       const float f = __shfl(i < 32 ? f0 : f1, (threadIdx.x & 32) + (i & 31));
+      const float m = __shfl(i < 32 ? m0 : m1, (threadIdx.x & 32) + (i & 31));
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
         const at_f32x2 x = *reinterpret_cast<const at_f32x2*>(base + i * part + r * D + 64 * j + 2 * lane);
-        O[2 * j] += i0 + k < used ? f * x.x : 0.0f;
-        O[2 * j + 1] += i0 + k < used ? f * x.y : 0.0f;
+        O[2 * j] += i0 + k < used ? rebased<E>(x.x, m, f) : 0.0f;
+        O[2 * j + 1] += i0 + k < used ? rebased<E>(x.y, m, f) : 0.0f;
       }
     }
   }
