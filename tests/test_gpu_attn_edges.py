@@ -9,7 +9,8 @@ import torch
 
 import w4a4_block_scaled_amd as w4
 from gpu_common import device, say
-from kv_common import ints
+from kv_common import UNIT, as_f64, ints
+from oracle import attention as A
 from test_gpu_attn_prefill import check, chunks, run
 
 pytestmark = pytest.mark.gpu
@@ -109,6 +110,7 @@ WAYS = {
     "decode": ([900, 40], [1, 1], 16), "decode, page 11": ([900, 40], [1, 1], 11), "decode, long": ([30000, 40], [1, 1], 16),
     "few": ([900, 40], [3, 2], 16), "few, long": ([30000, 40], [3, 2], 16),
     "whole": ([700, 40], [150, 60], 16), "whole, page 11": ([700, 40], [150, 60], 11), "split": ([3000, 40], [30, 20], 16),
+    "decode, 131071": ([131070], [1], 16), "few, 131071": ([131068], [3], 16), "split, 131071": ([131051], [20], 16),
 }
 
 
@@ -133,15 +135,19 @@ def steep(kind, dim, way, seed, gaps, group=4):
     k = torch.zeros_like(c["kd"])
     # score in the exponent of 2: dim^-0.5 / ln 2 * key
     x = torch.tensor([-g * dim ** 0.5 * np.log(2.0) for g in (gaps(t) for t in range(n))]).to(c["kd"].dtype).to(c["dev"])
-    for t0 in range(0, n, page):
-        m = min(page, n - t0)
-        k[int(c["tables"][0, t0 // page]), :m, 0, 0] = x[t0:t0 + m]
+    t = torch.arange(n, device=c["dev"])
+    at = ints(c["tables"][0], c["dev"]).long()[t // page], t % page, 0, 0
+    if kind == "fp8":
+        k.view(torch.uint8)[at] = x.view(torch.uint8)
+        c["scales"][0].fill_(1.0)
+    else:
+        k[at] = x
     c["kd"].copy_(k)
-    c["f64"][0] = k.cpu().float().numpy().astype(np.float64)
+    c["f64"][0] = as_f64(k)
     return c
 
 
-SMALL = [w for w in WAYS if not w.startswith("whole")]
+SMALL = [w for w in WAYS if not w.startswith("whole") and "131071" not in w]
 
 
 @pytest.mark.parametrize("way", SMALL)
@@ -166,3 +172,46 @@ def test_inf_of_a_small_weight(way, kind, gap, rest, first):
     keep = [i for i in range(64) if i not in (5, 6)]
     assert torch.isfinite(y[:n][:, :, keep]).all() and torch.equal(y[n:], clean[n:])
     assert (y[:n][:, :, keep].float() - clean[:n][:, :, keep].float()).abs().max() <= 2.0 ** -6
+
+
+# ------------------------------------------- weights far below the largest --
+
+@pytest.mark.parametrize("way", [w for w in WAYS if "long" not in w])
+@pytest.mark.parametrize("kind,high", [("fp16", "fp16"), ("fp8", "fp16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("gap", [16, 22, 26])
+def test_many_small_weights_beside_a_large_one(way, kind, high, gap):
+    """One token takes nearly all the weight and its value is 0, so that the output is
+    the sum of the others, each of about 2^-gap.
+
+    Bound, with u, c, eta, n, A and V as in kv_common, for the types' weights kept at
+    2^7 or more where the largest one is: FP16's step of 2^-24 rounds a weight by at
+    most 2^-25 / 2^7 of the largest (BF16 has no such step), and the exponents, of up
+    to gap + 15, are rounded by 2^-24 of themselves:
+    |y - o| <= u |o| + (1 + u) (c + 2 eta + (n / 16 + 64) 2^-23 + (gap + 15) 2^-24) A + n 2^-32 V + 2^-25.
+    (An fp32 sum here grows by 8 tokens or an MFMA of at least 16 at a time, n / 16
+    steps at most, and is joined from fewer than 64 parts in a row.)"""
+    say(f"[small] {way}, {kind}, 2^-{gap}")
+    past, new, _ = WAYS[way]
+    top = 5
+    c = steep(kind, 64, way, 12, lambda t: 0 if t == top else gap)
+    if high != c["high"]:
+        c["high"], c["q"] = high, c["q"].to(torch.float16)
+    p, r = place(c, 0, top)
+    v = torch.rand(c["vd"].shape, generator=torch.Generator().manual_seed(gap)).to(c["dev"]) + 0.5
+    v[p, r] = 0
+    c["vd"].copy_(v.to(c["vd"].dtype))
+    c["f64"][1] = as_f64(c["vd"]) * (1.0 if c["scales"][1] is None else as_f64(c["scales"][1])[:, None])
+    y, lse = attend(c, way)
+    u = UNIT[high]
+    weights = 2.0 ** -20 if high == "fp16" else 2.0 ** -15
+    if way.startswith("whole"):
+        weights = u
+    for i in (0, new[0] - 1):
+        o, ref_lse, (a, big, size, n) = A.attend(as_f64(c["q"])[i, 0], *c["f64"], c["tables"][0], c["lens"][0],
+                                                 past[0] + i, 0, 64 ** -0.5, 0, 0)
+        eta = 72 * 2.0 ** -23 * size + 2.0 ** -22
+        bound = u * np.abs(o) + (1 + u) * (weights + 2 * eta + (n / 16 + 64) * 2.0 ** -23 + (gap + 15) * 2.0 ** -24) * a
+        bound += (n * 2.0 ** -32 * big if high == "fp16" else 0) + 2.0 ** -25
+        err = np.abs(as_f64(y)[i, 0] - o)
+        assert np.all(err <= bound), f"row {i}: off by {err.max():.3e} ({(err / bound).max():.2f} of the bound)"
+        assert abs(lse[i, 0].item() - ref_lse) <= eta + n * 2.0 ** -22 + 2.0 ** -21 + 2.0 ** -22 * abs(ref_lse)

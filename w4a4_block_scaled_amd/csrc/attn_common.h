@@ -46,11 +46,20 @@ __device__ __forceinline__ uint32_t split_odd16(uint32_t u, uint32_t* plus, uint
   return keep;
 }
 
+// The reference m of a row's softmax weights 2^(score - m).  It follows the row's
+// maximum, kRaise below it, and is moved only where the maximum has grown by more
+// than kGrowth since, so that sums are rarely rebased and weights go up to
+// 2^(kGrowth + kRaise).  kRaise uses FP16's range: a weight is lost (rounded to a
+// step of 2^-24) only at 2^-32 of the largest one, where 131071 tokens together
+// weigh 2^-15 of it; without, at 2^-25, half a percent each.  BF16 has fp32's range.
+constexpr float kGrowth = 8.0f;
+
 // 16-bit element types.  pack(a, b): two fp32 to two elements, RNE, a in the
 // low half.  mfma16: 16 x 16 x 32, mfma32: 32 x 32 x 16; operands 8 elements
 // per lane.
 struct Bf16 {
   static constexpr uint32_t kExp = 0x7f80u, kOne = 0x3f80u;      // the exponent of Inf and NaN; 1.0
+  static constexpr float kRaise = 0.0f;
   static __device__ __forceinline__ bool not_finite(uint32_t u) { return has_odd<kExp>(u); }
   static __device__ __forceinline__ uint32_t finite(uint32_t u) { return without_odd<kExp>(u); }
   static __device__ __forceinline__ uint32_t split_odd(uint32_t u, uint32_t* plus, uint32_t* minus) {
@@ -76,6 +85,7 @@ struct Bf16 {
 };
 struct F16 {
   static constexpr uint32_t kExp = 0x7c00u, kOne = 0x3c00u;      // the exponent of Inf and NaN; 1.0
+  static constexpr float kRaise = 7.0f;
   static __device__ __forceinline__ bool not_finite(uint32_t u) { return has_odd<kExp>(u); }
   static __device__ __forceinline__ uint32_t finite(uint32_t u) { return without_odd<kExp>(u); }
   static __device__ __forceinline__ uint32_t split_odd(uint32_t u, uint32_t* plus, uint32_t* minus) {
@@ -146,7 +156,7 @@ __device__ __forceinline__ float sum_xor16(float x) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// exp2(x - m) as the weight of a partial result with maximum x against m;
+// exp2(x - m) as the weight of a partial result with reference x against m;
 // 0 for a partial result without a visible token.
 __device__ __forceinline__ float rebase(float x, float m) { return x == kNegInf ? 0.0f : exp2_fast(x - m); }
 

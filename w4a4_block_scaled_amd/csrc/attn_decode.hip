@@ -7,7 +7,7 @@
 // of which every workgroup takes an equal contiguous piece, whatever the lengths
 // are, so that the last ones to end end together.  A
 // workgroup that holds a unit whole writes its output; a unit cut by the
-// pieces' ends leaves partial results (unnormalised sum, maximum, sum of
+// pieces' ends leaves partial results (unnormalised sum, reference, sum of
 // weights) that a second kernel joins.
 //
 // Inside a tile each of the 4 waves takes 32 tokens.  Scores come from the
@@ -60,8 +60,8 @@ __device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, int length, int c
   return z;
 }
 
-// Results of a unit's piece: unnormalised sums o [rows x D], maxima m and sums
-// of weights l [rows], in the log2 domain.
+// Results of a unit's piece: unnormalised sums o [rows x D], references m of the
+// weights and sums of weights l [rows], in the log2 domain.
 struct Partial {
   float *o, *m, *l;
 };
@@ -211,7 +211,7 @@ __device__ __forceinline__ int64_t readlane(int64_t x, int l) {
   return int64_t(uint32_t(__builtin_amdgcn_readlane(int(x), l))) | int64_t(__builtin_amdgcn_readlane(int(x >> 32), l)) << 32;
 }
 
-// Output columns d .. d + 3 of row `row` of a kv head from its maximum, sum of
+// Output columns d .. d + 3 of row `row` of a kv head from its reference, sum of
 // weights and unnormalised sum.
 template <class T, int D, int E, bool FEW>
 __device__ __forceinline__ void finish(const AttnArgs& a, const Work& w, int head, const Queries& qs, const SeqSpan& sp,
@@ -470,10 +470,8 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
 #pragma unroll
       for (int i = 1; i < 8; ++i) mx = fmaxf(mx, p[i]);
       mx = max_xor32(max_xor16(mx));
-      // The sums are rebased only where a maximum has grown by more than 2^8: until
-      // then weights go up to 2^8, which costs neither type any accuracy.
-      if (__any(mx > m + 8.0f)) {
-        const float mn = fmaxf(m, mx), f = fmaxf(rebase(m, mn), odd ? kLeast : 0.0f);
+      if (__any(mx > m + (kGrowth + T::kRaise))) {
+        const float mn = fmaxf(m, mx - T::kRaise), f = fmaxf(rebase(m, mn), odd ? kLeast : 0.0f);
 #pragma unroll
         for (int j = 0; j < kBlocks; ++j) o[j] *= f;
         l *= f;

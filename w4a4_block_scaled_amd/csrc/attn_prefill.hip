@@ -19,8 +19,8 @@
 // computes the scores of the next tile and the weighted sum of this one, and
 // between any two MFMAs stands a slice of the softmax, of the masks or of the
 // next copies, held there by scheduling barriers (the two in turn, as written
-// without them: 577 us on the ragged chunks; interleaved 507).  Maxima are
-// rebased only where they grew past 2^8, so the sums are rarely touched.
+// without them: 577 us on the ragged chunks; interleaved 507).  Sums are
+// rebased only where a maximum has grown by more than 2^8, so they are rarely touched.
 // Copies go straight to LDS: by buffer loads, which LDS reads do not wait for.
 //
 // The weights are rounded to 16 bits (bf16: the relative error is 1.9e-3 against
@@ -376,13 +376,11 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
       }
     }
   };
-  // Takes a tile's largest score into the running maximum.  The sums are rebased
-  // only where a maximum has grown by more than 2^8: until then weights go up to
-  // 2^8, which costs neither type any accuracy.
+  // Takes a tile's largest score into the reference of the weights.
   auto rebase_sums = [&](float mx) {
     mx = max_xor32(mx) * cs;
-    if (__any(mx > m + 8.0f)) {
-      const float mn = fmaxf(m, mx), f = fmaxf(rebase(m, mn), least);
+    if (__any(mx > m + (kGrowth + T::kRaise))) {
+      const float mn = fmaxf(m, mx - T::kRaise), f = fmaxf(rebase(m, mn), least);
 #pragma unroll
       for (int n = 0; n < kBlocks; ++n) o[n] *= f;
       l *= f;
@@ -664,7 +662,7 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(AttnArgs a, PrefillWo
   const int tok = w.group.div(row), qi = rt.first_token + tok;
   if (qi < 0 || qi >= w.tokens) return;
   const float* base = w.parts + int64_t(blockIdx.x) * w.splits * kBM * (D + 2);
-  // lane i looks after the splits i, i + 32: their maxima and sums of weights
+  // lane i looks after the splits i, i + 32: their references and sums of weights
   float f0 = kNegInf, f1 = kNegInf, L = 0.0f;
   const int64_t part = int64_t(kBM) * (D + 2);
   if (lane < used) f0 = base[lane * part + kBM * D + r];
