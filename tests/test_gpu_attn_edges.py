@@ -174,6 +174,40 @@ def test_inf_of_a_small_weight(way, kind, gap, rest, first):
     assert (y[:n][:, :, keep].float() - clean[:n][:, :, keep].float()).abs().max() <= 2.0 ** -6
 
 
+@pytest.mark.parametrize("way", ["whole", "whole, page 11"])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("gap", [30, 110, 200])
+@pytest.mark.parametrize("rest", ["all as small", "others large"])
+@pytest.mark.parametrize("first", [True, False])
+def test_inf_of_a_small_weight_in_row_tiles(way, kind, gap, rest, first):
+    """The same where the keys are whole: most tiles are seen whole by all rows."""
+    test_inf_of_a_small_weight(way, kind, gap, rest, first)
+
+
+@pytest.mark.parametrize("kind,dim,page", [("bf16", 128, 16), ("fp16", 256, 16), ("fp16", 64, 11)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 70)])
+def test_inf_and_nan_in_row_tiles(kind, dim, page, window, sinks):
+    """Row tiles with the keys whole: every row gets the Inf and NaN of the tokens
+    that it sees, both signs together as NaN, and no others; the rest as before."""
+    say(f"[inf] row tiles, {kind}, D = {dim}, page {page}, window {window}")
+    past, new, group = 700, 250, 4
+    c = chunks(kind, 1, group, dim, page, [past], [new], seed=dim)
+    clean, _ = run(c, window, sinks)
+    held = [(2, 3, INF), (65, 4, NAN), (100, 5, -INF), (640, 6, INF), (650, 6, -INF), (699, 7, INF), (720, 8, INF),
+            (760, 9, NAN), (800, 10, INF), (949, 11, -INF)]
+    for t, d, x in held:
+        c["vd"][(*place(c, 0, t), 0, d)] = x
+    y, _ = run(c, window, sinks)
+    want = clean.float()
+    for i in range(new):
+        p = past + i
+        for t, d, x in held:
+            if t <= p and (not window or t > p - window or t < sinks):
+                seen = want[i, :, d]
+                want[i, :, d] = torch.where(torch.isfinite(seen), torch.full_like(seen, x), seen + x)
+    assert torch.equal(torch.nan_to_num(y.float(), nan=12345.0), torch.nan_to_num(want, nan=12345.0))
+
+
 # ------------------------------------------- weights far below the largest --
 
 @pytest.mark.parametrize("way", [w for w in WAYS if "long" not in w])

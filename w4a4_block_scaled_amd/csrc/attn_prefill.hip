@@ -629,6 +629,69 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
     }
     return;
   }
+  // A whole tile's Inf goes through the product, where a weight that rounds to 0
+  // makes it NaN, and so does a rebase of its sum by 0.  So a sum that is not finite
+  // is made again from the Inf and NaN that its row sees: finite values do not matter
+  // beside them, and the largest one stands for a sum that has no other cause than
+  // its size.  (The wave's lanes look over 64 tokens at a time.)
+  if constexpr (!SPLIT && E == 2) {
+    constexpr float kLargest = 0x1.fffffep127f;
+    float zero[8];              // NaN if any sum is not finite
+#pragma unroll
+    for (int e = 0; e < 8; ++e) zero[e] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) zero[e & 7] = __builtin_fmaf(o[n][e], 0.0f, zero[e & 7]);
+#pragma unroll
+    for (int e = 4; e; e >>= 1)
+#pragma unroll
+      for (int k = 0; k < e; ++k) zero[k] += zero[k + e];
+    if (__any(zero[0] != 0.0f)) {
+#pragma unroll
+      for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (!(fabsf(o[n][e]) < -kNegInf)) o[n][e] = copysignf(kLargest, o[n][e]);
+#pragma unroll 1
+      for (int base = 0; base < hi; base += 64) {
+        const int t = base + lane;
+        const uint8_t* row = vbase;
+        bool met = false;
+        if (t < hi && (t >= low || t < a.sinks)) {
+          const int i = a.kv.page.div(t), p = table[i];
+          if (uint32_t(p) < uint32_t(a.kv.pages)) {
+            row += (int64_t(p) * a.kv.page_stride + int64_t(t - i * int(a.kv.page.d)) * a.kv.token_stride) * E;
+#pragma unroll 1
+            for (int c = 0; c < kChunks; ++c) {
+              const at_u32x4 x = *reinterpret_cast<const at_u32x4*>(row + 16 * c);
+              met |= T::not_finite(x[0]) || T::not_finite(x[1]) || T::not_finite(x[2]) || T::not_finite(x[3]);
+            }
+          }
+        }
+#pragma unroll 1
+        for (uint64_t todo = __ballot(met); todo; todo &= todo - 1) {
+          const int from = __ffsll((unsigned long long)todo) - 1;
+          const uint8_t* v = reinterpret_cast<const uint8_t*>(__shfl(reinterpret_cast<uintptr_t>(row), from));
+          const bool see = sees(base + from, hi);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            const at_u32x2 x = *reinterpret_cast<const at_u32x2*>(v + 16 * c + 8 * half);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float y = k & 1 ? T::high(x[k >> 1]) : T::low(x[k >> 1]);
+              if (see && !(fabsf(y) < -kNegInf)) o[c >> 2][4 * (c & 3) + k] += y;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (fabsf(o[n][e]) == kLargest) o[n][e] = copysignf(-kNegInf, o[n][e]);
+    }
+  }
   if (!valid) return;
   const int h = head * a.group + in_group;
   const bool none = pos < 0 && !rt.over;
