@@ -160,19 +160,12 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // 0 for a partial result without a visible token.
 __device__ __forceinline__ float rebase(float x, float m) { return x == kNegInf ? 0.0f : exp2_fast(x - m); }
 
-// o times that factor f.  Where f underflows to 0, a sum that is Inf stays Inf, as
-// with every positive weight; 0 x Inf would be NaN.  (E4M3, E = 1, has no Inf.)
-template <int E>
-__device__ __forceinline__ float rebased(float o, float x, float f) {
-  return E == 2 && f == 0.0f && x != kNegInf && !(fabsf(o) < -kNegInf) ? o : o * f;
-}
-template <int E>
-__device__ __forceinline__ at_f32x4 rebased(at_f32x4 o, float x, float f) {
-  return (at_f32x4){rebased<E>(o[0], x, f), rebased<E>(o[1], x, f), rebased<E>(o[2], x, f), rebased<E>(o[3], x, f)};
-}
-// The same inside the loops, where they have met Inf or NaN among the values: a
-// factor of at least this, the least positive value.  What it leaves of finite sums
-// is far below their rounding.
+// The least such factor of a sum that may be Inf, the least positive value: a factor
+// that underflows to 0 would make it NaN, and every positive weight makes Inf.  What
+// it leaves of a finite sum is far below the rounding of the others.
 constexpr float kLeast = 0x1p-149f;
+__device__ __forceinline__ float rebase_joined(float x, float m) {
+  return x == kNegInf ? 0.0f : fmaxf(exp2_fast(x - m), kLeast);
+}
 
 }  // namespace w4a4

@@ -607,9 +607,9 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
       at_f32x4 O = {0, 0, 0, 0};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float m1 = lds_m[w][r], f = rebase(m1, M);
+        const float f = rebase_joined(lds_m[w][r], M);
         L += f * lds_l[w][r];
-        O += rebased<E>(*reinterpret_cast<const at_f32x4*>(&lds_o[w][r][d]), m1, f);
+        O += *reinterpret_cast<const at_f32x4*>(&lds_o[w][r][d]) * f;
       }
       if (whole) {
         finish<T, D, E, FEW>(a, work, head, qs, sp, unit_row + r, d, M, L, O);
@@ -653,9 +653,9 @@ __global__ void __launch_bounds__(256) decode_join_kernel(AttnArgs a, Work work)
       const Partial p = partial_at(work, D, blockIdx.x + i, i == 0);
       const float m = p.m[r], l = p.l[r];
       const at_f32x4 o = *reinterpret_cast<const at_f32x4*>(p.o + r * D + 4 * quad);
-      const float mn = fmaxf(M, m), f = rebase(M, mn), h = rebase(m, mn);
+      const float mn = fmaxf(M, m), f = rebase_joined(M, mn), h = rebase_joined(m, mn);
       L = L * f + l * h;
-      O = rebased<E>(O, M, f) + rebased<E>(o, m, h);
+      O = O * f + o * h;
       M = mn;
     }
     __syncthreads();              // the row before has been read
@@ -671,9 +671,9 @@ __global__ void __launch_bounds__(256) decode_join_kernel(AttnArgs a, Work work)
     L = 0.0f;
     O = (at_f32x4){0, 0, 0, 0};
     for (int i = 0; i < kSplits; ++i) {
-      const float f = rebase(lds_m[i], M);
+      const float f = rebase_joined(lds_m[i], M);
       L += f * lds_l[i];
-      O += rebased<E>(lds_o[i][quad], lds_m[i], f);
+      O += lds_o[i][quad] * f;
     }
     finish<T, D, E, FEW>(a, work, head, qs, sp, unit_row + r, 4 * quad, M, L, O);
   }

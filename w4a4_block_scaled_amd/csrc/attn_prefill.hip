@@ -536,8 +536,11 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
         load(v_in, vbase, here, voff, raw_v);
       }
       at_f32x16 s[2], none[2];
+      // Inf is settled after the rebase by this tile's maximum (the first one's is by
+      // 0); E4M3 has NaN only, and holds fewer registers this way round.
+      if (E == 1) settle(v_cur, t, buf);
       if (busy) scores(k_cur, t, s);
-      settle(v_cur, t, buf);    // after the rebase by this tile's maximum: the first one's is by 0
+      if (E == 2) settle(v_cur, t, buf);
       if (busy) compute(k_cur, v_cur, t, s, none, std::false_type());
       if (more) {
         arrived();
@@ -733,9 +736,8 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(AttnArgs a, PrefillWo
   float M = fmaxf(f0, f1);
 #pragma unroll
   for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor(M, d));
-  const float m0 = f0, m1 = f1;
-  f0 = rebase(m0, M);
-  f1 = rebase(m1, M);
+  f0 = rebase_joined(f0, M);
+  f1 = rebase_joined(f1, M);
   if (lane < used) L = f0 * base[lane * part + kBM * (D + 1) + r];
   if (lane + 32 < used) L += f1 * base[(lane + 32) * part + kBM * (D + 1) + r];
 #pragma unroll
@@ -748,12 +750,11 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(AttnArgs a, PrefillWo
     for (int k = 0; k < 8; ++k) {                     // 8 splits' loads in flight
       const int i = min(i0 + k, used - 1);
       const float f = __shfl(i < 32 ? f0 : f1, (threadIdx.x & 32) + (i & 31));
-      const float m = __shfl(i < 32 ? m0 : m1, (threadIdx.x & 32) + (i & 31));
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
         const at_f32x2 x = *reinterpret_cast<const at_f32x2*>(base + i * part + r * D + 64 * j + 2 * lane);
-        O[2 * j] += i0 + k < used ? rebased<E>(x.x, m, f) : 0.0f;
-        O[2 * j + 1] += i0 + k < used ? rebased<E>(x.y, m, f) : 0.0f;
+        O[2 * j] += i0 + k < used ? f * x.x : 0.0f;
+        O[2 * j + 1] += i0 + k < used ? f * x.y : 0.0f;
       }
     }
   }
