@@ -469,7 +469,8 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs,
  * t <= p and (window == 0, or t > p - window, or t < sinks): with a window, the
  * last `window` tokens and the first `sinks` ones.  A sequence of length 0
  * sees nothing: out = 0, lse = -inf.  Masked tokens are left out of the sums
- * whatever they hold (Inf and NaN included).
+ * whatever they hold (Inf and NaN included); an Inf among the values that a query
+ * sees makes Inf however small its weight is.
  *
  *   dtype   W4A4_BF16 or W4A4_F16, of q and out: the cache's type, or either
  *           of them with an E4M3 cache.
@@ -482,9 +483,10 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs,
  *           w4a4_attn_decode_workspace_bytes() bytes, 16-byte aligned, no
  *           initial contents needed.
  *
- * Scores, softmax statistics and sums are fp32.  The work is split evenly over
- * the card by the sequences' visible lengths, read on the device; results do
- * not depend on timing.
+ * Scores, softmax statistics and sums are fp32, and the sums of weighted values
+ * are divided last: |V| times the visible tokens must stay below 2^119, or they
+ * may overflow to Inf.  The work is split evenly over the card by the sequences'
+ * visible lengths, read on the device; results do not depend on timing.
  */
 size_t w4a4_attn_decode_workspace_bytes(const w4a4_kv_cache* cache, int64_t seqs, int q_heads);
 w4a4_status w4a4_attn_decode(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, w4a4_dtype dtype, int q_heads,
@@ -500,10 +502,12 @@ w4a4_status w4a4_attn_decode(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seq
  * cu[s+1]-1 of q, at positions lens[s] - count .. lens[s] - 1; cu, tokens as in
  * w4a4_kv_append (cu must not be NULL).  A query at a negative position sees
  * nothing.  lse is fp32 [tokens x q_heads].  Where the rows are too few to fill the
- * card and the tables can hold long sequences, the keys are split as well.  The
- * softmax weights are rounded to `dtype` for the matrix cores, in two parts
- * (about 16 bits) where the keys are split or a kv head has up to 16 rows per
- * sequence, else in one; statistics and sums are fp32.
+ * card and the tables can hold long sequences (max_pages * page_size > 1000), the
+ * keys are split as well.  The softmax weights are rounded to `dtype` for the matrix
+ * cores, in two parts (about 16 bits) where the keys are split or a kv head has up
+ * to 16 rows per sequence on average, else in one: so the last bits of a sequence's
+ * outputs depend on the tables' width and on what else is in the call.
+ * Statistics and sums are fp32.
  */
 size_t w4a4_attn_prefill_workspace_bytes(const w4a4_kv_cache* cache, int64_t seqs, int64_t tokens, int q_heads);
 w4a4_status w4a4_attn_prefill(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, const int32_t* cu,

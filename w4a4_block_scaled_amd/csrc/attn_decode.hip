@@ -25,7 +25,7 @@
 // ragged batch of bf16, 810 MB, 158 us, 5.1 TB/s; three sequences of 90 to 131
 // thousand tokens in E4M3, 340 MB, 76 us (69 and 7 of the join); a window of
 // 1024 with sinks over 128 fp16 sequences, D = 64, 514 MB, 108 us, 4.8 TB/s; one
-// sequence of 2.1 MB 13.4 us: two launches of 7.4 and 2.8 us, and the calls.
+// sequence of 2.1 MB 12.4 to 13.6 us: two launches of 7.4 and 2.7 us, and the calls.
 #include <algorithm>
 #include <type_traits>
 
@@ -762,7 +762,10 @@ hipError_t launch_attn_decode(const AttnArgs& a, int cache_dtype, int dtype, int
 // them once.  Here / there, 8 sequences of 8000 tokens, 8 kv heads of 4, D = 128:
 // 2 tokens each, bf16 64.2 / 81.2 us, E4M3 43.6 / 65.3; 4 tokens (16 rows) 69.7 /
 // 80.6 and 48.2 / 66.5.  With two blocks of 16 rows for 8 tokens it gained
-// nothing over attn_prefill's 79.6 and 69.5.
+// nothing over attn_prefill's 79.6 and 69.5.  The average hides one long chunk among
+// sequences without new tokens, which either way serves alike where they are many:
+// 256 tokens on 8000 beside 63 of 1000, bf16, 169 / 172 us (alone, as row tiles with
+// the keys split, 74).
 bool attn_few_serves(int64_t seqs, int64_t tokens, int group, int page_size) {
   return page_size % 8 == 0 && tokens * group <= seqs * kRows;
 }

@@ -24,15 +24,15 @@
 // Copies go straight to LDS: by buffer loads, which LDS reads do not wait for.
 //
 // The weights are rounded to 16 bits (bf16: the relative error is 1.9e-3 against
-// 64 bits, of which the output's own rounding is 1.6e-3; a second part would
-// double the second product).  Where the keys are split the matrix cores are
-// idle, and two parts are taken, as in decoding.
+// 64 bits, of which the output's own rounding is 1.6e-3; fp16: 2.7e-4, of which
+// 2.0e-4; a second part would double the second product).  Where the keys are split
+// the matrix cores are idle, and two parts are taken, as in decoding.
 //
-// Measured, 32 / 8 heads, D = 128, causal 8192 bf16: 512 to 518 us, 1.07 PFLOP/s (a
-// library product of 8192^3 reaches 1.44 here; the MFMAs are busy 56% of the
-// time on the ragged chunks, at 1.65 GHz), E4M3 537 to 548 us, D = 64 320 to 327;
-// 4096 at D = 256 333 to 338 us.  Ragged chunks over 28 / 4 heads, 526 GFLOP:
-// 491 to 509 us.  82 tokens: 10.5 us, 8.4 of them the kernel's.
+// Measured, 32 / 8 heads, D = 128, causal 8192 bf16: 512 to 528 us, 1.05 PFLOP/s (a
+// library product of 8192^3 reaches 1.44 here; the MFMAs are busy 55% of the
+// time on the ragged chunks, at 1.65 GHz), E4M3 537 to 557 us, D = 64 320 to 337;
+// 4096 at D = 256 332 to 346 us.  Ragged chunks over 28 / 4 heads, 526 GFLOP:
+// 491 to 514 us.  82 tokens: 10.5 us, 8.7 of them the kernel's.
 #include <algorithm>
 #include <type_traits>
 
@@ -776,8 +776,11 @@ int64_t row_tiles(int64_t seqs, int64_t tokens, int group) { return tokens * gro
 // on 8000 bf16 tokens 151.7 / 92.4).  Workspace is given for this many; tables that
 // hold kNoSplit tokens at most are not split, since the second launch and the
 // partial results cost what 15 steps of 64 tokens do: split / not split, a
-// prompt of 82 tokens 15.3 / 11.0 us, of 800 34.7 / 22.1, 16 tokens after 700
-// 19.5 / 18.8, after 1000 19.3 / 21.8.
+// prompt of 82 tokens 13.8 / 10.7 us, of 800 33.7 / 21.3, 16 tokens after 700
+// 19.5 / 18.8, after 1000 19.3 / 21.8.  Not split, the weights enter as one part.
+// (The host knows the tables' width, not the lengths: a short prompt in wide tables
+// is split, and where sequences without new tokens bring row tiles enough nothing is:
+// 64 tokens on 8000 beside 63 such sequences 166 us, alone 40.)
 constexpr int kNoSplit = 1000;
 int key_splits(int64_t tiles, int heads) {
   const int64_t wgs = tiles * heads;
