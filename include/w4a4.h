@@ -402,7 +402,8 @@ w4a4_status w4a4_dualquant_solve(w4a4_format fmt, int64_t N, int64_t K,
  * included.  Several layers have a cache each and share tables and lens.
  *
  * Element types: BF16 and FP16, or E4M3 (OCP FP8) with one positive fp32 scale
- * per head for K and for V (NULL: 1): a stored code stands for code * scale.
+ * per head for K and for V (NULL: 1): a stored code stands for code * scale; or
+ * E2M1 with block scales, whose pages are laid out by themselves (W4A4_E2M1).
  *
  * tables, lens and the other index arrays are device memory that the host
  * never reads, so their contents cannot be refused by a status.  Nothing is
@@ -414,7 +415,26 @@ w4a4_status w4a4_dualquant_solve(w4a4_format fmt, int64_t N, int64_t K,
  * Counts are int32 on the device: at most 2^30 sequences and list entries, and
  * fewer than 2^31 - 256 rows times query heads (W4A4_ERR_SHAPE beyond).
  */
-typedef enum { W4A4_BF16 = 0, W4A4_F16 = 1, W4A4_E4M3 = 2 } w4a4_dtype;
+typedef enum { W4A4_BF16 = 0, W4A4_F16 = 1, W4A4_E4M3 = 2, W4A4_E2M1 = 4 } w4a4_dtype;
+
+/*
+ * W4A4_E2M1 - a cache in MXFP4 (E2M1 codes, an E8M0 scale for every 32 values of
+ * a head's row): 17/32 of a byte per value.  A page is
+ *
+ *   codes   [heads][page_size][head_dim / 2]   bytes, value 2j of a row in the low
+ *           nibble of byte j, value 2j + 1 in the high one
+ *   scales  [heads][head_dim / 32][page_size]  bytes b behind them: 2^(b - 127), NaN
+ *           for 255
+ *
+ * w4a4_kv_page_bytes() bytes long, K and V alike.  page_stride is in bytes, a
+ * multiple of 16 and no less than a page; token_stride and head_stride are 0,
+ * k_scale and v_scale NULL.  Any bytes are valid contents.  Rows are stored by
+ * the rule of w4a4_quantize_act's MXFP4 (block exponent floor(log2 amax) - 2, codes
+ * to nearest even, saturating at 6; a block with Inf or NaN gets byte 255 and zero
+ * codes), from FP16 rows with exponents up to 13 (byte 140), so that what is stored
+ * stays within FP16.  Attention in FP16, and reading out in it, take scales up to
+ * that; larger ones give Inf or NaN.
+ */
 
 typedef struct {
   void* k;                 /* device, 16-byte aligned                            */
@@ -422,7 +442,7 @@ typedef struct {
   const float* k_scale;    /* device, fp32 [heads]; E4M3 only, NULL means 1      */
   const float* v_scale;
   int64_t page_stride;     /* elements; page, token and head strides are         */
-  int64_t token_stride;    /*   multiples of 16 bytes                            */
+  int64_t token_stride;    /*   multiples of 16 bytes (W4A4_E2M1: see there)     */
   int64_t head_stride;
   int32_t dtype;           /* w4a4_dtype                                         */
   int32_t pages;
@@ -439,6 +459,10 @@ typedef struct {
   int32_t max_pages;
 } w4a4_kv_seqs;
 
+/* Bytes of a page of W4A4_E2M1, without padding (0 for invalid arguments; head_dim
+ * 64, 128 or 256). */
+size_t w4a4_kv_page_bytes(int page_size, int heads, int head_dim);
+
 /*
  * w4a4_kv_append - store the keys and values of new tokens.
  *
@@ -447,7 +471,7 @@ typedef struct {
  *           count .. lens[s] - 1).  NULL: one row per sequence.
  *   tokens  rows of k and v (cu[seqs]; seqs if cu is NULL).
  *   dtype   W4A4_BF16 or W4A4_F16, the type of k and v: the cache's own, or
- *           either of them for an E4M3 cache.
+ *           either of them for an E4M3 or E2M1 cache.
  *   k, v    device, 16-byte aligned, heads x head_dim values per row; rows and
  *           heads at the given strides (elements, multiples of 8), so that the
  *           slices of a fused projection's output serve as they are.
@@ -458,6 +482,78 @@ typedef struct {
 w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, const int32_t* cu,
                            int64_t tokens, w4a4_dtype dtype, const void* k, int64_t k_row, int64_t k_head,
                            const void* v, int64_t v_row, int64_t v_head, void* stream);
+
+/*
+ * Rotary positions.  The first rot_dim values of a head's row are rot_dim / 2
+ * pairs (a, b): (i, i + rot_dim / 2), or (2i, 2i + 1) with `interleaved`.  At
+ * position p pair i becomes
+ *
+ *   factor * (a cos t - b sin t),  factor * (a sin t + b cos t),  t = p * freqs[i]
+ *
+ * with -t for t if `inverse` (with the same factor the gradient of the rotation).
+ * The other values stay as they are.  freqs holds what the kind of positions asks
+ * for: base^(-2i / rot_dim), compressed or stretched by parts for long contexts.
+ * Angles are taken from the exact p * freqs[i] in 64 bits, cos and sin to 2^-48; the
+ * products are fp32 where the result is a 16-bit value (rounded once), fp64 where it
+ * is rounded to 8 or 4 bits.
+ */
+typedef struct {
+  const float* freqs;      /* device, fp32 [rot_dim / 2], 4-byte aligned         */
+  int32_t rot_dim;         /* even, 2 .. the row's width                         */
+  int32_t interleaved;     /* 0 or 1                                             */
+  int32_t inverse;         /* 0 or 1                                             */
+  float factor;            /* of the rotated values; positive and finite         */
+} w4a4_rotation;
+
+/*
+ * w4a4_rope - rotate rows by their positions.
+ *
+ *   positions  device, int32 [tokens], any values, one for all heads of a row.
+ *   dtype      W4A4_BF16 or W4A4_F16, of x and out.
+ *   x, out     device, 16-byte aligned, [tokens, heads, head_dim] at the given row
+ *              and head strides (elements, multiples of 8).  out is x itself with
+ *              the same strides, or does not overlap it.  The queries and keys of a
+ *              fused projection's row are one x.
+ *   head_dim   a multiple of 8, 8 .. 512.
+ */
+w4a4_status w4a4_rope(const w4a4_rotation* rotation, int64_t tokens, const int32_t* positions, w4a4_dtype dtype,
+                      int heads, int head_dim, const void* x, int64_t x_row, int64_t x_head, void* out, int64_t o_row,
+                      int64_t o_head, void* stream);
+
+/*
+ * w4a4_kv_append_rope - rotate the queries and keys of new tokens and store keys
+ * and values, as w4a4_rope and w4a4_kv_append in one launch and with one rounding:
+ * what is stored in 8 or 4 bits comes from the unrounded rotated keys.
+ *
+ *   cu, tokens, dtype, k, v: as in w4a4_kv_append (E4M3: code = RNE_E4M3(x / scale)
+ *              of the fp64 quotient).
+ *   positions  device, int32 [tokens]: what q and k are rotated by; NULL: their
+ *              places in their sequences (lens[s] - count + i).  Where rows are
+ *              stored goes by the places alone.
+ *   q, q_out   device, [tokens, q_heads, head_dim], as x and out of w4a4_rope;
+ *              q_heads 0: none.  Rows of tokens that belong to no sequence are left as
+ *              they were.  q_out does not overlap k or v.
+ */
+w4a4_status w4a4_kv_append_rope(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, const int32_t* cu,
+                                int64_t tokens, w4a4_dtype dtype, const w4a4_rotation* rotation,
+                                const int32_t* positions, int q_heads, const void* q, int64_t q_row, int64_t q_head,
+                                void* q_out, int64_t o_row, int64_t o_head, const void* k, int64_t k_row,
+                                int64_t k_head, const void* v, int64_t v_row, int64_t v_head, void* stream);
+
+/*
+ * w4a4_kv_read - the rows of each sequence's last tokens out of the cache, in 16
+ * bits: what w4a4_kv_append with the same cu stores, as the cache holds it.
+ *
+ *   cu, tokens as in w4a4_kv_append.
+ *   dtype      W4A4_BF16 or W4A4_F16, of k and v: the cache's type, or either of
+ *              them for an E4M3 or E2M1 cache.
+ *   k, v       device, out, 16-byte aligned, at the given strides (multiples of 8).
+ *
+ * Rows without a valid page are NaN; those of no sequence are left as they were.
+ */
+w4a4_status w4a4_kv_read(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, const int32_t* cu, int64_t tokens,
+                         w4a4_dtype dtype, void* k, int64_t k_row, int64_t k_head, void* v, int64_t v_row,
+                         int64_t v_head, void* stream);
 
 /*
  * w4a4_attn_decode - attention of one new token per sequence over the cache.
@@ -473,7 +569,7 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs,
  * sees makes Inf however small its weight is.
  *
  *   dtype   W4A4_BF16 or W4A4_F16, of q and out: the cache's type, or either
- *           of them with an E4M3 cache.
+ *           of them with an E4M3 or E2M1 cache.
  *   q_heads a multiple of cache->heads.
  *   q, out  device, 16-byte aligned, [seqs, q_heads, head_dim] at the given row
  *           and head strides (elements, multiples of 8).

@@ -12,7 +12,7 @@ without the ``w4a4_`` prefix:
 
 The paged key-value cache and the attention between the linears:
 
-    kv_append(k, v, k_cache, v_cache, tables, lens)
+    q = kv_append_rope(q, k, v, k_cache, v_cache, tables, lens, freqs)
     out = attn_decode(q, k_cache, v_cache, tables, lens)
 
 There is no fallback: if the library is missing or fails to load, the
@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 from typing import Optional, Tuple
 
@@ -30,7 +31,7 @@ import torch
 __all__ = ["FORMATS", "lib", "library_path", "block_size", "scale_dtype", "quantize_act", "pack_weight",
            "unpack_weight", "linear", "linear_noalloc", "linear_workspace", "packed_weight_bytes", "W4A4Error",
            "attn_decode", "attn_prefill", "kv_append", "kv_copy_pages", "kv_reserve", "kv_fork", "kv_free", "kv_trim",
-           "kv_compact"]
+           "kv_compact", "kv_append_rope", "kv_read", "kv_cache_e2m1", "rope", "rope_freqs"]
 
 FORMATS = {"mxfp4": 0, "nvfp4": 1, "mxint4": 2, "int4g64": 3, "mxfp8": 4, "mxint8": 5, "int8g128": 6}
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -56,6 +57,11 @@ class _KvCache(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("pages", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("factor", ctypes.c_float)]
 
 
 class _KvSeqs(ctypes.Structure):
@@ -122,7 +128,14 @@ def lib() -> ctypes.CDLL:
     L.w4a4_kv_free.argtypes = [sp, vp, i32, vp, i32, vp]
     L.w4a4_kv_trim.argtypes = [sp, i32, vp, i32, vp, i32, i32, i32, vp]
     L.w4a4_kv_compact.argtypes = [i32, vp, i64, i64, sp, vp, i32, vp, vp, sz, vp]
-    for name in ("kv_append", "attn_decode", "attn_prefill", "kv_copy_pages", "kv_reserve", "kv_fork", "kv_free",
+    rp = ctypes.POINTER(_Rotation)
+    L.w4a4_kv_page_bytes.argtypes = [i32, i32, i32]
+    L.w4a4_kv_page_bytes.restype = sz
+    L.w4a4_rope.argtypes = [rp, i64, vp, i32, i32, i32, vp, i64, i64, vp, i64, i64, vp]
+    L.w4a4_kv_append_rope.argtypes = [cp, sp, vp, i64, i32, rp, vp, i32, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp,
+                                      i64, i64, vp]
+    L.w4a4_kv_read.argtypes = [cp, sp, vp, i64, i32, vp, i64, i64, vp, i64, i64, vp]
+    for name in ("rope", "kv_append_rope", "kv_read", "kv_append", "attn_decode", "attn_prefill", "kv_copy_pages", "kv_reserve", "kv_fork", "kv_free",
                  "kv_trim", "kv_compact"):
         getattr(L, "w4a4_" + name).restype = i32
     L.w4a4_last_error.argtypes = []
@@ -387,7 +400,9 @@ def probe_empty(device) -> None:
 #
 #   k_cache, v_cache  [pages, page_size, heads, head_dim], the last dimension
 #                     contiguous, the others in any order in memory (the same
-#                     for both); bfloat16, float16 or float8_e4m3fn
+#                     for both); bfloat16, float16 or float8_e4m3fn; or uint8, a
+#                     cache in 4 bits: [pages, page_size, heads, head_dim * 17 / 32]
+#                     bytes, pages laid out as W4A4_E2M1 says (see kv_cache_e2m1)
 #   k_scale, v_scale  fp32 [heads] or None (1): a stored E4M3 value stands for
 #                     value * scale
 #   tables            int32 [seqs, max_pages]: page of the tokens page_size * j ..
@@ -396,13 +411,13 @@ def probe_empty(device) -> None:
 #   caches            tensors of pages [..., pages, page_size, heads, head_dim], or
 #                     one such tensor (leading dimensions: layers, K and V)
 
-_KV_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+_KV_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2, torch.uint8: 4}
 
 
 def _kv_type(t: torch.Tensor, what: str) -> int:
     f = _KV_TYPES.get(t.dtype)
     if f is None:
-        raise W4A4Error(4, f"{what}: type {t.dtype} (bfloat16, float16 or float8_e4m3fn)")
+        raise W4A4Error(4, f"{what}: type {t.dtype} (bfloat16, float16, or of a cache float8_e4m3fn or uint8)")
     return f
 
 
@@ -436,6 +451,13 @@ def _kv_cache(what: str, k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> 
     elif k_scale is not None or v_scale is not None:
         raise W4A4Error(4, f"{what}: scales belong to a float8_e4m3fn cache")
     pages, page, heads, dim = shape
+    if f == 4:
+        size = page * heads * dim
+        if dim % 17 or (heads > 1 and stride[2] != dim) or (page > 1 and stride[1] != heads * dim):
+            raise W4A4Error(2, f"{what}: a 4-bit cache is [pages, page_size, heads, head_dim * 17 / 32] bytes, each page "
+                               f"contiguous, not {tuple(shape)} with strides {tuple(stride)}")
+        return _KvCache(k.data_ptr(), v.data_ptr(), None, None, stride[0] if pages > 1 else -(-size // 16) * 16, 0, 0, f,
+                        pages, page, heads, dim // 17 * 32)
     return _KvCache(k.data_ptr(), v.data_ptr(), ks, vs, stride[0], stride[1], stride[2], f, pages, page, heads, dim)
 
 
@@ -472,7 +494,8 @@ def _kv_stream(device: torch.device) -> int:
 def _attn_workspace_bytes(prefill: bool, dtype: int, page: int, heads: int, dim: int, seqs: int, tokens: int,
                           q_heads: int) -> int:
     """w4a4_attn_*_workspace_bytes: depends on these numbers alone."""
-    c = _KvCache(16, 16, None, None, 0, 0, 0, dtype, 1, page, heads, dim)
+    stride = lib().w4a4_kv_page_bytes(page, heads, dim) + 15 & ~15 if dtype == 4 else 0
+    c = _KvCache(16, 16, None, None, stride, 0, 0, dtype, 1, page, heads, dim)
     return (lib().w4a4_attn_prefill_workspace_bytes(c, seqs, tokens, q_heads) if prefill else
             lib().w4a4_attn_decode_workspace_bytes(c, seqs, q_heads))
 
@@ -501,6 +524,165 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
             raise W4A4Error(2, f"kv_append: cu_seqlens has {cu_seqlens.numel()} entries for {s.seqs} sequences")
         cu = cu_seqlens.data_ptr()
     _check(lib().w4a4_kv_append(c, s, cu, tokens, _kv_type(k, "kv_append"), *rows, _kv_stream(dev)))
+
+
+def kv_cache_e2m1(pages, page_size: int, heads: int, head_dim: int, device="cuda") -> torch.Tensor:
+    """An empty 4-bit cache, uint8 [*pages, page_size, heads, head_dim * 17 / 32]; pages: their number, or a
+    shape that ends with it, e.g. (layers, 2, pages) for K and V of all layers.  Pages
+    begin at multiples of 16 bytes, so they may have gaps between them."""
+    lead = (pages,) if isinstance(pages, int) else tuple(pages)
+    size = lib().w4a4_kv_page_bytes(page_size, heads, head_dim)
+    if size == 0:
+        raise W4A4Error(2, f"kv_cache_e2m1: page_size={page_size} heads={heads} head_dim={head_dim}")
+    store = torch.zeros((*lead, -(-size // 16) * 16), dtype=torch.uint8, device=device)
+    width = head_dim // 32 * 17
+    return store.as_strided((*lead, page_size, heads, width), (*store.stride()[:-1], heads * width, width, 1))
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", scale: float = 1.0,
+               original: int = 0, low: float = 1.0, high: float = 4.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+               device="cuda"):
+    """(freqs float32 [rot_dim / 2], factor) of rotary positions: base^(-2 i / rot_dim) radians per position, and
+
+    scaling "linear"  freqs / scale: positions compressed by `scale`
+            "ntk"     base * scale^(rot_dim / (rot_dim - 2)): the slowest pair is stretched by `scale`, the
+                      fastest not at all
+            "bands"   by the turns that a pair makes over `original` positions: more than `high` as they are,
+                      fewer than `low` divided by `scale`, between them a linear blend of the two
+            "yarn"    between the pairs that make beta_fast and beta_slow turns over `original` positions a
+                      linear ramp (over the pairs' numbers) from as they are to divided by `scale`; factor
+                      0.1 ln(scale) + 1
+    """
+    if rot_dim < 2 or rot_dim % 2 or not base > 0 or not scale > 0:
+        raise W4A4Error(2, f"rope_freqs: rot_dim={rot_dim} base={base} scale={scale}")
+    if scaling in ("bands", "yarn") and original < 1:
+        raise W4A4Error(2, f"rope_freqs: {scaling} needs the original number of positions, not {original}")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise W4A4Error(2, "rope_freqs: ntk needs two pairs")
+        base = base * scale ** (rot_dim / (rot_dim - 2))
+    f, factor = base ** (-i / rot_dim), 1.0
+    if scaling == "linear":
+        f = f / scale
+    elif scaling == "bands":
+        if not high > low:
+            raise W4A4Error(2, f"rope_freqs: bands from {low} to {high} turns")
+        keep = ((original * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * keep + f / scale * (1 - keep)
+    elif scaling == "yarn":
+        if not beta_fast > beta_slow > 0 or not base > 1:
+            raise W4A4Error(2, f"rope_freqs: beta_fast={beta_fast} beta_slow={beta_slow} base={base}")
+        # the pair (as a real number) that makes n turns over the original positions
+        at = [rot_dim * math.log(original / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (beta_fast, beta_slow)]
+        first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot_dim - 1)
+        ramp = ((i / 2 - first) / max(last - first, 1e-3)).clamp(0, 1)
+        f, factor = f * (1 - ramp) + f / scale * ramp, 0.1 * math.log(scale) + 1.0 if scale > 1 else 1.0
+    elif scaling not in ("none", "ntk"):
+        raise W4A4Error(2, f"rope_freqs: scaling {scaling!r} (none, linear, ntk, bands or yarn)")
+    return f.to(torch.float32).to(device), factor
+
+
+def _rotation(what: str, freqs: torch.Tensor, interleaved, inverse, factor, device) -> _Rotation:
+    if freqs.dtype != torch.float32 or freqs.dim() != 1 or not freqs.is_contiguous() or freqs.device != device:
+        raise W4A4Error(2, f"{what}: freqs are contiguous float32 [rot_dim / 2] on {device}")
+    return _Rotation(freqs.data_ptr(), 2 * freqs.shape[0], bool(interleaved), bool(inverse), factor)
+
+
+def _positions(what: str, positions: Optional[torch.Tensor], tokens: int, device) -> Optional[int]:
+    if positions is None:
+        return None
+    _int32(what, device, positions)
+    if positions.numel() != tokens:
+        raise W4A4Error(2, f"{what}: {positions.numel()} positions for {tokens} rows")
+    return positions.data_ptr()
+
+
+def _like_rows(what: str, out: Optional[torch.Tensor], x: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.dtype != x.dtype:
+        raise W4A4Error(4, f"{what} is {out.dtype}, its input {x.dtype}")
+    return out
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, interleaved: bool = False,
+         factor: float = 1.0, inverse: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """w4a4_rope: rows x [tokens, heads, head_dim] (any row and head strides) rotated by their positions
+    (int32 [tokens]) over their first 2 * len(freqs) values; freqs and factor as from
+    rope_freqs.  interleaved: pairs (2i, 2i + 1) instead of halves.  inverse: back, or a
+    gradient.  out: x itself (in place), or other memory."""
+    dev = x.device
+    r = _rotation("rope", freqs, interleaved, inverse, factor, dev)
+    if x.dim() != 3:
+        raise W4A4Error(2, f"rope: x {tuple(x.shape)} (need [tokens, heads, head_dim])")
+    tokens, heads, dim = x.shape
+    at = _positions("rope", positions, tokens, dev)
+    out = _like_rows("rope: out", out, x)
+    rows = (*_kv_rows("rope: x", x, tokens, None, dim, dev), *_kv_rows("rope: out", out, tokens, heads, dim, dev))
+    _check(lib().w4a4_rope(r, tokens, at, _kv_type(x, "rope"), heads, dim, *rows, _kv_stream(dev)))
+    return out
+
+
+def kv_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, freqs: torch.Tensor, *,
+                   cu_seqlens: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                   interleaved: bool = False, factor: float = 1.0, k_scale: Optional[torch.Tensor] = None,
+                   v_scale: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None):
+    """w4a4_kv_append_rope: kv_append of keys rotated as by rope(), with the queries [tokens, q_heads,
+    head_dim] (or None) rotated into the result, q_out or a new tensor.
+
+    positions int32 [tokens]: what is rotated by; None: the tokens' places in their sequences.
+    """
+    name, dev = "kv_append_rope", k_cache.device
+    c = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
+    s = _kv_seqs(name, tables, lens, dev)
+    r = _rotation(name, freqs, interleaved, False, factor, dev)
+    tokens, dim = k.shape[0], c.head_dim
+    rows = (*_kv_rows(name + ": k", k, tokens, c.heads, dim, dev), *_kv_rows(name + ": v", v, tokens, c.heads, dim, dev))
+    if k.dtype != v.dtype or (q is not None and q.dtype != k.dtype):
+        raise W4A4Error(4, f"{name}: k is {k.dtype}, v is {v.dtype}{'' if q is None else f', q is {q.dtype}'}")
+    at = _positions(name, positions, tokens, dev)
+    cu = None if cu_seqlens is None else _cu(name, cu_seqlens, s.seqs, dev)
+    q_rows, heads, out = (None, 0, 0, None, 0, 0), 0, None
+    if q is not None:
+        q_at = _kv_rows(name + ": q", q, tokens, None, dim, dev)
+        heads, out = q.shape[1], _like_rows(name + ": q_out", q_out, q)
+        q_rows = (*q_at, *_kv_rows(name + ": q_out", out, tokens, heads, dim, dev))
+    elif q_out is not None:
+        raise W4A4Error(2, f"{name}: q_out without q")
+    _check(lib().w4a4_kv_append_rope(c, s, cu, tokens, _kv_type(k, name), r, at, heads, *q_rows, *rows, _kv_stream(dev)))
+    return out
+
+
+def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor,
+            cu_seqlens: Optional[torch.Tensor], tokens: int, *, dtype: torch.dtype = torch.bfloat16,
+            k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None, out=None):
+    """w4a4_kv_read: (k, v) [tokens, heads, head_dim] of `dtype`: the rows that kv_append with the same
+    cu_seqlens (tokens: its last entry; None: one row per sequence) stores, as the
+    cache holds them.  out: (k, v) to write into."""
+    name, dev = "kv_read", k_cache.device
+    c = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
+    s = _kv_seqs(name, tables, lens, dev)
+    cu = None if cu_seqlens is None else _cu(name, cu_seqlens, s.seqs, dev)
+    if tokens < 0:
+        raise W4A4Error(2, f"{name}: {tokens} tokens")
+    if out is None:
+        out = tuple(torch.empty((tokens, c.heads, c.head_dim), dtype=dtype, device=dev) for _ in range(2))
+    k, v = out
+    if k.dtype != dtype or v.dtype != dtype:
+        raise W4A4Error(4, f"{name}: out is {k.dtype} and {v.dtype}, not {dtype}")
+    rows = (*_kv_rows(name + ": k", k, tokens, c.heads, c.head_dim, dev),
+            *_kv_rows(name + ": v", v, tokens, c.heads, c.head_dim, dev))
+    _check(lib().w4a4_kv_read(c, s, cu, tokens, _kv_type(k, name), *rows, _kv_stream(dev)))
+    return k, v
+
+
+def _cu(what: str, cu: torch.Tensor, seqs: int, device) -> int:
+    _int32(what, device, cu)
+    if cu.numel() != seqs + 1:
+        raise W4A4Error(2, f"{what}: cu_seqlens has {cu.numel()} entries for {seqs} sequences")
+    return cu.data_ptr()
 
 
 def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, scale, window, sinks, out, return_lse,

@@ -59,6 +59,8 @@ constexpr float kGrowth = 8.0f;
 // per lane.
 struct Bf16 {
   static constexpr uint32_t kExp = 0x7f80u, kOne = 0x3f80u;      // the exponent of Inf and NaN; 1.0
+  static constexpr uint32_t kNanPair = 0x7fc07fc0u;
+  static constexpr int kFp4Exp = 127;             // largest exponent of a 4-bit block stored from this type
   static constexpr float kRaise = 0.0f;
   static __device__ __forceinline__ bool not_finite(uint32_t u) { return has_odd<kExp>(u); }
   static __device__ __forceinline__ uint32_t finite(uint32_t u) { return without_odd<kExp>(u); }
@@ -74,6 +76,10 @@ struct Bf16 {
   static __device__ __forceinline__ x2 from_e4m3(uint32_t u) {
     return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u, 1.0f, HI);
   }
+  template <int B>
+  static __device__ __forceinline__ x2 from_fp4(uint32_t u, float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, scale, B);
+  }
   static __device__ __forceinline__ float low(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
   static __device__ __forceinline__ float high(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
   static __device__ __forceinline__ at_f32x4 mfma16(at_u32x4 a, at_u32x4 b, at_f32x4 c) {
@@ -85,6 +91,8 @@ struct Bf16 {
 };
 struct F16 {
   static constexpr uint32_t kExp = 0x7c00u, kOne = 0x3c00u;      // the exponent of Inf and NaN; 1.0
+  static constexpr uint32_t kNanPair = 0x7e007e00u;
+  static constexpr int kFp4Exp = 13;              // so that 6 * 2^13 stays in range
   static constexpr float kRaise = 7.0f;
   static __device__ __forceinline__ bool not_finite(uint32_t u) { return has_odd<kExp>(u); }
   static __device__ __forceinline__ uint32_t finite(uint32_t u) { return without_odd<kExp>(u); }
@@ -99,6 +107,10 @@ struct F16 {
   template <bool HI>
   static __device__ __forceinline__ x2 from_e4m3(uint32_t u) {
     return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, HI);
+  }
+  template <int B>
+  static __device__ __forceinline__ x2 from_fp4(uint32_t u, float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, scale, B);
   }
   static __device__ __forceinline__ float low(uint32_t u) {
     return float(__builtin_bit_cast(x2, u).x);
@@ -119,6 +131,14 @@ template <class T, bool HI>
 __device__ __forceinline__ uint32_t e4m3_pair(uint32_t u) {
   return __builtin_bit_cast(uint32_t, T::template from_e4m3<HI>(u));
 }
+
+// The two E2M1 codes of byte B of u times a block's scale, as two elements of T;
+// the scale is 2^(byte - 127), NaN for byte 255.
+template <class T, int B>
+__device__ __forceinline__ uint32_t fp4_pair(uint32_t u, float scale) {
+  return __builtin_bit_cast(uint32_t, T::template from_fp4<B>(u, scale));
+}
+__device__ __forceinline__ float fp4_scale(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
 
 // x of the lanes l and l ^ 32 (l ^ 16), in either order: halves (odd and even
 // quarters) of two registers change places.

@@ -164,6 +164,97 @@ struct Tile {
   }
 };
 
+// The same of 32 tokens held in 4 bits: codes, and the scale bytes of the blocks that
+// they lie in.  A lane's keys are a block (D = 64: half of one), so that one scale
+// serves all steps of a load.
+template <class T, int D, bool OCT>
+struct Fp4Tile {
+  static constexpr int kSteps = D / 32;
+  static constexpr int kRun = D >= 128 ? 8 : 4;
+  static constexpr int kRuns = D / 16 / kRun;
+  static constexpr int kLoads = D >= 128 ? D / 128 : 1;        // of a lane's keys: 16 bytes each (D = 64: 8)
+  static constexpr int kDwords = D >= 128 ? 4 : 2;             // of a load: steps
+
+  uint32_t k[2][kLoads][kDwords];
+  uint32_t ks[2][kLoads];
+  uint32_t v[8][kRuns];
+  uint32_t vs[kRuns][OCT ? 2 : 8];      // bytes of 4 tokens each, or of one
+
+  // First d of the 8 that quarter g holds of step j.
+  static __device__ __forceinline__ int key_dim(int j, int g) {
+    return 128 * (j / kDwords) + (D / (4 * kLoads)) * g + 8 * (j % kDwords);
+  }
+  static __device__ __forceinline__ int key_block(int i, int g) { return D == 64 ? g >> 1 : 4 * i + g; }
+  static __device__ __forceinline__ int value_block(int r, int c) { return D == 64 ? c >> 3 : 4 * r + (c >> 2); }
+
+  __device__ __forceinline__ void load_k(int b, const uint8_t* row, const uint8_t* scale, int page, int g) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      if constexpr (D == 64) {
+        const at_u32x2 x = *reinterpret_cast<const at_u32x2*>(row + 8 * g);
+        k[b][i][0] = x.x;
+        k[b][i][1] = x.y;
+      } else {
+        const at_u32x4 x = *reinterpret_cast<const at_u32x4*>(row + 64 * i + 16 * g);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) k[b][i][w] = x[w];
+      }
+      ks[b][i] = scale[key_block(i, g) * page];
+    }
+  }
+  __device__ __forceinline__ void load_v(int i, const uint8_t* row, int c) {
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) {
+      if constexpr (D == 64) v[i][r] = *reinterpret_cast<const uint16_t*>(row + 2 * c);
+      else v[i][r] = *reinterpret_cast<const uint32_t*>(row + 64 * r + 4 * c);
+    }
+  }
+  // of 8 tokens (OCT), or of token i
+  __device__ __forceinline__ void load_vs(int i, const uint8_t* scale, int page, int c) {
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) {
+      const uint8_t* p = scale + value_block(r, c) * page;
+      if constexpr (OCT) {
+        const at_u32x2 x = *reinterpret_cast<const at_u32x2*>(p);
+        vs[r][0] = x.x;
+        vs[r][1] = x.y;
+      } else {
+        vs[r][i] = *p;
+      }
+    }
+  }
+  __device__ __forceinline__ void clear_v(int i) {
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) {
+      v[i][r] = 0;
+      if constexpr (OCT) vs[r][i >> 2] &= ~(0xffu << 8 * (i & 3));
+      else vs[r][i] = 0;
+    }
+  }
+
+  __device__ __forceinline__ at_u32x4 key(int b, int j) const {
+    const uint32_t x = k[b][j / kDwords][j % kDwords];
+    const float s = fp4_scale(ks[b][j / kDwords]);
+    return (at_u32x4){fp4_pair<T, 0>(x, s), fp4_pair<T, 1>(x, s), fp4_pair<T, 2>(x, s), fp4_pair<T, 3>(x, s)};
+  }
+  template <int B>
+  __device__ __forceinline__ uint32_t value_pair(int i, int r) const {
+    return fp4_pair<T, B>(v[i][r], fp4_scale(OCT ? vs[r][i >> 2] >> 8 * (i & 3) & 0xffu : vs[r][i]));
+  }
+  __device__ __forceinline__ void values(int r, int j, at_u32x4* lo, at_u32x4* hi) const {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      uint32_t x, y;
+      if (j == 0) x = value_pair<0>(2 * t, r), y = value_pair<0>(2 * t + 1, r);
+      else if (j == 2) x = value_pair<1>(2 * t, r), y = value_pair<1>(2 * t + 1, r);
+      else if (j == 4) x = value_pair<2>(2 * t, r), y = value_pair<2>(2 * t + 1, r);
+      else x = value_pair<3>(2 * t, r), y = value_pair<3>(2 * t + 1, r);
+      (*lo)[t] = __builtin_amdgcn_perm(y, x, 0x05040100);
+      (*hi)[t] = __builtin_amdgcn_perm(y, x, 0x07060302);
+    }
+  }
+};
+
 // Table entries and page rows of the tokens that a lane reads of a tile.
 template <bool OCT>
 struct Rows {
@@ -172,6 +263,8 @@ struct Rows {
 
 // ------------------------------------------------------------------ kernel --
 
+// E: element bytes of the cache, 0 for 4 bits with block scales.
+//
 // Whether a wave holds two tiles in registers or one, and the workgroups that
 // then share a CU.  One tile is enough to keep the memory busy where its bytes
 // are few or the rows' addresses take the registers; two gain where a tile is
@@ -255,7 +348,9 @@ __device__ __forceinline__ at_u32x4 add_odd(at_u32x4 v, at_u32x4 see, at_f32x4* 
 // FEW: the sequences have any number of queries (a few, if it is to be fast).
 template <class T, int D, int E, bool OCT, bool FEW>
 __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(AttnArgs a, Work work) {
-  typedef Tile<T, D, E> TileT;
+  constexpr bool FP4 = E == 0;
+  constexpr int kUnit = FP4 ? 1 : E;                     // bytes that the cache's strides count
+  typedef std::conditional_t<FP4, Fp4Tile<T, D, OCT>, Tile<T, D, E>> TileT;
   constexpr bool TWO = two_tiles(D, E, OCT);
   static_assert(wgs_per_cu(D, E, OCT) <= kMaxPerCu);
   constexpr int kSteps = TileT::kSteps, kRun = TileT::kRun, kRuns = TileT::kRuns;
@@ -352,9 +447,10 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
     const int pos_max = past + (FEW ? work.group.div(unit_row + rows - 1) : 0);
     const float cs = a.scale_log2 * (E == 1 && a.kv.k_scale ? a.kv.k_scale[head] : 1.0f);
     const int32_t* table = a.kv.tables + seq * a.kv.table_stride;
-    const uint8_t* kbase = static_cast<const uint8_t*>(a.kv.k) + head * a.kv.head_stride * E;
-    const uint8_t* vbase = static_cast<const uint8_t*>(a.kv.v) + head * a.kv.head_stride * E;
-    const int64_t step = a.kv.token_stride * E;
+    const uint8_t* kbase = static_cast<const uint8_t*>(a.kv.k) + head * a.kv.head_stride * kUnit;
+    const uint8_t* vbase = static_cast<const uint8_t*>(a.kv.v) + head * a.kv.head_stride * kUnit;
+    const int64_t step = a.kv.token_stride * kUnit;
+    const int64_t scales = FP4 ? a.kv.scale_at + head * a.kv.scale_head : 0;      // of this head, in a page
 
     // query operand: row c, zero past the unit's rows
     at_u32x4 q[kSteps];
@@ -410,7 +506,11 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
     // query sees a token there (the keys' entries are the values').
     auto row_at = [&](const Rows<OCT>& r, int i) -> int64_t {
       const int p = uint32_t(r.page[i]) < uint32_t(a.kv.pages) ? r.page[i] : 0;
-      return (int64_t(p) * a.kv.page_stride + int64_t(r.slot[i]) * a.kv.token_stride) * E;
+      return (int64_t(p) * a.kv.page_stride + int64_t(r.slot[i]) * a.kv.token_stride) * kUnit;
+    };
+    auto scale_at = [&](const Rows<OCT>& r, int i) -> int64_t {
+      const int p = uint32_t(r.page[i]) < uint32_t(a.kv.pages) ? r.page[i] : 0;
+      return int64_t(p) * a.kv.page_stride + scales + r.slot[i];
     };
     auto load_keys = [&](TileT& x, const Rows<OCT>& r, int t) {
       int stop;
@@ -426,12 +526,23 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
       }
       const int64_t k0 = row_at(r, 0);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) x.load_k(b, kbase + (OCT ? k0 + (4 * b + (c & 3)) * step : b ? row_at(r, 1) : k0), g);
+      for (int b = 0; b < 2; ++b) {
+        const uint8_t* row = kbase + (OCT ? k0 + (4 * b + (c & 3)) * step : b ? row_at(r, 1) : k0);
+        if constexpr (FP4)
+          x.load_k(b, row, static_cast<const uint8_t*>(a.kv.k) + (OCT ? scale_at(r, 0) + 4 * b + (c & 3) : scale_at(r, b)),
+                   int(a.kv.page.d), g);
+        else x.load_k(b, row, g);
+      }
     };
     auto load_values = [&](TileT& x, const Rows<OCT>& r) {
       const int64_t v0 = row_at(r, OCT ? 1 : 2);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x.load_v(i, vbase + (OCT ? v0 + i * step : i ? row_at(r, OCT ? 1 : 2 + i) : v0), c);
+      if constexpr (FP4) {
+#pragma unroll
+        for (int i = 0; i < (OCT ? 1 : 8); ++i)
+          x.load_vs(i, static_cast<const uint8_t*>(a.kv.v) + scale_at(r, OCT ? 1 : 2 + i), int(a.kv.page.d), c);
+      }
     };
     auto load = [&](TileT& x, const Rows<OCT>& r, int t) {
       load_keys(x, r, t);
@@ -738,6 +849,9 @@ hipError_t launch_dim(const AttnArgs& a, const int32_t* cu, int64_t tokens, int 
 
 hipError_t launch_any(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype, int D,
                       void* workspace, hipStream_t stream) {
+  if (cache_dtype == W4A4_E2M1)
+    return dtype == W4A4_BF16 ? launch_dim<Bf16, 0>(a, cu, tokens, D, workspace, stream)
+                              : launch_dim<F16, 0>(a, cu, tokens, D, workspace, stream);
   const bool e4m3 = cache_dtype == W4A4_E4M3;
   if (dtype == W4A4_BF16)
     return e4m3 ? launch_dim<Bf16, 1>(a, cu, tokens, D, workspace, stream)

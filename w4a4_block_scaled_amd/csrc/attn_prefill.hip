@@ -147,8 +147,12 @@ __device__ __forceinline__ at_u32x2 transpose_from_lds(const Lds16* src) {
 // to be kept out of every tile, since the second part may be 0).
 template <class T, int D, int E, bool ONE, bool SPLIT>
 __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs a, PrefillWork w) {
+  constexpr bool FP4 = E == 0;
+  constexpr int kUnit = FP4 ? 1 : E;              // bytes that the cache's strides count
   constexpr int kChunks = D / 8;                  // 16-byte chunks of a row of 16-bit elements
-  constexpr int kLoads = kChunks * E / 8;         // 16-byte loads per thread and tensor: 64 rows x D x E bytes
+  constexpr int kPiece = FP4 && D == 64 ? 8 : 16; // bytes of a load
+  constexpr int kRowLoads = FP4 ? D / 2 / kPiece : D * E / 16;       // of a cache row
+  constexpr int kLoads = kBN * kRowLoads / 256;   // per thread and tensor
   constexpr int kSteps = D / 16;                  // score MFMAs per 32 tokens
   constexpr int kBlocks = D / 32;                 // value blocks
   // Two tiles of keys, two of values, and three words.  One object: with several,
@@ -197,8 +201,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
 
   const float cs = a.scale_log2 * (E == 1 && a.kv.k_scale ? a.kv.k_scale[head] : 1.0f);
   const int32_t* table = a.kv.tables + rt.seq * a.kv.table_stride;
-  const uint8_t* kbase = static_cast<const uint8_t*>(a.kv.k) + head * a.kv.head_stride * E;
-  const uint8_t* vbase = static_cast<const uint8_t*>(a.kv.v) + head * a.kv.head_stride * E;
+  const uint8_t* kbase = static_cast<const uint8_t*>(a.kv.k) + head * a.kv.head_stride * kUnit;
+  const uint8_t* vbase = static_cast<const uint8_t*>(a.kv.v) + head * a.kv.head_stride * kUnit;
 
   at_u32x4 q[kSteps];
   {
@@ -217,11 +221,11 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   // bytes, kRowLoads of a cache row.  16-bit caches are copied to LDS directly
   // (lane l of a wave writes 16 bytes at 16 l, so the lane picks the chunk that
   // belongs there), E4M3 goes through registers.
-  constexpr int kRowLoads = D * E / 16, kRows = 64 / kRowLoads;      // rows of one load
+  constexpr int kRows = 64 / kRowLoads;           // rows of one load
   auto load_row = [&](int j) { return j * kRows + lane / kRowLoads; };           // of the wave's 16
   auto chunk = [&](int j, bool v) {
     const int r = 16 * wave + load_row(j), c = lane % kRowLoads;
-    return E == 1 ? c : c ^ (v ? value_swz<D>(r) : key_swz<D>(r));
+    return E != 2 ? c : c ^ (v ? value_swz<D>(r) : key_swz<D>(r));
   };
   // Where the rows are.  Lane l looks up one page for the tiles ahead: the wave's
   // 16 tokens of tile t + l if they lie on one page (ONE), or its token l % 16 of
@@ -231,6 +235,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   constexpr int kAhead = ONE ? 64 : 4;
   bool bad = false;
   int64_t where = 0;          // byte offset of the lane's row
+  int64_t where_scale = 0;    // FP4: of its first scale byte
+  const int64_t head_scales = FP4 ? a.kv.scale_at + head * a.kv.scale_head : 0;
   auto look_ahead = [&](int t) {
     const int tl = min(t + (ONE ? lane : lane >> 4), t1 - 1);
     int stop;
@@ -239,19 +245,26 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
     const int slot = u - i * int(a.kv.page.d), p = table[i];
     const bool good = uint32_t(p) < uint32_t(a.kv.pages);
     bad |= !good && tk < stop && (min(tk + (ONE ? 16 : 1), stop) > low || tk < a.sinks);
-    where = (int64_t(good ? p : 0) * a.kv.page_stride + int64_t(slot) * a.kv.token_stride) * E;
+    where = (int64_t(good ? p : 0) * a.kv.page_stride + int64_t(slot) * a.kv.token_stride) * kUnit;
+    if constexpr (FP4) where_scale = int64_t(good ? p : 0) * a.kv.page_stride + head_scales + slot;
   };
   // ONE: what a lane reads is at a fixed offset from the first token's row.
   uint32_t koff[kLoads], voff[kLoads];
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
-    const uint32_t row = ONE ? uint32_t(load_row(j)) * uint32_t(a.kv.token_stride * E) : 0;
-    koff[j] = row + 16 * chunk(j, false);
-    voff[j] = row + 16 * chunk(j, true);
+    const uint32_t row = ONE ? uint32_t(load_row(j)) * uint32_t(a.kv.token_stride * kUnit) : 0;
+    koff[j] = row + kPiece * chunk(j, false);
+    voff[j] = row + kPiece * chunk(j, true);
   }
-  at_u32x4 raw_k[E == 1 ? kLoads : 1], raw_v[E == 1 ? kLoads : 1];
+  // FP4: a load's pieces are of one block each; its scale byte
+  const uint32_t soff = FP4 ? (lane % kRowLoads * kPiece / 16) * a.kv.page.d : 0;
+  struct Raw {
+    at_u32x4 x;
+    uint32_t scale;
+  };
+  Raw raw_k[E != 2 ? kLoads : 1], raw_v[E != 2 ? kLoads : 1];
   struct Place {
-    int64_t at[ONE ? 1 : kLoads];
+    int64_t at[ONE ? 1 : kLoads], scale[ONE ? 1 : kLoads];
   };
   auto place_of = [&](int t) {
     const int n = (t - t0) % kAhead;
@@ -260,34 +273,61 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
     Place x;
     if constexpr (ONE) {
       x.at[0] = int64_t(uint32_t(__builtin_amdgcn_readlane(lo, n))) | int64_t(__builtin_amdgcn_readlane(hi32, n)) << 32;
+      if constexpr (FP4)
+        x.scale[0] = int64_t(uint32_t(__builtin_amdgcn_readlane(int(where_scale), n))) |
+                     int64_t(__builtin_amdgcn_readlane(int(where_scale >> 32), n)) << 32;
     } else {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         const int from = 16 * n + load_row(j);
         x.at[j] = int64_t(uint32_t(__shfl(lo, from))) | int64_t(__shfl(hi32, from)) << 32;
+        if constexpr (FP4)
+          x.scale[j] = int64_t(uint32_t(__shfl(int(where_scale), from))) | int64_t(__shfl(int(where_scale >> 32), from)) << 32;
       }
     }
     return x;
   };
-  auto load = [&](Lds16* tile, const uint8_t* base, const Place& x, const uint32_t* offset, at_u32x4* raw) {
+  auto load = [&](Lds16* tile, const uint8_t* base, const Place& x, const uint32_t* offset, Raw* raw) {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const uint8_t* p = base + x.at[ONE ? 0 : j];
       Lds16* const to = tile + (wave * kLoads + j) * 64 * 8;
-      if constexpr (E == 1) raw[j] = *reinterpret_cast<const at_u32x4*>(p + offset[j]);
+      if constexpr (FP4) {
+        if constexpr (kPiece == 8) {
+          const at_u32x2 y = *reinterpret_cast<const at_u32x2*>(p + offset[j]);
+          raw[j].x.x = y.x;
+          raw[j].x.y = y.y;
+        } else {
+          raw[j].x = *reinterpret_cast<const at_u32x4*>(p + offset[j]);
+        }
+        const uint8_t* scales = base - head * a.kv.head_stride + x.scale[ONE ? 0 : j] + (ONE ? load_row(j) : 0);
+        raw[j].scale = scales[soff];
+      } else if constexpr (E == 1) raw[j].x = *reinterpret_cast<const at_u32x4*>(p + offset[j]);
       else if constexpr (ONE) copy_to_lds(p, offset[j], to);
       else copy_to_lds(p + offset[j], to);
     }
   };
-  // E4M3: the pieces that have come go to LDS as 16-bit elements.
-  auto put = [&](Lds16* tile, const at_u32x4* raw, bool v) {
-    if constexpr (E == 1) {
+  // 8 and 4 bits: the pieces that have come go to LDS as 16-bit elements.
+  auto put = [&](Lds16* tile, const Raw* raw, bool v) {
+    if constexpr (FP4) {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int r = 16 * wave + load_row(j), c = lane % kRowLoads, z = v ? value_swz<D>(r) : key_swz<D>(r);
+        const float f = fp4_scale(raw[j].scale);
+#pragma unroll
+        for (int s = 0; s < kPiece / 4; ++s) {
+          const uint32_t x = raw[j].x[s];
+          *reinterpret_cast<LDS_AS at_u32x4*>(tile + r * D + 8 * ((kPiece / 4 * c + s) ^ z)) =
+              (at_u32x4){fp4_pair<T, 0>(x, f), fp4_pair<T, 1>(x, f), fp4_pair<T, 2>(x, f), fp4_pair<T, 3>(x, f)};
+        }
+      }
+    } else if constexpr (E == 1) {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         const int r = 16 * wave + load_row(j), c = chunk(j, v), z = v ? value_swz<D>(r) : key_swz<D>(r);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const uint32_t x = raw[j][2 * s], y = raw[j][2 * s + 1];
+          const uint32_t x = raw[j].x[2 * s], y = raw[j].x[2 * s + 1];
           *reinterpret_cast<LDS_AS at_u32x4*>(tile + r * D + 8 * ((2 * c + s) ^ z)) =
               (at_u32x4){e4m3_pair<T, false>(x), e4m3_pair<T, true>(x), e4m3_pair<T, false>(y), e4m3_pair<T, true>(y)};
         }
@@ -538,7 +578,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
       at_f32x16 s[2], none[2];
       // Inf is settled after the rebase by this tile's maximum (the first one's is by
       // 0); E4M3 has NaN only, and holds fewer registers this way round.
-      if (E == 1) settle(v_cur, t, buf);
+      if (E != 2) settle(v_cur, t, buf);
       if (busy) scores(k_cur, t, s);
       if (E == 2) settle(v_cur, t, buf);
       if (busy) compute(k_cur, v_cur, t, s, none, std::false_type());
@@ -844,6 +884,8 @@ hipError_t launch_attn_prefill(const AttnArgs& a, const int32_t* cu, int64_t tok
   w.group = fast_div(uint32_t(a.group));
   w.parts = static_cast<float*>(workspace);
   w.used = reinterpret_cast<int32_t*>(w.parts + size_t(w.row_tiles) * a.kv.heads * w.splits * kBM * (head_dim + 2));
+  if (cache_dtype == W4A4_E2M1)
+    return dtype == W4A4_BF16 ? launch_dim<Bf16, 0>(a, w, head_dim, stream) : launch_dim<F16, 0>(a, w, head_dim, stream);
   const bool e4m3 = cache_dtype == W4A4_E4M3;
   if (dtype == W4A4_BF16)
     return e4m3 ? launch_dim<Bf16, 1>(a, w, head_dim, stream) : launch_dim<Bf16, 2>(a, w, head_dim, stream);

@@ -22,9 +22,14 @@ using w4a4::ok;
 const int64_t kMaxIndex = int64_t(1) << 31, kMaxRows = kMaxIndex - 256, kMaxCount = int64_t(1) << 30;
 const int64_t kMaxGrid = int64_t(1) << 24;      // workgroups of 256
 
+// Of an E2M1 page: codes and block scales.
+int64_t page_bytes(int page_size, int heads, int head_dim) {
+  return int64_t(page_size) * heads * (head_dim / 2 + head_dim / 32);
+}
+
 w4a4_status check_cache(const char* what, const w4a4_kv_cache* c) {
   if (!c) return fail(W4A4_ERR_NULL, "%s: cache must be non-NULL", what);
-  if (c->dtype != W4A4_BF16 && c->dtype != W4A4_F16 && c->dtype != W4A4_E4M3)
+  if (c->dtype != W4A4_BF16 && c->dtype != W4A4_F16 && c->dtype != W4A4_E4M3 && c->dtype != W4A4_E2M1)
     return fail(W4A4_ERR_FORMAT, "%s: unknown cache type %d", what, int(c->dtype));
   if (c->pages < 1 || c->page_size < 1 || c->page_size > 65536 || c->heads < 1 ||
       (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256))
@@ -33,7 +38,15 @@ w4a4_status check_cache(const char* what, const w4a4_kv_cache* c) {
                 "65536, head_dim 64, 128 or 256)",
                 what, int(c->pages), int(c->page_size), int(c->heads), int(c->head_dim));
   if (!c->k || !c->v) return fail(W4A4_ERR_NULL, "%s: cache k and v must be non-NULL", what);
-  const int64_t unit = c->dtype == W4A4_E4M3 ? 16 : 8;
+  if (c->dtype == W4A4_E2M1) {
+    const int64_t bytes = page_bytes(c->page_size, c->heads, c->head_dim);
+    if (c->page_stride < bytes || c->token_stride != 0 || c->head_stride != 0)
+      return fail(W4A4_ERR_SHAPE, "%s: E2M1 pages of %lld bytes, page stride %lld, token and head strides %lld and %lld (need 0)",
+                  what, (long long)bytes, (long long)c->page_stride, (long long)c->token_stride,
+                  (long long)c->head_stride);
+    if (c->k_scale || c->v_scale) return fail(W4A4_ERR_FORMAT, "%s: an E2M1 cache has no scales per head", what);
+  }
+  const int64_t unit = c->dtype == W4A4_E4M3 || c->dtype == W4A4_E2M1 ? 16 : 8;
   if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0)
     return fail(W4A4_ERR_SHAPE, "%s: cache strides must not be negative", what);
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % unit || c->token_stride % unit ||
@@ -58,7 +71,7 @@ w4a4_status check_seqs(const char* what, const w4a4_kv_seqs* s, bool lens) {
 
 w4a4_status check_type(const char* what, const w4a4_kv_cache* c, w4a4_dtype t) {
   if (t != W4A4_BF16 && t != W4A4_F16) return fail(W4A4_ERR_FORMAT, "%s: type %d (need BF16 or FP16)", what, int(t));
-  if (c->dtype != W4A4_E4M3 && c->dtype != int(t))
+  if (c->dtype != W4A4_E4M3 && c->dtype != W4A4_E2M1 && c->dtype != int(t))
     return fail(W4A4_ERR_FORMAT, "%s: type %d with a cache of type %d", what, int(t), int(c->dtype));
   return W4A4_OK;
 }
@@ -80,6 +93,13 @@ w4a4::KvView view(const w4a4_kv_cache* c, const w4a4_kv_seqs* s) {
   v.page_stride = c->page_stride;
   v.token_stride = c->token_stride;
   v.head_stride = c->head_stride;
+  v.scale_at = v.scale_head = 0;
+  if (c->dtype == W4A4_E2M1) {
+    v.token_stride = c->head_dim / 2;
+    v.head_stride = int64_t(c->page_size) * v.token_stride;
+    v.scale_at = c->heads * v.head_stride;
+    v.scale_head = int64_t(c->page_size) * (c->head_dim / 32);
+  }
   v.tables = s->tables;
   v.lens = s->lens;
   v.table_stride = s->table_stride;
@@ -174,9 +194,64 @@ w4a4_status check_list(const char* what, const void* a, const void* b, int64_t n
   return W4A4_OK;
 }
 
+w4a4_status check_rotation(const char* what, const w4a4_rotation* r, int dim) {
+  if (!r) return fail(W4A4_ERR_NULL, "%s: rotation must be non-NULL", what);
+  if (r->rot_dim < 2 || r->rot_dim > dim || r->rot_dim % 2)
+    return fail(W4A4_ERR_SHAPE, "%s: rot_dim=%d of rows of %d (need even, 2 to their width)", what, int(r->rot_dim), dim);
+  if (r->interleaved < 0 || r->interleaved > 1 || r->inverse < 0 || r->inverse > 1)
+    return fail(W4A4_ERR_SHAPE, "%s: interleaved=%d inverse=%d (need 0 or 1)", what, int(r->interleaved), int(r->inverse));
+  if (!(r->factor > 0.0f) || !isfinite(r->factor))
+    return fail(W4A4_ERR_SHAPE, "%s: factor=%g must be positive and finite", what, double(r->factor));
+  if (!r->freqs) return fail(W4A4_ERR_NULL, "%s: freqs must be non-NULL", what);
+  if (!aligned(r->freqs, 4)) return fail(W4A4_ERR_ALIGN, "%s: freqs needs 4-byte alignment", what);
+  return W4A4_OK;
+}
+
+// Rows may be rotated in place, not into other rows of themselves.
+w4a4_status check_in_place(const char* what, const void* x, int64_t x_row, int64_t x_head, const void* out,
+                           int64_t o_row, int64_t o_head) {
+  if (x == out && (x_row != o_row || x_head != o_head))
+    return fail(W4A4_ERR_SHAPE, "%s: in place, the strides must be the same", what);
+  return W4A4_OK;
+}
+
+w4a4_status check_rows_grid(const char* what, int64_t tokens, int64_t vectors, int dim) {
+  if (w4a4::rows_workgroups(tokens, vectors, dim) >= kMaxGrid)
+    return fail(W4A4_ERR_SHAPE, "%s: %lld rows are too many for one call", what, (long long)tokens);
+  return W4A4_OK;
+}
+
+w4a4::RowsIn rotated_rows(const w4a4_rotation* r, const int32_t* positions, int64_t tokens, int dim) {
+  w4a4::RowsIn a = {};
+  a.positions = positions;
+  a.tokens = tokens;
+  a.dim = dim;
+  if (r) {
+    a.freqs = r->freqs;
+    a.rot = r->rot_dim;
+    a.interleaved = r->interleaved;
+    a.inverse = r->inverse;
+    a.factor = r->factor;
+  }
+  return a;
+}
+
+// The rows of a call that go into or come out of a cache: cu, tokens.
+w4a4_status check_tokens(const char* what, const w4a4_kv_seqs* s, const int32_t* cu, int64_t tokens) {
+  if (tokens < 0 || tokens >= kMaxIndex || (!cu && tokens != s->seqs))
+    return fail(W4A4_ERR_SHAPE, "%s: %lld tokens for %d sequences", what, (long long)tokens, int(s->seqs));
+  if (!aligned(cu, 4)) return fail(W4A4_ERR_ALIGN, "%s: cu needs 4-byte alignment", what);
+  return W4A4_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t w4a4_kv_page_bytes(int page_size, int heads, int head_dim) {
+  if (page_size < 1 || page_size > 65536 || heads < 1 || (head_dim != 64 && head_dim != 128 && head_dim != 256)) return 0;
+  return size_t(page_bytes(page_size, heads, head_dim));
+}
 
 w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, const int32_t* cu, int64_t tokens,
                            w4a4_dtype dtype, const void* k, int64_t k_row, int64_t k_head, const void* v,
@@ -193,9 +268,104 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs,
   st = check_rows(what, "k", k, k_row, k_head);
   if (st == W4A4_OK) st = check_rows(what, "v", v, v_row, v_head);
   if (st != W4A4_OK) return st;
+  if (cache->dtype == W4A4_E2M1) {
+    st = check_rows_grid(what, tokens, 2 * int64_t(cache->heads), cache->head_dim);
+    if (st != W4A4_OK) return st;
+    w4a4::RowsIn a = rotated_rows(nullptr, nullptr, tokens, cache->head_dim);
+    a.kv = view(cache, seqs);
+    a.cu = cu;
+    a.k = k, a.k_row = k_row, a.k_head = k_head;
+    a.v = v, a.v_row = v_row, a.v_head = v_head;
+    return hip_status(w4a4::launch_rows_in(a, cache->dtype, dtype, static_cast<hipStream_t>(stream)), "kv_append launch");
+  }
   return hip_status(w4a4::launch_kv_append(view(cache, seqs), cache->dtype, cache->head_dim, cu, tokens, dtype, k, k_row,
                                            k_head, v, v_row, v_head, static_cast<hipStream_t>(stream)),
                     "kv_append launch");
+}
+
+w4a4_status w4a4_rope(const w4a4_rotation* rotation, int64_t tokens, const int32_t* positions, w4a4_dtype dtype,
+                      int heads, int head_dim, const void* x, int64_t x_row, int64_t x_head, void* out, int64_t o_row,
+                      int64_t o_head, void* stream) {
+  const char* what = "rope";
+  if (dtype != W4A4_BF16 && dtype != W4A4_F16) return fail(W4A4_ERR_FORMAT, "%s: type %d (need BF16 or FP16)", what, int(dtype));
+  if (tokens < 0 || tokens >= kMaxIndex || heads < 0 || heads > 65536 || head_dim < 8 || head_dim > 512 || head_dim % 8)
+    return fail(W4A4_ERR_SHAPE, "%s: %lld rows of %d heads of %d (need a multiple of 8, 8 to 512)", what,
+                (long long)tokens, heads, head_dim);
+  w4a4_status st = check_rotation(what, rotation, head_dim);
+  if (st != W4A4_OK) return st;
+  if (tokens == 0 || heads == 0) return ok();
+  if (!positions) return fail(W4A4_ERR_NULL, "%s: positions must be non-NULL", what);
+  if (!aligned(positions, 4)) return fail(W4A4_ERR_ALIGN, "%s: positions needs 4-byte alignment", what);
+  st = check_rows(what, "x", x, x_row, x_head);
+  if (st == W4A4_OK) st = check_rows(what, "out", out, o_row, o_head);
+  if (st == W4A4_OK) st = check_in_place(what, x, x_row, x_head, out, o_row, o_head);
+  if (st == W4A4_OK) st = check_rows_grid(what, tokens, heads, head_dim);
+  if (st != W4A4_OK) return st;
+  w4a4::RowsIn a = rotated_rows(rotation, positions, tokens, head_dim);
+  a.q_heads = heads;
+  a.q = x, a.q_row = x_row, a.q_head = x_head;
+  a.out = out, a.o_row = o_row, a.o_head = o_head;
+  return hip_status(w4a4::launch_rows_in(a, 0, dtype, static_cast<hipStream_t>(stream)), "rope launch");
+}
+
+w4a4_status w4a4_kv_append_rope(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, const int32_t* cu,
+                                int64_t tokens, w4a4_dtype dtype, const w4a4_rotation* rotation,
+                                const int32_t* positions, int q_heads, const void* q, int64_t q_row, int64_t q_head,
+                                void* q_out, int64_t o_row, int64_t o_head, const void* k, int64_t k_row,
+                                int64_t k_head, const void* v, int64_t v_row, int64_t v_head, void* stream) {
+  const char* what = "kv_append_rope";
+  w4a4_status st = check_cache(what, cache);
+  if (st == W4A4_OK) st = check_seqs(what, seqs, true);
+  if (st == W4A4_OK) st = check_type(what, cache, dtype);
+  if (st == W4A4_OK) st = check_tokens(what, seqs, cu, tokens);
+  if (st == W4A4_OK) st = check_rotation(what, rotation, cache->head_dim);
+  if (st != W4A4_OK) return st;
+  if (q_heads < 0 || q_heads > 65536 || cache->heads > 65536)
+    return fail(W4A4_ERR_SHAPE, "%s: %d query heads, %d kv heads", what, q_heads, int(cache->heads));
+  if (!aligned(positions, 4)) return fail(W4A4_ERR_ALIGN, "%s: positions needs 4-byte alignment", what);
+  if (tokens == 0 || seqs->seqs == 0) return ok();
+  st = check_rows(what, "k", k, k_row, k_head);
+  if (st == W4A4_OK) st = check_rows(what, "v", v, v_row, v_head);
+  if (st == W4A4_OK && q_heads) st = check_rows(what, "q", q, q_row, q_head);
+  if (st == W4A4_OK && q_heads) st = check_rows(what, "q_out", q_out, o_row, o_head);
+  if (st == W4A4_OK && q_heads) st = check_in_place(what, q, q_row, q_head, q_out, o_row, o_head);
+  if (st == W4A4_OK) st = check_rows_grid(what, tokens, q_heads + 2 * int64_t(cache->heads), cache->head_dim);
+  if (st != W4A4_OK) return st;
+  w4a4::RowsIn a = rotated_rows(rotation, positions, tokens, cache->head_dim);
+  a.kv = view(cache, seqs);
+  a.cu = cu;
+  a.q_heads = q_heads;
+  a.q = q, a.q_row = q_row, a.q_head = q_head;
+  a.out = q_out, a.o_row = o_row, a.o_head = o_head;
+  a.k = k, a.k_row = k_row, a.k_head = k_head;
+  a.v = v, a.v_row = v_row, a.v_head = v_head;
+  return hip_status(w4a4::launch_rows_in(a, cache->dtype, dtype, static_cast<hipStream_t>(stream)),
+                    "kv_append_rope launch");
+}
+
+w4a4_status w4a4_kv_read(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, const int32_t* cu, int64_t tokens,
+                         w4a4_dtype dtype, void* k, int64_t k_row, int64_t k_head, void* v, int64_t v_row,
+                         int64_t v_head, void* stream) {
+  const char* what = "kv_read";
+  w4a4_status st = check_cache(what, cache);
+  if (st == W4A4_OK) st = check_seqs(what, seqs, true);
+  if (st == W4A4_OK) st = check_type(what, cache, dtype);
+  if (st == W4A4_OK) st = check_tokens(what, seqs, cu, tokens);
+  if (st != W4A4_OK) return st;
+  if (cache->heads > 65536) return fail(W4A4_ERR_SHAPE, "%s: %d kv heads", what, int(cache->heads));
+  if (tokens == 0 || seqs->seqs == 0) return ok();
+  st = check_rows(what, "k", k, k_row, k_head);
+  if (st == W4A4_OK) st = check_rows(what, "v", v, v_row, v_head);
+  if (st == W4A4_OK) st = check_rows_grid(what, tokens, 2 * int64_t(cache->heads), cache->head_dim);
+  if (st != W4A4_OK) return st;
+  w4a4::RowsOut a = {};
+  a.kv = view(cache, seqs);
+  a.cu = cu;
+  a.tokens = tokens;
+  a.dim = cache->head_dim;
+  a.k = k, a.k_row = k_row, a.k_head = k_head;
+  a.v = v, a.v_row = v_row, a.v_head = v_head;
+  return hip_status(w4a4::launch_rows_out(a, cache->dtype, dtype, static_cast<hipStream_t>(stream)), "kv_read launch");
 }
 
 size_t w4a4_attn_decode_workspace_bytes(const w4a4_kv_cache* cache, int64_t seqs, int q_heads) {

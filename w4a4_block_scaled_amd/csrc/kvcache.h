@@ -29,12 +29,15 @@ inline FastDiv fast_div(uint32_t d) {
 }
 
 // Device view of w4a4_kv_cache + w4a4_kv_seqs.  Strides in elements.
+// (E2M1: in bytes; a page's scale bytes begin scale_at bytes into it, head by head,
+// scale_head bytes each: [head_dim / 32, page_size].)
 struct KvView {
   const void* k;
   const void* v;
   const float* k_scale;
   const float* v_scale;
   int64_t page_stride, token_stride, head_stride;
+  int64_t scale_at, scale_head;
   const int32_t* tables;
   const int32_t* lens;
   int64_t table_stride;
@@ -63,11 +66,51 @@ __device__ __forceinline__ int kv_page(const KvView& kv, const int32_t* row, int
   const int p = row[i];
   return (p >= 0 && p < kv.pages) ? p : -1;
 }
+
+// Row of `cu` that holds token i: the last s with cu[s] <= i < cu[s + 1].
+__device__ __forceinline__ int find_seq(const int32_t* cu, int seqs, int i) {
+  int lo = 0, hi = seqs;          // cu[lo] <= i < cu[hi] if the token belongs to any
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
 #endif
 
 hipError_t launch_kv_append(const KvView& kv, int dtype, int head_dim, const int32_t* cu, int64_t tokens, int in_dtype,
                             const void* k, int64_t k_row, int64_t k_head, const void* v, int64_t v_row, int64_t v_head,
                             hipStream_t stream);
+
+// Rotation of rows, alone (kv.heads == 0) or on the way into a cache.
+struct RowsIn {
+  KvView kv;
+  const int32_t* cu;              // NULL: one row per sequence
+  const int32_t* positions;       // NULL: the tokens' places in their sequences
+  const float* freqs;
+  const void *q, *k, *v;
+  void* out;                      // of the rotated q
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head;    // elements
+  int64_t tokens;
+  int32_t q_heads, dim;
+  int32_t rot;                    // 0: no rotation
+  int32_t interleaved, inverse;
+  float factor;
+};
+// cache_dtype: of kv, if it has heads; dtype: of the rows
+int64_t rows_workgroups(int64_t tokens, int64_t vectors, int dim);      // vectors: heads of a token, in and out
+hipError_t launch_rows_in(const RowsIn& a, int cache_dtype, int dtype, hipStream_t stream);
+
+// Rows of the cache in 16 bits.
+struct RowsOut {
+  KvView kv;
+  const int32_t* cu;
+  void *k, *v;
+  int64_t k_row, k_head, v_row, v_head;
+  int64_t tokens;
+  int32_t dim;
+};
+hipError_t launch_rows_out(const RowsOut& a, int cache_dtype, int dtype, hipStream_t stream);
 
 size_t attn_decode_workspace(int q_heads, int heads, int head_dim);
 hipError_t launch_attn_decode(const AttnArgs& a, int cache_dtype, int dtype, int head_dim, void* workspace,

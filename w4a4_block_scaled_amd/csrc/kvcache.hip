@@ -25,16 +25,6 @@ struct AppendArgs {
   int head_chunks;    // head_dim / 8
 };
 
-// Row of `cu` that holds token i: the last s with cu[s] <= i < cu[s + 1].
-__device__ __forceinline__ int find_seq(const int32_t* cu, int seqs, int i) {
-  int lo = 0, hi = seqs;          // cu[lo] <= i < cu[hi] if the token belongs to any
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= i) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 __device__ __forceinline__ float bits_to_f32(uint16_t b, bool f16) {
   if (f16) return float(__builtin_bit_cast(_Float16, b));
   return __builtin_bit_cast(float, uint32_t(b) << 16);

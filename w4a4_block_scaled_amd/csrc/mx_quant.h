@@ -27,8 +27,9 @@ __device__ __forceinline__ int quad_xor1(int v) { return __builtin_amdgcn_mov_dp
 __device__ __forceinline__ int quad_xor2(int v) { return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true); }
 
 // Codes and the scale byte of one 32-block from this lane's 8 elements (the
-// block is spread over 4 consecutive lanes, which must all be present).
-template <int FMT>
+// block is spread over 4 consecutive lanes, which must all be present).  E_MAX:
+// the largest exponent of the scale; larger values saturate.
+template <int FMT, int E_MAX = 127>
 __device__ __forceinline__ void quant8_mx(const float (&x)[8], uint32_t& word, uint32_t& sbyte) {
   // block amax as the integer maximum of the magnitude bit patterns: for
   // finite values they order as the values do, and any Inf or NaN gives a
@@ -42,7 +43,7 @@ __device__ __forceinline__ void quant8_mx(const float (&x)[8], uint32_t& word, u
   const bool bad = abits > 0x7f7fffffu;  // Inf or NaN in the block
 
   int e = -127;
-  if (abits != 0) e = max(-127, min(127, floor_log2(__uint_as_float(abits)) - 2));
+  if (abits != 0) e = max(-127, min(E_MAX, floor_log2(__uint_as_float(abits)) - 2));
 
   word = 0;
   if (FMT == MXFP4) {
