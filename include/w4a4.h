@@ -427,7 +427,7 @@ typedef enum { W4A4_BF16 = 0, W4A4_F16 = 1, W4A4_E4M3 = 2, W4A4_E2M1 = 4 } w4a4_
  *           for 255
  *
  * w4a4_kv_page_bytes() bytes long, K and V alike.  page_stride is in bytes, a
- * multiple of 16 and no less than a page; token_stride and head_stride are 0,
+ * multiple of 16, no less than a page and less than 2^31; token_stride and head_stride are 0,
  * k_scale and v_scale NULL.  Any bytes are valid contents.  Rows are stored by
  * the rule of w4a4_quantize_act's MXFP4 (block exponent floor(log2 amax) - 2, codes
  * to nearest even, saturating at 6; a block with Inf or NaN gets byte 255 and zero

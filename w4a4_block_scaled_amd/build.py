@@ -20,7 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libw4a4.so")
 SOURCES = ["quantize.hip", "pack.hip", "gemm.hip", "solver.hip", "int4g64.hip", "int8g128.hip", "probe.hip",
-           "kvcache.hip", "kvrows.hip", "attn_decode.hip", "attn_prefill.hip", "capi.cpp", "capi_kv.cpp"]
+           "kvcache.hip", "kvrows.hip", "attn_decode.hip", "attn_fp4.hip", "attn_prefill.hip", "capi.cpp", "capi_kv.cpp"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -29,65 +29,10 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "attn_common.h"
+#include "attn_list.h"
 
 namespace w4a4 {
 namespace {
-
-constexpr int kTile = 128;       // tokens per workgroup step: 4 waves x 32
-constexpr int kRows = 16;        // of a unit
-
-// The list of work: per sequence, tiles over [0, sink_end) and [start, len).
-// A length beyond the table's capacity is cut to it and marked (`over`).
-struct SeqSpan {
-  int len, low, start, sink_end, sink_tiles, tiles;
-  bool over;
-};
-
-// `count`: the sequence's queries, its last tokens.
-__device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, int length, int count) {
-  SeqSpan z;
-  const int cap = int(min(int64_t(a.kv.max_pages) * a.kv.page.d, int64_t(1) << 30));
-  const int len = max(length, 0);
-  z.over = len > cap;
-  z.len = min(len, cap);
-  z.low = a.window ? max(z.len - count + 1 - a.window, 0) : 0;   // first token of the first query's window
-  z.start = z.low & ~7;
-  z.sink_end = min(a.sinks, z.start);
-  z.sink_tiles = (z.sink_end + kTile - 1) / kTile;
-  // at least one: a sequence without tokens still has outputs to write
-  z.tiles = max(z.sink_tiles + (z.len - z.start + kTile - 1) / kTile, 1);
-  return z;
-}
-
-// Results of a unit's piece: unnormalised sums o [rows x D], references m of the
-// weights and sums of weights l [rows], in the log2 domain.
-struct Partial {
-  float *o, *m, *l;
-};
-
-// A cut unit: written by the workgroup that begins it.
-struct Cut {
-  int32_t seq, unit, count, unused;      // count: workgroups that hold parts of it
-};
-
-struct Work {
-  float* parts;       // [workgroups x 2] partial results
-  Cut* cuts;          // [workgroups]
-  int rows;           // of a partial result
-  const int32_t* cu;  // FEW: rows of q
-  int tokens;
-  FastDiv group;
-};
-
-__host__ __device__ constexpr int partial_floats(int rows, int D) { return (rows * (D + 2) + 3) / 4 * 4; }
-
-// A workgroup has at most two pieces of cut units: one that goes on from the
-// workgroup before (slot 0) and one that it begins (slot 1).
-__device__ __forceinline__ Partial partial_at(const Work& w, int D, int64_t wg, int slot) {
-  float* p = w.parts + (wg * 2 + slot) * partial_floats(w.rows, D);
-  return {p, p + w.rows * D, p + w.rows * (D + 1)};
-}
 
 // ---------------------------------------------------------------- operands --
 
@@ -164,97 +109,6 @@ struct Tile {
   }
 };
 
-// The same of 32 tokens held in 4 bits: codes, and the scale bytes of the blocks that
-// they lie in.  A lane's keys are a block (D = 64: half of one), so that one scale
-// serves all steps of a load.
-template <class T, int D, bool OCT>
-struct Fp4Tile {
-  static constexpr int kSteps = D / 32;
-  static constexpr int kRun = D >= 128 ? 8 : 4;
-  static constexpr int kRuns = D / 16 / kRun;
-  static constexpr int kLoads = D >= 128 ? D / 128 : 1;        // of a lane's keys: 16 bytes each (D = 64: 8)
-  static constexpr int kDwords = D >= 128 ? 4 : 2;             // of a load: steps
-
-  uint32_t k[2][kLoads][kDwords];
-  uint32_t ks[2][kLoads];
-  uint32_t v[8][kRuns];
-  uint32_t vs[kRuns][OCT ? 2 : 8];      // bytes of 4 tokens each, or of one
-
-  // First d of the 8 that quarter g holds of step j.
-  static __device__ __forceinline__ int key_dim(int j, int g) {
-    return 128 * (j / kDwords) + (D / (4 * kLoads)) * g + 8 * (j % kDwords);
-  }
-  static __device__ __forceinline__ int key_block(int i, int g) { return D == 64 ? g >> 1 : 4 * i + g; }
-  static __device__ __forceinline__ int value_block(int r, int c) { return D == 64 ? c >> 3 : 4 * r + (c >> 2); }
-
-  __device__ __forceinline__ void load_k(int b, const uint8_t* row, const uint8_t* scale, int page, int g) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      if constexpr (D == 64) {
-        const at_u32x2 x = *reinterpret_cast<const at_u32x2*>(row + 8 * g);
-        k[b][i][0] = x.x;
-        k[b][i][1] = x.y;
-      } else {
-        const at_u32x4 x = *reinterpret_cast<const at_u32x4*>(row + 64 * i + 16 * g);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) k[b][i][w] = x[w];
-      }
-      ks[b][i] = scale[key_block(i, g) * page];
-    }
-  }
-  __device__ __forceinline__ void load_v(int i, const uint8_t* row, int c) {
-#pragma unroll
-    for (int r = 0; r < kRuns; ++r) {
-      if constexpr (D == 64) v[i][r] = *reinterpret_cast<const uint16_t*>(row + 2 * c);
-      else v[i][r] = *reinterpret_cast<const uint32_t*>(row + 64 * r + 4 * c);
-    }
-  }
-  // of 8 tokens (OCT), or of token i
-  __device__ __forceinline__ void load_vs(int i, const uint8_t* scale, int page, int c) {
-#pragma unroll
-    for (int r = 0; r < kRuns; ++r) {
-      const uint8_t* p = scale + value_block(r, c) * page;
-      if constexpr (OCT) {
-        const at_u32x2 x = *reinterpret_cast<const at_u32x2*>(p);
-        vs[r][0] = x.x;
-        vs[r][1] = x.y;
-      } else {
-        vs[r][i] = *p;
-      }
-    }
-  }
-  __device__ __forceinline__ void clear_v(int i) {
-#pragma unroll
-    for (int r = 0; r < kRuns; ++r) {
-      v[i][r] = 0;
-      if constexpr (OCT) vs[r][i >> 2] &= ~(0xffu << 8 * (i & 3));
-      else vs[r][i] = 0;
-    }
-  }
-
-  __device__ __forceinline__ at_u32x4 key(int b, int j) const {
-    const uint32_t x = k[b][j / kDwords][j % kDwords];
-    const float s = fp4_scale(ks[b][j / kDwords]);
-    return (at_u32x4){fp4_pair<T, 0>(x, s), fp4_pair<T, 1>(x, s), fp4_pair<T, 2>(x, s), fp4_pair<T, 3>(x, s)};
-  }
-  template <int B>
-  __device__ __forceinline__ uint32_t value_pair(int i, int r) const {
-    return fp4_pair<T, B>(v[i][r], fp4_scale(OCT ? vs[r][i >> 2] >> 8 * (i & 3) & 0xffu : vs[r][i]));
-  }
-  __device__ __forceinline__ void values(int r, int j, at_u32x4* lo, at_u32x4* hi) const {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      uint32_t x, y;
-      if (j == 0) x = value_pair<0>(2 * t, r), y = value_pair<0>(2 * t + 1, r);
-      else if (j == 2) x = value_pair<1>(2 * t, r), y = value_pair<1>(2 * t + 1, r);
-      else if (j == 4) x = value_pair<2>(2 * t, r), y = value_pair<2>(2 * t + 1, r);
-      else x = value_pair<3>(2 * t, r), y = value_pair<3>(2 * t + 1, r);
-      (*lo)[t] = __builtin_amdgcn_perm(y, x, 0x05040100);
-      (*hi)[t] = __builtin_amdgcn_perm(y, x, 0x07060302);
-    }
-  }
-};
-
 // Table entries and page rows of the tokens that a lane reads of a tile.
 template <bool OCT>
 struct Rows {
@@ -263,8 +117,6 @@ struct Rows {
 
 // ------------------------------------------------------------------ kernel --
 
-// E: element bytes of the cache, 0 for 4 bits with block scales.
-//
 // Whether a wave holds two tiles in registers or one, and the workgroups that
 // then share a CU.  One tile is enough to keep the memory busy where its bytes
 // are few or the rows' addresses take the registers; two gain where a tile is
@@ -280,45 +132,7 @@ constexpr int wgs_per_cu(int D, int E, bool oct) {
   return oct && D == 64 ? (E == 1 ? 4 : 3) : 2;
 }
 
-// Tiles that beginning a unit counts as, where a workgroup has 8 tiles or more:
-// with 0 the pieces of short sequences, of many units each, end last.  0 / 1 / 2
-// on 32 sequences of 100 to 6000 tokens: E4M3, D=128 66.5 / 53.1 / 53.4 us,
-// bf16, D=256 157.9 / 147.2 / 148.7; on equal lengths of 3050, 53.6 / 54.8 for
-// 0 / 2; the ragged batch 158.9 / 157.5 / 160.1.
-constexpr int kStart = 1;
 constexpr int kMaxPerCu = 4;     // the workspaces' size
-
-// A sequence's queries: the rows of one kv head are count * group, token by token.
-struct Queries {
-  int count, first;
-};
-template <bool FEW>
-__device__ __forceinline__ Queries queries_of(const Work& w, int s) {
-  if (!FEW) return {1, s};
-  const int first = w.cu[s];
-  return {min(max(w.cu[s + 1] - first, 0), w.tokens), first};
-}
-
-__device__ __forceinline__ int readlane(int x, int l) { return __builtin_amdgcn_readlane(x, l); }
-__device__ __forceinline__ int64_t readlane(int64_t x, int l) {
-  return int64_t(uint32_t(__builtin_amdgcn_readlane(int(x), l))) | int64_t(__builtin_amdgcn_readlane(int(x >> 32), l)) << 32;
-}
-
-// Output columns d .. d + 3 of row `row` of a kv head from its reference, sum of
-// weights and unnormalised sum.
-template <class T, int D, int E, bool FEW>
-__device__ __forceinline__ void finish(const AttnArgs& a, const Work& w, int head, const Queries& qs, const SeqSpan& sp,
-                                       int row, int d, float M, float L, at_f32x4 O) {
-  const int tok = FEW ? w.group.div(row) : 0, h = head * a.group + row - tok * a.group;
-  const int64_t at = int64_t(qs.first) + tok;
-  if (FEW && (at < 0 || at >= w.tokens)) return;
-  const bool none = sp.len - qs.count + tok < 0 && !sp.over;       // a query before position 0
-  const float inv = (E == 1 && a.kv.v_scale ? a.kv.v_scale[head] : 1.0f) / L;
-  at_u32x2 y = {T::pack(O[0] * inv, O[1] * inv), T::pack(O[2] * inv, O[3] * inv)};
-  if (none) y = (at_u32x2){0, 0};
-  *reinterpret_cast<at_u32x2*>(static_cast<uint16_t*>(a.out) + at * a.o_row + h * a.o_head + d) = y;
-  if (a.lse && d == 0) a.lse[at * a.q_heads + h] = none ? kNegInf : (M + __log2f(L)) * 0.693147180559945f;
-}
 
 // Adds the Inf and NaN of a value operand to the sums of the rows that see them
 // (`see`: 1.0 or 0 per token and row), and returns it with zeros in their place.
@@ -348,14 +162,11 @@ __device__ __forceinline__ at_u32x4 add_odd(at_u32x4 v, at_u32x4 see, at_f32x4* 
 // FEW: the sequences have any number of queries (a few, if it is to be fast).
 template <class T, int D, int E, bool OCT, bool FEW>
 __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(AttnArgs a, Work work) {
-  constexpr bool FP4 = E == 0;
-  constexpr int kUnit = FP4 ? 1 : E;                     // bytes that the cache's strides count
-  typedef std::conditional_t<FP4, Fp4Tile<T, D, OCT>, Tile<T, D, E>> TileT;
+  typedef Tile<T, D, E> TileT;
   constexpr bool TWO = two_tiles(D, E, OCT);
   static_assert(wgs_per_cu(D, E, OCT) <= kMaxPerCu);
   constexpr int kSteps = TileT::kSteps, kRun = TileT::kRun, kRuns = TileT::kRuns;
   constexpr int kBlocks = D / 16;                        // MFMAs of the value product
-  typedef std::conditional_t<FEW, int64_t, int> Sum;     // of tiles (FEW: times units) of 64 sequences
   __shared__ float lds_o[4][kRows][D + 4];
   __shared__ float lds_m[4][kRows], lds_l[4][kRows];
 
@@ -364,55 +175,13 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
   const int64_t wg = blockIdx.x;
   if (threadIdx.x == 0) work.cuts[wg].count = 0;
 
-  // This workgroup's piece [item, end) of the list of (sequence, unit, tile),
-  // and the sequence that `item` falls in, with the place where that begins.
-  // Lane l looks after the sequences l, l + 64, ...; up to 64 sequences take one
-  // load of the lengths.
+  Piece pc;
+  if (!find_piece<FEW>(a, work, kRows, lane, &pc)) return;
+  const int64_t total = pc.total, wgs = pc.wgs, end = pc.end;
+  const int extra = pc.extra, len0 = pc.len0;
+  int64_t item = pc.item, seq_begin = pc.seq_begin;
+  int seq = pc.seq;
   auto units_of = [&](int count) { return a.kv.heads * ((count * a.group + kRows - 1) / kRows); };
-  const int64_t units1 = FEW ? 1 : units_of(1);
-  auto length = [&](int s) { return s < a.kv.seqs ? a.kv.lens[s] : 0; };
-  auto share_of = [&](int s, int len) -> Sum {
-    if (s >= a.kv.seqs) return 0;
-    const int count = queries_of<FEW>(work, s).count;
-    const Sum tiles = seq_span(a, len, count).tiles;
-    return FEW ? tiles * units_of(count) : tiles;
-  };
-  auto scan = [&](Sum t) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const Sum y = __shfl_up(t, d);
-      if (lane >= d) t += y;
-    }
-    return t;
-  };
-  const int len0 = length(lane);
-  const Sum mine0 = share_of(lane, len0), in0 = scan(mine0);
-  int64_t total = readlane(in0, 63);
-  for (int base = 64; base < a.kv.seqs; base += 64) total += readlane(scan(share_of(base + lane, length(base + lane))), 63);
-  // a unit's first tiles stand for the cost of beginning it, and hold no tokens
-  const int extra = !FEW && total * units1 >= 8 * int64_t(gridDim.x) ? kStart : 0;
-  total = (total + int64_t(extra) * (FEW ? 0 : a.kv.seqs)) * units1;
-  const int64_t wgs = min(int64_t(gridDim.x), total);
-  if (wg >= wgs) return;
-  int64_t item = wg * total / wgs;
-  const int64_t end = (wg + 1) * total / wgs;
-  int seq = 0;
-  int64_t seq_begin = 0;
-  for (int base = 0; base < a.kv.seqs; base += 64) {
-    Sum mine = mine0, in = in0;
-    if (base) {
-      mine = share_of(base + lane, length(base + lane));
-      in = scan(mine);
-    }
-    const uint64_t past = __ballot(seq_begin + (int64_t(in) + extra * (lane + 1)) * units1 > item);
-    if (past) {
-      const int l = __ffsll((unsigned long long)past) - 1;
-      seq = base + l;
-      seq_begin += (int64_t(readlane(Sum(in - mine), l)) + extra * l) * units1;
-      break;
-    }
-    seq_begin += (int64_t(readlane(in, 63)) + extra * 64) * units1;
-  }
 
   while (item < end && seq < a.kv.seqs) {
     const Queries qs = queries_of<FEW>(work, seq);
@@ -447,10 +216,9 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
     const int pos_max = past + (FEW ? work.group.div(unit_row + rows - 1) : 0);
     const float cs = a.scale_log2 * (E == 1 && a.kv.k_scale ? a.kv.k_scale[head] : 1.0f);
     const int32_t* table = a.kv.tables + seq * a.kv.table_stride;
-    const uint8_t* kbase = static_cast<const uint8_t*>(a.kv.k) + head * a.kv.head_stride * kUnit;
-    const uint8_t* vbase = static_cast<const uint8_t*>(a.kv.v) + head * a.kv.head_stride * kUnit;
-    const int64_t step = a.kv.token_stride * kUnit;
-    const int64_t scales = FP4 ? a.kv.scale_at + head * a.kv.scale_head : 0;      // of this head, in a page
+    const uint8_t* kbase = static_cast<const uint8_t*>(a.kv.k) + head * a.kv.head_stride * E;
+    const uint8_t* vbase = static_cast<const uint8_t*>(a.kv.v) + head * a.kv.head_stride * E;
+    const int64_t step = a.kv.token_stride * E;
 
     // query operand: row c, zero past the unit's rows
     at_u32x4 q[kSteps];
@@ -506,11 +274,7 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
     // query sees a token there (the keys' entries are the values').
     auto row_at = [&](const Rows<OCT>& r, int i) -> int64_t {
       const int p = uint32_t(r.page[i]) < uint32_t(a.kv.pages) ? r.page[i] : 0;
-      return (int64_t(p) * a.kv.page_stride + int64_t(r.slot[i]) * a.kv.token_stride) * kUnit;
-    };
-    auto scale_at = [&](const Rows<OCT>& r, int i) -> int64_t {
-      const int p = uint32_t(r.page[i]) < uint32_t(a.kv.pages) ? r.page[i] : 0;
-      return int64_t(p) * a.kv.page_stride + scales + r.slot[i];
+      return (int64_t(p) * a.kv.page_stride + int64_t(r.slot[i]) * a.kv.token_stride) * E;
     };
     auto load_keys = [&](TileT& x, const Rows<OCT>& r, int t) {
       int stop;
@@ -526,23 +290,12 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
       }
       const int64_t k0 = row_at(r, 0);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint8_t* row = kbase + (OCT ? k0 + (4 * b + (c & 3)) * step : b ? row_at(r, 1) : k0);
-        if constexpr (FP4)
-          x.load_k(b, row, static_cast<const uint8_t*>(a.kv.k) + (OCT ? scale_at(r, 0) + 4 * b + (c & 3) : scale_at(r, b)),
-                   int(a.kv.page.d), g);
-        else x.load_k(b, row, g);
-      }
+      for (int b = 0; b < 2; ++b) x.load_k(b, kbase + (OCT ? k0 + (4 * b + (c & 3)) * step : b ? row_at(r, 1) : k0), g);
     };
     auto load_values = [&](TileT& x, const Rows<OCT>& r) {
       const int64_t v0 = row_at(r, OCT ? 1 : 2);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x.load_v(i, vbase + (OCT ? v0 + i * step : i ? row_at(r, OCT ? 1 : 2 + i) : v0), c);
-      if constexpr (FP4) {
-#pragma unroll
-        for (int i = 0; i < (OCT ? 1 : 8); ++i)
-          x.load_vs(i, static_cast<const uint8_t*>(a.kv.v) + scale_at(r, OCT ? 1 : 2 + i), int(a.kv.page.d), c);
-      }
     };
     auto load = [&](TileT& x, const Rows<OCT>& r, int t) {
       load_keys(x, r, t);
@@ -736,82 +489,12 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, E, OCT)) decode_kernel(Attn
   }
 }
 
-// Joins the partial results of units that were cut: o = sum o_i 2^(m_i - M),
-// the same for l.  Grid (workgroups, row shares), each workgroup the unit that
-// the one of its number has begun, if any, and one of its rows, so that the
-// chains of dependent reads are short: its launch and their latency bound it.
-// D / 4 threads hold a column quad each, the rest of the 256 share the parts.
-// 2.8 us for 8 units of one sequence, 4 to 5 for a batch, 7 where a unit has up
-// to 43 parts.
-template <class T, int D, int E, bool FEW>
-__global__ void __launch_bounds__(256) decode_join_kernel(AttnArgs a, Work work) {
-  constexpr int kQuads = D / 4, kSplits = 256 / kQuads;
-  __shared__ at_f32x4 lds_o[kSplits][kQuads];
-  __shared__ float lds_m[kSplits], lds_l[kSplits];
-  const Cut cut = work.cuts[blockIdx.x];
-  if (cut.count <= 1) return;
-  const Queries qs = queries_of<FEW>(work, cut.seq);
-  const SeqSpan sp = seq_span(a, a.kv.lens[cut.seq], qs.count);
-  const int blocks_per_head = (qs.count * a.group + kRows - 1) / kRows;
-  const int head = cut.unit / blocks_per_head, unit_row = (cut.unit % blocks_per_head) * kRows;
-  const int rows = min(qs.count * a.group - unit_row, kRows);
-  const int quad = threadIdx.x % kQuads, split = threadIdx.x / kQuads;
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    float M = kNegInf, L = 0.0f;
-    at_f32x4 O = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int i = split; i < cut.count; i += kSplits) {
-      const Partial p = partial_at(work, D, blockIdx.x + i, i == 0);
-      const float m = p.m[r], l = p.l[r];
-      const at_f32x4 o = *reinterpret_cast<const at_f32x4*>(p.o + r * D + 4 * quad);
-      const float mn = fmaxf(M, m), f = rebase_joined(M, mn), h = rebase_joined(m, mn);
-      L = L * f + l * h;
-      O = O * f + o * h;
-      M = mn;
-    }
-    __syncthreads();              // the row before has been read
-    lds_o[split][quad] = O;
-    if (quad == 0) {
-      lds_m[split] = M;
-      lds_l[split] = L;
-    }
-    __syncthreads();
-    if (split) continue;
-    M = lds_m[0];
-    for (int i = 1; i < kSplits; ++i) M = fmaxf(M, lds_m[i]);
-    L = 0.0f;
-    O = (at_f32x4){0, 0, 0, 0};
-    for (int i = 0; i < kSplits; ++i) {
-      const float f = rebase_joined(lds_m[i], M);
-      L += f * lds_l[i];
-      O += lds_o[i][quad] * f;
-    }
-    finish<T, D, E, FEW>(a, work, head, qs, sp, unit_row + r, 4 * quad, M, L, O);
-  }
-}
-
 // Workgroups of a full card.
 int full_card(int D, int E, bool oct) { return 256 * wgs_per_cu(D, E, oct); }
 constexpr int kMaxWgs = 256 * kMaxPerCu;
 
 int64_t all_units(int64_t seqs, int q_heads, int heads) {
   return seqs * heads * ((q_heads / heads + kRows - 1) / kRows);
-}
-
-size_t workspace_bytes(int rows, int D, int wgs) {
-  return size_t(wgs) * (2 * size_t(partial_floats(rows, D)) * 4 + sizeof(Cut));
-}
-
-// [parts] [cuts]
-Work work_at(void* workspace, int rows, int D, int wgs) {
-  Work w;
-  w.rows = rows;
-  w.parts = static_cast<float*>(workspace);
-  w.cuts = reinterpret_cast<Cut*>(w.parts + size_t(wgs) * 2 * partial_floats(rows, D));
-  w.cu = nullptr;
-  w.tokens = 0;
-  w.group = fast_div(1);
-  return w;
 }
 
 template <class T, int D, int E, bool OCT, bool FEW>
@@ -849,9 +532,6 @@ hipError_t launch_dim(const AttnArgs& a, const int32_t* cu, int64_t tokens, int 
 
 hipError_t launch_any(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype, int D,
                       void* workspace, hipStream_t stream) {
-  if (cache_dtype == W4A4_E2M1)
-    return dtype == W4A4_BF16 ? launch_dim<Bf16, 0>(a, cu, tokens, D, workspace, stream)
-                              : launch_dim<F16, 0>(a, cu, tokens, D, workspace, stream);
   const bool e4m3 = cache_dtype == W4A4_E4M3;
   if (dtype == W4A4_BF16)
     return e4m3 ? launch_dim<Bf16, 1>(a, cu, tokens, D, workspace, stream)
@@ -868,6 +548,7 @@ size_t attn_decode_workspace(int q_heads, int heads, int head_dim) {
 
 hipError_t launch_attn_decode(const AttnArgs& a, int cache_dtype, int dtype, int head_dim, void* workspace,
                               hipStream_t stream) {
+  if (cache_dtype == W4A4_E2M1) return launch_attn_fp4(a, nullptr, a.kv.seqs, dtype, head_dim, workspace, stream);
   return launch_any(a, nullptr, a.kv.seqs, cache_dtype, dtype, head_dim, workspace, stream);
 }
 
@@ -880,14 +561,20 @@ hipError_t launch_attn_decode(const AttnArgs& a, int cache_dtype, int dtype, int
 // sequences without new tokens, which either way serves alike where they are many:
 // 256 tokens on 8000 beside 63 of 1000, bf16, 169 / 172 us (alone, as row tiles with
 // the keys split, 74).
-bool attn_few_serves(int64_t seqs, int64_t tokens, int group, int page_size) {
+// (4 bits: attn_fp4.hip has up to three blocks of 16.)
+bool attn_few_serves(int64_t seqs, int64_t tokens, int group, int page_size, int cache_dtype, int head_dim) {
+  if (cache_dtype == W4A4_E2M1) return page_size % 8 == 0 && attn_fp4_blocks(seqs, tokens, group, head_dim) > 0;
   return page_size % 8 == 0 && tokens * group <= seqs * kRows;
 }
 
-size_t attn_few_workspace(int head_dim) { return workspace_bytes(kRows, head_dim, kMaxWgs); }
+size_t attn_few_workspace(int64_t seqs, int64_t tokens, int group, int cache_dtype, int head_dim) {
+  if (cache_dtype == W4A4_E2M1) return attn_fp4_workspace(kRows * attn_fp4_blocks(seqs, tokens, group, head_dim), head_dim);
+  return workspace_bytes(kRows, head_dim, kMaxWgs);
+}
 
 hipError_t launch_attn_few(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype,
                            int head_dim, void* workspace, hipStream_t stream) {
+  if (cache_dtype == W4A4_E2M1) return launch_attn_fp4(a, cu, tokens, dtype, head_dim, workspace, stream);
   return launch_any(a, cu, tokens, cache_dtype, dtype, head_dim, workspace, stream);
 }
 

@@ -856,9 +856,10 @@ hipError_t launch_dim(const AttnArgs& a, const PrefillWork& w, int D, hipStream_
 }  // namespace
 
 // [parts] [used]
-size_t attn_prefill_workspace(int64_t seqs, int64_t tokens, int q_heads, int heads, int head_dim, int page_size) {
-  if (attn_few_serves(seqs, tokens, q_heads / heads, page_size))
-    return attn_few_workspace(head_dim);
+size_t attn_prefill_workspace(int64_t seqs, int64_t tokens, int q_heads, int heads, int head_dim, int page_size,
+                              int cache_dtype) {
+  if (attn_few_serves(seqs, tokens, q_heads / heads, page_size, cache_dtype, head_dim))
+    return attn_few_workspace(seqs, tokens, q_heads / heads, cache_dtype, head_dim);
   const int64_t tiles = row_tiles(seqs, tokens, q_heads / heads);
   const int splits = key_splits(tiles, heads);
   if (splits == 1) return 0;
@@ -866,15 +867,16 @@ size_t attn_prefill_workspace(int64_t seqs, int64_t tokens, int q_heads, int hea
 }
 
 // Of the row tiles' launch (few rows have no more than fill the card: 0).
-int64_t attn_prefill_workgroups(int64_t seqs, int64_t tokens, int q_heads, int heads, int page_size) {
-  if (attn_few_serves(seqs, tokens, q_heads / heads, page_size)) return 0;
+int64_t attn_prefill_workgroups(int64_t seqs, int64_t tokens, int q_heads, int heads, int head_dim, int page_size,
+                                int cache_dtype) {
+  if (attn_few_serves(seqs, tokens, q_heads / heads, page_size, cache_dtype, head_dim)) return 0;
   const int64_t tiles = row_tiles(seqs, tokens, q_heads / heads);
   return tiles * heads * key_splits(tiles, heads);
 }
 
 hipError_t launch_attn_prefill(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype,
                                int head_dim, void* workspace, hipStream_t stream) {
-  if (attn_few_serves(a.kv.seqs, tokens, a.group, int(a.kv.page.d)))
+  if (attn_few_serves(a.kv.seqs, tokens, a.group, int(a.kv.page.d), cache_dtype, head_dim))
     return launch_attn_few(a, cu, tokens, cache_dtype, dtype, head_dim, workspace, stream);
   PrefillWork w;
   w.cu = cu;

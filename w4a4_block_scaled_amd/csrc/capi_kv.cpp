@@ -40,8 +40,10 @@ w4a4_status check_cache(const char* what, const w4a4_kv_cache* c) {
   if (!c->k || !c->v) return fail(W4A4_ERR_NULL, "%s: cache k and v must be non-NULL", what);
   if (c->dtype == W4A4_E2M1) {
     const int64_t bytes = page_bytes(c->page_size, c->heads, c->head_dim);
-    if (c->page_stride < bytes || c->token_stride != 0 || c->head_stride != 0)
-      return fail(W4A4_ERR_SHAPE, "%s: E2M1 pages of %lld bytes, page stride %lld, token and head strides %lld and %lld (need 0)",
+    if (c->page_stride < bytes || c->page_stride >= kMaxIndex || c->token_stride != 0 || c->head_stride != 0)
+      return fail(W4A4_ERR_SHAPE,
+                  "%s: E2M1 pages of %lld bytes, page stride %lld (need less than 2^31), token and head strides %lld and "
+                  "%lld (need 0)",
                   what, (long long)bytes, (long long)c->page_stride, (long long)c->token_stride,
                   (long long)c->head_stride);
     if (c->k_scale || c->v_scale) return fail(W4A4_ERR_FORMAT, "%s: an E2M1 cache has no scales per head", what);
@@ -398,7 +400,8 @@ size_t w4a4_attn_prefill_workspace_bytes(const w4a4_kv_cache* cache, int64_t seq
   if (check_cache("attn_prefill_workspace_bytes", cache) != W4A4_OK || !heads_ok(cache, q_heads) || seqs <= 0 ||
       tokens <= 0 || tokens * q_heads >= kMaxRows)
     return 0;
-  return w4a4::attn_prefill_workspace(seqs, tokens, q_heads, cache->heads, cache->head_dim, cache->page_size);
+  return w4a4::attn_prefill_workspace(seqs, tokens, q_heads, cache->heads, cache->head_dim, cache->page_size,
+                                      cache->dtype);
 }
 
 w4a4_status w4a4_attn_prefill(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, const int32_t* cu, int64_t tokens,
@@ -416,7 +419,8 @@ w4a4_status w4a4_attn_prefill(const w4a4_kv_cache* cache, const w4a4_kv_seqs* se
                   lse, workspace, ws_bytes, need);
   if (st != W4A4_OK) return st;
   if (tokens == 0) return ok();
-  if (w4a4::attn_prefill_workgroups(seqs->seqs, tokens, q_heads, cache->heads, cache->page_size) >= kMaxGrid)
+  if (w4a4::attn_prefill_workgroups(seqs->seqs, tokens, q_heads, cache->heads, cache->head_dim, cache->page_size,
+                                     cache->dtype) >= kMaxGrid)
     return fail(W4A4_ERR_SHAPE, "%s: %lld tokens of %d sequences are too many for one call", what, (long long)tokens,
                 int(seqs->seqs));
   if (!cu) return fail(W4A4_ERR_NULL, "%s: cu must be non-NULL", what);

@@ -117,13 +117,23 @@ hipError_t launch_attn_decode(const AttnArgs& a, int cache_dtype, int dtype, int
                               hipStream_t stream);
 
 // The same kernel for several queries per sequence, where there are few of them.
-bool attn_few_serves(int64_t seqs, int64_t tokens, int group, int page_size);
-size_t attn_few_workspace(int head_dim);
+bool attn_few_serves(int64_t seqs, int64_t tokens, int group, int page_size, int cache_dtype, int head_dim);
+size_t attn_few_workspace(int64_t seqs, int64_t tokens, int group, int cache_dtype, int head_dim);
 hipError_t launch_attn_few(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype,
                            int head_dim, void* workspace, hipStream_t stream);
 
-size_t attn_prefill_workspace(int64_t seqs, int64_t tokens, int q_heads, int heads, int head_dim, int page_size);
-int64_t attn_prefill_workgroups(int64_t seqs, int64_t tokens, int q_heads, int heads, int page_size);
+// Over a 4-bit cache: one query per sequence (cu NULL), or a few (pages of a multiple of 8).
+// attn_fp4_blocks: blocks of 16 rows that a kv head of a sequence has on average, 0 where
+// they are too many.
+int attn_fp4_blocks(int64_t seqs, int64_t tokens, int group, int head_dim);
+size_t attn_fp4_workspace(int rows, int head_dim);
+hipError_t launch_attn_fp4(const AttnArgs& a, const int32_t* cu, int64_t tokens, int dtype, int head_dim,
+                           void* workspace, hipStream_t stream);
+
+size_t attn_prefill_workspace(int64_t seqs, int64_t tokens, int q_heads, int heads, int head_dim, int page_size,
+                              int cache_dtype);
+int64_t attn_prefill_workgroups(int64_t seqs, int64_t tokens, int q_heads, int heads, int head_dim, int page_size,
+                                int cache_dtype);
 hipError_t launch_attn_prefill(const AttnArgs& a, const int32_t* cu, int64_t tokens, int cache_dtype, int dtype,
                                int head_dim, void* workspace, hipStream_t stream);
 
