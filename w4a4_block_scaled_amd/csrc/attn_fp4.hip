@@ -8,12 +8,9 @@
 // Scores S^T = K Q^T come from the scaled 16 x 16 x 128 MFMA, which takes the codes and
 // the scale bytes as they are in the cache.  Its other operand has to be small too: a
 // query's blocks of 32 are split into four parts in FP6 (E2M3), each with a scale of
-// its own.  With the block's largest value in [2, 4) 2^e, a part is right to 2^-4 of its
-// own unit and the parts' units are 2^e, 2^(e - 4), 2^(e - 9) and 2^(e - 14), so that the four
-// together are right to 2^(e - 18).  (Products of 2 and 4 significant bits add up in
-// fp32; measured against 64 bits 2^-23 of the sum of their sizes where a block's values
-// are of one size, 2^-16 where they span 2^16.)  D = 64 fills the instruction's 128
-// products with two parts.
+// its own (attn_fp4.h).  (Products of 2 and 4 significant bits add up in fp32; measured
+// against 64 bits 2^-23 of the sum of their sizes where a block's values are of one size,
+// 2^-16 where they span 2^16.)  D = 64 fills the instruction's 128 products with two parts.
 //
 // O^T = V^T P^T as in attn_decode.hip: V's operand is 8 tokens of one d per lane, so the
 // codes are widened to BF16 (one instruction per pair, which takes the scale) and pairs
@@ -22,57 +19,13 @@
 // range that the cache's scales have.
 #include <algorithm>
 
+#include "attn_fp4.h"
 #include "attn_list.h"
 
 namespace w4a4 {
 namespace {
 
-typedef int at_i32x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t at_u32x6 __attribute__((ext_vector_type(6)));
-typedef float at_f32x32 __attribute__((ext_vector_type(32)));
-typedef __bf16 at_bf16x32 __attribute__((ext_vector_type(32)));
-
 constexpr int kParts = 4;                                // of a query's block
-__host__ __device__ constexpr int part_shift(int p) { return p == 0 ? 0 : 5 * p - 1; }
-
-// The four parts of 32 values of a query and their scale bytes (one each; NaN's
-// byte where a value is Inf or NaN).  Exponents below -100 count as that: 2^-118 of
-// an error.
-template <class T>
-__device__ __forceinline__ uint32_t split_query(const uint16_t* row, at_u32x6 (&part)[kParts]) {
-  float x[32];
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const at_u32x4 u = *reinterpret_cast<const at_u32x4*>(row + 8 * i);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[8 * i + 2 * k] = T::low(u[k]);
-      x[8 * i + 2 * k + 1] = T::high(u[k]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 32; ++i) top = max(top, __builtin_bit_cast(uint32_t, x[i]) & 0x7fffffffu);
-  const bool odd = top >= 0x7f800000u;
-  const int e = max(int(top >> 23) - 128, -100);
-  uint32_t bytes = 0;
-#pragma unroll
-  for (int p = 0; p < kParts; ++p) {
-    const uint32_t byte = uint32_t(e - part_shift(p) + 127);
-    const float scale = __builtin_bit_cast(float, byte << 23);
-    at_bf16x32 b;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) b[i] = (__bf16)x[i];
-    part[p] = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(b, scale);
-    if (p + 1 < kParts) {
-      const at_f32x32 y = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(part[p], scale);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] -= y[i];
-    }
-    bytes |= (odd ? 255u : byte) << (8 * p);
-  }
-  return bytes;
-}
 
 // Keys in the codes k with the scale byte ks, times part `PART`'s operand; its scale is
 // byte BYTE of qs.
@@ -195,7 +148,7 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(A
       for (int i = 0; i < kSteps; ++i) {
         if (kLdsQ && (n * kSteps + i) % 4 != wave) continue;       // the waves share them
         at_u32x6 part[kParts];
-        uint32_t bytes = split_query<T>(qp + (D == 64 ? 32 * (g & 1) : 128 * i + 32 * g), part);
+        uint32_t bytes = split_query<T, kParts>(qp + (D == 64 ? 32 * (g & 1) : 128 * i + 32 * g), part);
         if constexpr (D == 64) {        // quarters 0, 1: parts 0 and 2; quarters 2, 3: parts 1 and 3
 #pragma unroll
           for (int k = 0; k < 2; ++k)

@@ -28,6 +28,10 @@
 // 2.0e-4; a second part would double the second product).  Where the keys are split
 // the matrix cores are idle, and two parts are taken, as in decoding.
 //
+// FP4 (4-bit caches): keys lie in LDS as the cache has them, codes and scale bytes, and the
+// scores come from the scaled 32 x 32 x 64 MFMA, the queries in four FP6 parts (attn_fp4.h);
+// values are widened on their way to LDS, as from E4M3.
+//
 // Measured, 32 / 8 heads, D = 128, causal 8192 bf16: 512 to 528 us, 1.05 PFLOP/s (a
 // library product of 8192^3 reaches 1.44 here; the MFMAs are busy 55% of the
 // time on the ragged chunks, at 1.65 GHz), E4M3 537 to 557 us, D = 64 320 to 337;
@@ -35,8 +39,9 @@
 // 491 to 514 us.  82 tokens: 10.5 us, 8.7 of them the kernel's.
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
-#include "attn_common.h"
+#include "attn_fp4.h"
 
 namespace w4a4 {
 namespace {
@@ -139,6 +144,16 @@ __device__ __forceinline__ at_u32x2 transpose_from_lds(const Lds16* src) {
   return __builtin_bit_cast(at_u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS s4*)src));
 }
 
+// f(0) .. f(N - 1), the numbers as types.
+template <int N, class F, int... I>
+__device__ __forceinline__ void unroll(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void unroll(F f) {
+  unroll<N>(f, std::make_integer_sequence<int, N>());
+}
+
 // ONE: the page size is a multiple of 16, so that 16 tokens from a multiple of
 // 16 lie on one page, and one lookup serves the wave that stages them (causal
 // 8192: 512 us; row by row, page 11, 566).
@@ -153,11 +168,19 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   constexpr int kPiece = FP4 && D == 64 ? 8 : 16; // bytes of a load
   constexpr int kRowLoads = FP4 ? D / 2 / kPiece : D * E / 16;       // of a cache row
   constexpr int kLoads = kBN * kRowLoads / 256;   // per thread and tensor
-  constexpr int kSteps = D / 16;                  // score MFMAs per 32 tokens
+  // Score MFMAs per 32 tokens: of 16 d's; FP4: of 64 d's and a part of the queries each (as
+  // long together as 16-bit ones, without widening the keys: ragged chunks over 28 / 4 heads
+  // 528 -> 506 us.  Three parts, 477 us, would leave 2^-13 of a block's unit, which a query
+  // with an outlier feels).
+  constexpr int kParts = FP4 ? 4 : 1;
+  constexpr int kSteps = FP4 ? D / 64 * kParts : D / 16;
+  constexpr int kKeyOps = FP4 ? D / 64 : D / 16;  // key operands of 32 tokens
+  constexpr int kKeyLoads = FP4 ? (D == 256 ? 2 : 1) : 1;       // FP4: 16-byte copies of a tile's keys per thread
   constexpr int kBlocks = D / 32;                 // value blocks
   // Two tiles of keys, two of values, and three words.  One object: with several,
   // the compiler no longer sees that copies into one tile leave the others alone,
   // and waits for them before every read.
+  // (FP4: keys as they are in the cache, and their scale bytes.)
   __shared__ __align__(16) uint16_t smem[4 * kBN * D + 8];
   volatile LDS_AS int* const flags = (volatile LDS_AS int*)((Lds16*)smem + 4 * kBN * D);
   constexpr int kBad = 2;                         // [0], [1]: the tile with Inf or NaN among its values
@@ -204,12 +227,23 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   const uint8_t* kbase = static_cast<const uint8_t*>(a.kv.k) + head * a.kv.head_stride * kUnit;
   const uint8_t* vbase = static_cast<const uint8_t*>(a.kv.v) + head * a.kv.head_stride * kUnit;
 
-  at_u32x4 q[kSteps];
+  std::conditional_t<FP4, at_u32x6, at_u32x4> q[kSteps];
+  uint32_t q_scale[FP4 ? D / 64 : 1];         // FP4: the parts' scale bytes of 64 d's
   {
     const uint16_t* qp = static_cast<const uint16_t*>(a.q) + int64_t(min(max(qi, 0), w.tokens - 1)) * a.q_row +
-                         (int64_t(head) * a.group + in_group) * a.q_head + 8 * half;
+                         (int64_t(head) * a.group + in_group) * a.q_head;
+    if constexpr (FP4) {
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) q[j] = *reinterpret_cast<const at_u32x4*>(qp + 16 * j);
+      for (int j = 0; j < D / 64; ++j) {
+        at_u32x6 part[kParts];
+        q_scale[j] = split_query<T, kParts>(qp + 64 * j + 32 * half, part);
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) q[kParts * j + p] = part[p];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) q[j] = *reinterpret_cast<const at_u32x4*>(qp + 8 * half + 16 * j);
+    }
   }
 
   auto tile_at = [&](int t, int* stop) {
@@ -256,8 +290,15 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
     koff[j] = row + kPiece * chunk(j, false);
     voff[j] = row + kPiece * chunk(j, true);
   }
-  // FP4: a load's pieces are of one block each; its scale byte
+  // FP4.  Of the values a thread has one piece per load, all of one block, and its scale
+  // byte; the keys are copied as they are, kKeyLoads pieces per thread (D = 64: the upper
+  // half of a wave again those of the lower, to a place that is not read), and one scale
+  // byte per 4 blocks, of the wave's token lane % 16.
   const uint32_t soff = FP4 ? (lane % kRowLoads * kPiece / 16) * a.kv.page.d : 0;
+  constexpr int kKeyRow = D / 2;                  // bytes
+  auto key_row = [&](int j) { return D == 64 ? (lane & 31) >> 1 : (j * 64 + lane) / (kKeyRow / 16); };       // of the wave's 16
+  auto raw_swz = [](int r) { return D == 64 ? (r >> 3) & 1 : D == 128 ? (r >> 2) & 3 : (r >> 1) & 7; };
+  auto key_chunk = [&](int j) { return lane % (kKeyRow / 16) ^ raw_swz(key_row(j)); };
   struct Raw {
     at_u32x4 x;
     uint32_t scale;
@@ -265,29 +306,50 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   Raw raw_k[E != 2 ? kLoads : 1], raw_v[E != 2 ? kLoads : 1];
   struct Place {
     int64_t at[ONE ? 1 : kLoads], scale[ONE ? 1 : kLoads];
+    int64_t key[!ONE && FP4 ? kKeyLoads : 1], key_scale;
   };
   auto place_of = [&](int t) {
     const int n = (t - t0) % kAhead;
     if (n == 0) look_ahead(t);
-    const int lo = int(where), hi32 = int(where >> 32);
+    auto uniform = [&](int64_t x) {
+      return int64_t(uint32_t(__builtin_amdgcn_readlane(int(x), n))) | int64_t(__builtin_amdgcn_readlane(int(x >> 32), n)) << 32;
+    };
+    auto from_row = [&](int64_t x, int row) {
+      const int from = 16 * n + row;
+      return int64_t(uint32_t(__shfl(int(x), from))) | int64_t(__shfl(int(x >> 32), from)) << 32;
+    };
     Place x;
     if constexpr (ONE) {
-      x.at[0] = int64_t(uint32_t(__builtin_amdgcn_readlane(lo, n))) | int64_t(__builtin_amdgcn_readlane(hi32, n)) << 32;
-      if constexpr (FP4)
-        x.scale[0] = int64_t(uint32_t(__builtin_amdgcn_readlane(int(where_scale), n))) |
-                     int64_t(__builtin_amdgcn_readlane(int(where_scale >> 32), n)) << 32;
+      x.at[0] = uniform(where);
+      if constexpr (FP4) x.scale[0] = uniform(where_scale);
     } else {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        const int from = 16 * n + load_row(j);
-        x.at[j] = int64_t(uint32_t(__shfl(lo, from))) | int64_t(__shfl(hi32, from)) << 32;
-        if constexpr (FP4)
-          x.scale[j] = int64_t(uint32_t(__shfl(int(where_scale), from))) | int64_t(__shfl(int(where_scale >> 32), from)) << 32;
+        x.at[j] = from_row(where, load_row(j));
+        if constexpr (FP4) x.scale[j] = from_row(where_scale, load_row(j));
+      }
+      if constexpr (FP4) {
+#pragma unroll
+        for (int j = 0; j < kKeyLoads; ++j) x.key[j] = from_row(where, key_row(j));
+        x.key_scale = from_row(where_scale, lane & 15);
       }
     }
     return x;
   };
-  auto load = [&](Lds16* tile, const uint8_t* base, const Place& x, const uint32_t* offset, Raw* raw) {
+  auto load = [&](Lds16* tile, const uint8_t* base, const Place& x, const uint32_t* offset, Raw* raw, auto values) {
+    constexpr bool VALUES = decltype(values)::value;
+    if constexpr (FP4 && !VALUES) {
+      const uint8_t* cache = base - head * a.kv.head_stride;
+#pragma unroll
+      for (int j = 0; j < kKeyLoads; ++j) {
+        Lds16* const to = tile + (wave * kKeyLoads + j) * 64 * 8;
+        const uint32_t off = (ONE ? key_row(j) * kKeyRow : 0) + 16 * key_chunk(j);
+        if constexpr (ONE) copy_to_lds(base + x.at[0], off, to);
+        else copy_to_lds(base + x.key[j] + off, to);
+        raw[j].scale = (cache + (ONE ? x.scale[0] + (lane & 15) : x.key_scale))[uint32_t(min((lane >> 4) + 4 * j, D / 32 - 1)) * a.kv.page.d];
+      }
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const uint8_t* p = base + x.at[ONE ? 0 : j];
@@ -307,9 +369,15 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
       else copy_to_lds(p + offset[j], to);
     }
   };
+  // The scale bytes of a tile's keys: [64 tokens][D / 32, padded to 4] behind the keys.
+  constexpr int kScaleAt = 4 * kKeyLoads * 64 * 16, kScaleRow = D == 256 ? 8 : 4;
   // 8 and 4 bits: the pieces that have come go to LDS as 16-bit elements.
   auto put = [&](Lds16* tile, const Raw* raw, bool v) {
-    if constexpr (FP4) {
+    if (FP4 && !v) {
+      LDS_AS uint8_t* const to = (LDS_AS uint8_t*)tile + kScaleAt + (16 * wave + (lane & 15)) * kScaleRow + (lane >> 4);
+#pragma unroll
+      for (int j = 0; j < kKeyLoads; ++j) to[4 * j] = uint8_t(raw[j].scale);
+    } else if constexpr (FP4) {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         const int r = 16 * wave + load_row(j), c = lane % kRowLoads, z = v ? value_swz<D>(r) : key_swz<D>(r);
@@ -362,7 +430,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
     }
   };
   auto arrived = [] {
-    if constexpr (E == 2) __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
+    if constexpr (E != 1) __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
   };
 
   at_f32x16 o[kBlocks];
@@ -380,9 +448,13 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   // operand of step j (32 tokens: row lane % 32, chunk 2 j + lane / 32), and of the
   // value operand of block n (32 d's, by two transposing reads of 4 tokens x 16
   // d's per 16 lanes; a multiple of 8 tokens does not change the swizzle).
-  int k_at[kSteps], v_at[kBlocks];
+  // (FP4: of step j the block 2 j + lane / 32 of 32 d's.  A wave's 16 tokens have kKeyLoads
+  // KiB of their own; 32 tokens further the swizzle is the same.)
+  int k_at[kKeyOps], v_at[kBlocks];
 #pragma unroll
-  for (int j = 0; j < kSteps; ++j) k_at[j] = col * D + 8 * ((2 * j + half) ^ key_swz<D>(col));
+  for (int j = 0; j < kKeyOps; ++j)
+    k_at[j] = FP4 ? (col >> 4) * kKeyLoads * 512 + (col & 15) * (kKeyRow / 2) + 8 * ((2 * j + half) ^ raw_swz(col & 15))
+                  : col * D + 8 * ((2 * j + half) ^ key_swz<D>(col));
 #pragma unroll
   for (int n = 0; n < kBlocks; ++n) {
     const int i = lane & 15, d = 32 * n + 16 * ((lane >> 4) & 1) + 4 * (i & 3), r = 4 * half + (i >> 2);
@@ -390,7 +462,41 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   }
   // Key operand of MFMA i of a tile's scores (block i % 2 of 32 tokens, step i / 2).
   // Register e of the block's scores is the token 8 (e / 4) + 4 half + e % 4.
-  auto key = [&](const Lds16* kt, int i) { return read16(kt + k_at[i >> 1] + 32 * D * (i & 1)); };
+  auto key = [&](const Lds16* kt, int i) {
+    return read16(kt + k_at[i >> 1] + (FP4 ? kKeyLoads * 1024 : 32 * D) * (i & 1));
+  };
+  // FP4: the scale bytes of a tile's keys: of block b of 32 tokens, byte 2 (j % 2) of word j / 2
+  // is that of step j and this half.
+  struct KeyScales {
+    uint32_t w[2][D == 256 ? 2 : 1];
+  };
+  auto key_scales = [&](const Lds16* kt) {
+    KeyScales x = {};
+    if constexpr (FP4) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int k = 0; k < (D == 256 ? 2 : 1); ++k)
+          x.w[b][k] = *reinterpret_cast<const LDS_AS uint32_t*>((const LDS_AS uint8_t*)kt + kScaleAt + (32 * b + col) * kScaleRow + 4 * k) >> (8 * half);
+    }
+    return x;
+  };
+  // Score MFMA m of 2 kSteps: by steps, in a step by parts (the smallest first), the two
+  // blocks of tokens in turn.  Its key operand, and whether that is done with.
+  constexpr auto key_of = [](int m) { return FP4 ? m / (2 * kParts) * 2 + (m & 1) : m; };
+  constexpr auto key_done = [](int m) { return !FP4 || m % (2 * kParts) >= 2 * kParts - 2; };
+  auto score = [&](auto which, at_u32x4 k, const KeyScales& ks, at_f32x16 c) {
+    constexpr int M = decltype(which)::value;
+    if constexpr (FP4) {
+      constexpr int J = M / (2 * kParts), P = kParts - 1 - M % (2 * kParts) / 2;
+      const at_u32x6 z = q[kParts * J + P];
+      const at_i32x8 x = {int(k.x), int(k.y), int(k.z), int(k.w), 0, 0, 0, 0};
+      const at_i32x8 y = {int(z[0]), int(z[1]), int(z[2]), int(z[3]), int(z[4]), int(z[5]), 0, 0};
+      return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 2, 2 * (J % 2), int(ks.w[M & 1][J / 2]), P, int(q_scale[J]));
+    } else {
+      return T::mfma32(k, q[M >> 1], c);
+    }
+  };
   // Value operand of block n, 16 tokens from tb.
   auto value = [&](const Lds16* vt, int n, int tb) {
     const at_u32x2 x = transpose_from_lds(vt + v_at[n] + tb * D), y = transpose_from_lds(vt + v_at[n] + (tb + 8) * D);
@@ -463,7 +569,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   // Operands are read kDepth MFMAs ahead.
   auto compute = [&](const Lds16* k_next, const Lds16* v_cur, int t, const at_f32x16 (&s)[2], at_f32x16 (&ahead)[2], auto next) {
     constexpr bool NEXT = decltype(next)::value;
-    constexpr int kScores = 2 * kSteps, kValues = 4 * kBlocks, kDepth = D == 256 ? 2 : 4, kFirst = 10;
+    constexpr int kScores = 2 * kSteps, kKeys = 2 * kKeyOps, kValues = 4 * kBlocks, kDepth = D == 256 ? 2 : 4;
+    constexpr int kFirst = 16 * kScores / (kScores + kValues) + 2;      // 10 where both are as many
     const float mm = m == kNegInf ? 0.0f : m;
     at_u32x4 p[4], rest[SPLIT ? 4 : 1];      // weights of 16 tokens as operands (SPLIT: in two parts)
     auto pair = [&](int u) {
@@ -483,20 +590,22 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e) ahead[b][e] = 0.0f;
+      const KeyScales ks = key_scales(k_next);
+      auto operand = [&](int i) { return i < kKeys ? key(k_next, i) : v_operand(i - kKeys); };
 #pragma unroll
-      for (int i = 0; i < kDepth; ++i) f[i] = key(k_next, i);
-#pragma unroll
-      for (int i = 0; i < kScores; ++i) {
-        ahead[i & 1] = T::mfma32(f[i % kDepth], q[i >> 1], ahead[i & 1]);
-        f[i % kDepth] = i + kDepth < kScores ? key(k_next, i + kDepth) : v_operand(i + kDepth - kScores);
+      for (int i = 0; i < kDepth; ++i) f[i] = operand(i);
+      unroll<kScores>([&](auto which) {
+        constexpr int i = decltype(which)::value, k = key_of(i);
+        ahead[i & 1] = score(which, f[k % kDepth], ks, ahead[i & 1]);
+        if constexpr (key_done(i)) f[k % kDepth] = operand(k + kDepth);
 #pragma unroll
         for (int u = i * kFirst / kScores; u < (i + 1) * kFirst / kScores; ++u) pair(u);
         __builtin_amdgcn_sched_barrier(0);
-      }
+      });
       if (!whole(t + 1)) mask(t + 1, ahead);
     } else {
 #pragma unroll
-      for (int i = 0; i < kDepth; ++i) f[i] = v_operand(i);
+      for (int i = 0; i < kDepth; ++i) f[(kKeys + i) % kDepth] = v_operand(i);
 #pragma unroll
       for (int u = 0; u < kFirst; ++u) pair(u);
     }
@@ -504,9 +613,10 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
 #pragma unroll
     for (int v = 0; v < kValues; ++v) {
       const int n = v % kBlocks, i = v / kBlocks;
-      o[n] = T::mfma32(f[v % kDepth], p[i], o[n]);
-      if constexpr (SPLIT) o[n] = T::mfma32(f[v % kDepth], rest[i], o[n]);
-      if (v + kDepth < kValues) f[v % kDepth] = v_operand(v + kDepth);
+      at_u32x4& y = f[(kKeys + v) % kDepth];
+      o[n] = T::mfma32(y, p[i], o[n]);
+      if constexpr (SPLIT) o[n] = T::mfma32(y, rest[i], o[n]);
+      if (v + kDepth < kValues) y = v_operand(v + kDepth);
       if (v < kValues / 2) {
 #pragma unroll
         for (int u = kFirst + v * (16 - kFirst) / (kValues / 2); u < kFirst + (v + 1) * (16 - kFirst) / (kValues / 2); ++u) pair(u);
@@ -527,8 +637,11 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[b][e] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 2 * kSteps; ++i) s[i & 1] = T::mfma32(key(kt, i), q[i >> 1], s[i & 1]);
+    const KeyScales ks = key_scales(kt);
+    unroll<2 * kSteps>([&](auto which) {
+      constexpr int i = decltype(which)::value;
+      s[i & 1] = score(which, key(kt, key_of(i)), ks, s[i & 1]);
+    });
     if (!whole(t)) mask(t, s);
     float mx = kNegInf;
 #pragma unroll
@@ -548,10 +661,10 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
   };
   auto tile_step = [&](Lds16* __restrict__ k_in, Lds16* __restrict__ k_next, Lds16* __restrict__ v_cur,
                        Lds16* __restrict__ v_in, int t, int buf, const at_f32x16 (&s)[2], at_f32x16 (&ahead)[2]) {
-    load(v_in, vbase, here, voff, raw_v);
+    load(v_in, vbase, here, voff, raw_v, std::true_type());
     if (t + 2 < t1) {
       here = place_of(t + 2);
-      load(k_in, kbase, here, koff, raw_k);
+      load(k_in, kbase, here, koff, raw_k, std::false_type());
     }
     settle(v_cur, t, buf);
     compute(k_next, v_cur, t, s, ahead, std::true_type());
@@ -572,8 +685,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
       const bool more = t + 1 < t1;
       if (more) {
         here = place_of(t + 1);
-        load(k_in, kbase, here, koff, raw_k);
-        load(v_in, vbase, here, voff, raw_v);
+        load(k_in, kbase, here, koff, raw_k, std::false_type());
+        load(v_in, vbase, here, voff, raw_v, std::true_type());
       }
       at_f32x16 s[2], none[2];
       // Inf is settled after the rebase by this tile's maximum (the first one's is by
@@ -592,8 +705,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
     };
     if (t0 < t1) {
       here = place_of(t0);
-      load(lk, kbase, here, koff, raw_k);
-      load(lv, vbase, here, voff, raw_v);
+      load(lk, kbase, here, koff, raw_k, std::false_type());
+      load(lv, vbase, here, voff, raw_v, std::true_type());
       __syncthreads();          // the flags are set before a wave marks its tile in them
       arrived();
       put(lk, raw_k, false);
@@ -609,18 +722,19 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) prefill_kernel(AttnArgs
     // the keys of t0, its values, and the keys of t0 + 1; the scores of t0 wait
     // for the first only
     here = place_of(t0);
-    load(lk, kbase, here, koff, raw_k);
+    load(lk, kbase, here, koff, raw_k, std::false_type());
     put(lk, raw_k, false);
-    load(lv, vbase, here, voff, raw_v);
+    load(lv, vbase, here, voff, raw_v, std::true_type());
     put(lv, raw_v, true);
     if (t0 + 1 < t1) {
       here = place_of(t0 + 1);
-      load(lk + kBN * D, kbase, here, koff, raw_k);
+      load(lk + kBN * D, kbase, here, koff, raw_k, std::false_type());
       put(lk + kBN * D, raw_k, false);
       if constexpr (E == 2) __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * kLoads));
     } else if constexpr (E == 2) {
       __builtin_amdgcn_s_waitcnt(wait_vmcnt(kLoads));
     }
+    if constexpr (FP4) arrived();
     __syncthreads();
     at_f32x16 s[2], s2[2];
     scores(lk, t0, s);
