@@ -217,8 +217,8 @@ w4a4_status check_in_place(const char* what, const void* x, int64_t x_row, int64
   return W4A4_OK;
 }
 
-w4a4_status check_rows_grid(const char* what, int64_t tokens, int64_t vectors, int dim) {
-  if (w4a4::rows_workgroups(tokens, vectors, dim) >= kMaxGrid)
+w4a4_status check_rows_grid(const char* what, int64_t tokens, int64_t q_heads, int64_t kv_heads, int dim) {
+  if (w4a4::rows_workgroups(tokens, q_heads, kv_heads, dim) >= kMaxGrid)
     return fail(W4A4_ERR_SHAPE, "%s: %lld rows are too many for one call", what, (long long)tokens);
   return W4A4_OK;
 }
@@ -271,7 +271,7 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs,
   if (st == W4A4_OK) st = check_rows(what, "v", v, v_row, v_head);
   if (st != W4A4_OK) return st;
   if (cache->dtype == W4A4_E2M1) {
-    st = check_rows_grid(what, tokens, 2 * int64_t(cache->heads), cache->head_dim);
+    st = check_rows_grid(what, tokens, 0, cache->heads, cache->head_dim);
     if (st != W4A4_OK) return st;
     w4a4::RowsIn a = rotated_rows(nullptr, nullptr, tokens, cache->head_dim);
     a.kv = view(cache, seqs);
@@ -301,7 +301,7 @@ w4a4_status w4a4_rope(const w4a4_rotation* rotation, int64_t tokens, const int32
   st = check_rows(what, "x", x, x_row, x_head);
   if (st == W4A4_OK) st = check_rows(what, "out", out, o_row, o_head);
   if (st == W4A4_OK) st = check_in_place(what, x, x_row, x_head, out, o_row, o_head);
-  if (st == W4A4_OK) st = check_rows_grid(what, tokens, heads, head_dim);
+  if (st == W4A4_OK) st = check_rows_grid(what, tokens, heads, 0, head_dim);
   if (st != W4A4_OK) return st;
   w4a4::RowsIn a = rotated_rows(rotation, positions, tokens, head_dim);
   a.q_heads = heads;
@@ -331,7 +331,7 @@ w4a4_status w4a4_kv_append_rope(const w4a4_kv_cache* cache, const w4a4_kv_seqs* 
   if (st == W4A4_OK && q_heads) st = check_rows(what, "q", q, q_row, q_head);
   if (st == W4A4_OK && q_heads) st = check_rows(what, "q_out", q_out, o_row, o_head);
   if (st == W4A4_OK && q_heads) st = check_in_place(what, q, q_row, q_head, q_out, o_row, o_head);
-  if (st == W4A4_OK) st = check_rows_grid(what, tokens, q_heads + 2 * int64_t(cache->heads), cache->head_dim);
+  if (st == W4A4_OK) st = check_rows_grid(what, tokens, q_heads, cache->heads, cache->head_dim);
   if (st != W4A4_OK) return st;
   w4a4::RowsIn a = rotated_rows(rotation, positions, tokens, cache->head_dim);
   a.kv = view(cache, seqs);
@@ -358,7 +358,7 @@ w4a4_status w4a4_kv_read(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, c
   if (tokens == 0 || seqs->seqs == 0) return ok();
   st = check_rows(what, "k", k, k_row, k_head);
   if (st == W4A4_OK) st = check_rows(what, "v", v, v_row, v_head);
-  if (st == W4A4_OK) st = check_rows_grid(what, tokens, 2 * int64_t(cache->heads), cache->head_dim);
+  if (st == W4A4_OK) st = check_rows_grid(what, tokens, 0, cache->heads, cache->head_dim);
   if (st != W4A4_OK) return st;
   w4a4::RowsOut a = {};
   a.kv = view(cache, seqs);

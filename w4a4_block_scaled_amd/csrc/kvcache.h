@@ -98,7 +98,7 @@ struct RowsIn {
   float factor;
 };
 // cache_dtype: of kv, if it has heads; dtype: of the rows
-int64_t rows_workgroups(int64_t tokens, int64_t vectors, int dim);      // vectors: heads of a token, in and out
+int64_t rows_workgroups(int64_t tokens, int64_t q_heads, int64_t kv_heads, int dim);      // of launch_rows_in (and _out: more)
 hipError_t launch_rows_in(const RowsIn& a, int cache_dtype, int dtype, hipStream_t stream);
 
 // Rows of the cache in 16 bits.
