@@ -185,3 +185,16 @@ def test_binding_refuses_more():
         w4.kv_append(t["k"], t["v"], *c)
     with pytest.raises(w4.W4A4Error, match="GPU"):
         w4.attn_decode(t["q"], *c)
+
+
+def test_binding_refuses_what_a_c_type_does_not_hold():
+    t = tensors()
+    x, pos, f = t["q"], ints(1, 2, 3), t["freqs"]
+    with pytest.raises(w4.W4A4Error, match="does not fit"):
+        w4.rope(x, pos, f, factor=1e300)
+    wide = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16).expand(1, BIG, 1, 64)
+    with pytest.raises(w4.W4A4Error, match="does not fit"):
+        w4.kv_append(t["k"], t["v"], wide, wide, t["tables"], t["lens"])
+    wide = ints(0)[:, None].expand(BIG, 1)
+    with pytest.raises(w4.W4A4Error, match="does not fit"):
+        w4.kv_append(t["k"], t["v"], t["k_cache"], t["v_cache"], wide, None)

@@ -24,6 +24,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -36,6 +37,7 @@ __all__ = ["FORMATS", "lib", "library_path", "block_size", "scale_dtype", "quant
 FORMATS = {"mxfp4": 0, "nvfp4": 1, "mxint4": 2, "int4g64": 3, "mxfp8": 4, "mxint8": 5, "int8g128": 6}
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
+_KV_LIB = None
 
 
 class W4A4Error(RuntimeError):
@@ -112,7 +114,19 @@ def lib() -> ctypes.CDLL:
     L.w4a4_probe_empty.restype = i32
     L.w4a4_probe_mfma_fp4.argtypes = [vp, ctypes.c_int, ctypes.c_int, vp, vp]
     L.w4a4_probe_mfma_fp4.restype = i32
-    cp, sp, f32 = ctypes.POINTER(_KvCache), ctypes.POINTER(_KvSeqs), ctypes.c_float
+    _declare_kv(L, ctypes.POINTER(_KvCache), ctypes.POINTER(_KvSeqs), ctypes.POINTER(_Rotation))
+    L.w4a4_last_error.argtypes = []
+    L.w4a4_last_error.restype = ctypes.c_char_p
+    L.w4a4_version.argtypes = []
+    L.w4a4_version.restype = ctypes.c_char_p
+    _LIB = L
+    return L
+
+
+def _declare_kv(L: ctypes.CDLL, cp, sp, rp) -> None:
+    """The entry points of the cache, its attention and rotary positions; cp, sp, rp: how a cache, its
+    sequences and a rotation are passed."""
+    i64, sz, vp, i32, f32 = ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
     L.w4a4_kv_append.argtypes = [cp, sp, vp, i64, i32, vp, i64, i64, vp, i64, i64, vp]
     L.w4a4_attn_decode_workspace_bytes.argtypes = [cp, i64, i32]
     L.w4a4_attn_decode_workspace_bytes.restype = sz
@@ -128,7 +142,6 @@ def lib() -> ctypes.CDLL:
     L.w4a4_kv_free.argtypes = [sp, vp, i32, vp, i32, vp]
     L.w4a4_kv_trim.argtypes = [sp, i32, vp, i32, vp, i32, i32, i32, vp]
     L.w4a4_kv_compact.argtypes = [i32, vp, i64, i64, sp, vp, i32, vp, vp, sz, vp]
-    rp = ctypes.POINTER(_Rotation)
     L.w4a4_kv_page_bytes.argtypes = [i32, i32, i32]
     L.w4a4_kv_page_bytes.restype = sz
     L.w4a4_rope.argtypes = [rp, i64, vp, i32, i32, i32, vp, i64, i64, vp, i64, i64, vp]
@@ -138,12 +151,30 @@ def lib() -> ctypes.CDLL:
     for name in ("rope", "kv_append_rope", "kv_read", "kv_append", "attn_decode", "attn_prefill", "kv_copy_pages", "kv_reserve", "kv_fork", "kv_free",
                  "kv_trim", "kv_compact"):
         getattr(L, "w4a4_" + name).restype = i32
-    L.w4a4_last_error.argtypes = []
-    L.w4a4_last_error.restype = ctypes.c_char_p
-    L.w4a4_version.argtypes = []
-    L.w4a4_version.restype = ctypes.c_char_p
-    _LIB = L
-    return L
+
+
+def _kv_lib() -> ctypes.CDLL:
+    """lib() once more, with those structures passed as packed bytes: a third of a ctypes.Structure's
+    cost per call."""
+    global _KV_LIB
+    if _KV_LIB is None:
+        lib()
+        L = ctypes.CDLL(library_path())
+        _declare_kv(L, ctypes.c_char_p, ctypes.c_char_p, ctypes.c_char_p)
+        _KV_LIB = L
+    return _KV_LIB
+
+
+_PACK_CACHE = struct.Struct("PPPPqqqiiiii").pack       # as _KvCache, _KvSeqs, _Rotation
+_PACK_SEQS = struct.Struct("PPqii").pack
+_PACK_ROTATION = struct.Struct("Piiif").pack
+
+
+def _pack(what: str, pack, *fields) -> bytes:
+    try:
+        return pack(*fields)
+    except (struct.error, OverflowError) as e:
+        raise W4A4Error(2, f"{what}: an argument does not fit its C type ({e})") from None
 
 
 def _fmt(fmt) -> int:
@@ -421,9 +452,12 @@ def _kv_type(t: torch.Tensor, what: str) -> int:
     return f
 
 
+_I32 = torch.int32
+
+
 def _int32(what: str, device, *tensors) -> None:
     for t in tensors:
-        if t is not None and (t.dtype != torch.int32 or t.device != device or not t.is_contiguous()):
+        if t is not None and (t.dtype is not _I32 or t.device != device or not t.is_contiguous()):
             raise W4A4Error(2, f"{what}: index tensors are int32, on {device}, with contiguous entries")
 
 
@@ -434,20 +468,23 @@ def _c_ints(what: str, *numbers) -> None:
             raise W4A4Error(2, f"{what}: {x} does not fit 32 bits")
 
 
-def _kv_cache(what: str, k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> _KvCache:
-    shape, stride = k.shape, k.stride()
-    if len(shape) != 4 or shape != v.shape or stride != v.stride() or stride[3] != 1 or k.dtype != v.dtype or \
+def _kv_cache(what: str, k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> Tuple[bytes, int, int, int, int]:
+    """(w4a4_kv_cache packed, type, page_size, heads, head_dim)"""
+    shape, stride, dtype = k.shape, k.stride(), k.dtype
+    if len(shape) != 4 or shape != v.shape or stride != v.stride() or stride[3] != 1 or dtype != v.dtype or \
             k.device != v.device:
         raise W4A4Error(2, f"{what}: caches {tuple(k.shape)} and {tuple(v.shape)} must be alike, [pages, page_size, "
                            "heads, head_dim] with a contiguous last dimension")
-    f = _kv_type(k, what)
-    ks = vs = None
+    f = _KV_TYPES.get(dtype)
+    if f is None:
+        _kv_type(k, what)
+    ks = vs = 0
     if f == 2:
         for t in (k_scale, v_scale):
             if t is not None and (t.dtype != torch.float32 or t.numel() != shape[2] or not t.is_contiguous() or
                                   t.device != k.device):
                 raise W4A4Error(2, f"{what}: scales are contiguous float32 [heads] on the cache's device")
-        ks, vs = (None if t is None else t.data_ptr() for t in (k_scale, v_scale))
+        ks, vs = (0 if t is None else t.data_ptr() for t in (k_scale, v_scale))
     elif k_scale is not None or v_scale is not None:
         raise W4A4Error(4, f"{what}: scales belong to a float8_e4m3fn cache")
     pages, page, heads, dim = shape
@@ -456,21 +493,25 @@ def _kv_cache(what: str, k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> 
         if dim % 17 or (heads > 1 and stride[2] != dim) or (page > 1 and stride[1] != heads * dim):
             raise W4A4Error(2, f"{what}: a 4-bit cache is [pages, page_size, heads, head_dim * 17 / 32] bytes, each page "
                                f"contiguous, not {tuple(shape)} with strides {tuple(stride)}")
-        return _KvCache(k.data_ptr(), v.data_ptr(), None, None, stride[0] if pages > 1 else -(-size // 16) * 16, 0, 0, f,
-                        pages, page, heads, dim // 17 * 32)
-    return _KvCache(k.data_ptr(), v.data_ptr(), ks, vs, stride[0], stride[1], stride[2], f, pages, page, heads, dim)
+        dim = dim // 17 * 32
+        at = (0, 0, stride[0] if pages > 1 else -(-size // 16) * 16, 0, 0)
+    else:
+        at = (ks, vs, *stride[:3])
+    return _pack(what, _PACK_CACHE, k.data_ptr(), v.data_ptr(), *at, f, pages, page, heads, dim), f, page, heads, dim
 
 
-def _kv_seqs(what: str, tables: torch.Tensor, lens: Optional[torch.Tensor], device) -> _KvSeqs:
-    shape = tables.shape
-    if len(shape) != 2 or (shape[1] > 1 and tables.stride(1) != 1) or tables.dtype != torch.int32 or \
+def _kv_seqs(what: str, tables: torch.Tensor, lens: Optional[torch.Tensor], device) -> Tuple[bytes, int]:
+    """(w4a4_kv_seqs packed, their number)"""
+    shape, stride = tables.shape, tables.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1) or tables.dtype is not _I32 or \
             tables.device != device or (lens is not None and (lens.dim() != 1 or lens.shape[0] != shape[0])):
         raise W4A4Error(2, f"{what}: tables {tuple(tables.shape)} must be int32 [seqs, max_pages] on {device} with "
                            "contiguous rows, lens [seqs]")
-    _int32(what, device, lens)
+    if lens is not None and (lens.dtype is not _I32 or lens.device != device or not lens.is_contiguous()):
+        _int32(what, device, lens)
     seqs, width = shape
-    return _KvSeqs(tables.data_ptr(), None if lens is None else lens.data_ptr(),
-                   tables.stride(0) if seqs > 1 else width, seqs, width)
+    return _pack(what, _PACK_SEQS, tables.data_ptr(), 0 if lens is None else lens.data_ptr(),
+                 stride[0] if seqs > 1 else width, seqs, width), seqs
 
 
 def _kv_rows(what: str, x: torch.Tensor, rows: int, heads, dim: int, device) -> Tuple[int, int, int]:
@@ -510,20 +551,14 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     its last tokens; None: one row per sequence.
     """
     dev = k_cache.device
-    c = _kv_cache("kv_append", k_cache, v_cache, k_scale, v_scale)
-    s = _kv_seqs("kv_append", tables, lens, dev)
+    c, _, _, heads, dim = _kv_cache("kv_append", k_cache, v_cache, k_scale, v_scale)
+    s, seqs = _kv_seqs("kv_append", tables, lens, dev)
     tokens = k.shape[0]
-    rows = (*_kv_rows("kv_append: k", k, tokens, c.heads, c.head_dim, dev),
-            *_kv_rows("kv_append: v", v, tokens, c.heads, c.head_dim, dev))
+    rows = (*_kv_rows("kv_append: k", k, tokens, heads, dim, dev), *_kv_rows("kv_append: v", v, tokens, heads, dim, dev))
     if k.dtype != v.dtype:
         raise W4A4Error(4, f"kv_append: k is {k.dtype}, v is {v.dtype}")
-    cu = None
-    if cu_seqlens is not None:
-        _int32("kv_append", dev, cu_seqlens)
-        if cu_seqlens.numel() != s.seqs + 1:
-            raise W4A4Error(2, f"kv_append: cu_seqlens has {cu_seqlens.numel()} entries for {s.seqs} sequences")
-        cu = cu_seqlens.data_ptr()
-    _check(lib().w4a4_kv_append(c, s, cu, tokens, _kv_type(k, "kv_append"), *rows, _kv_stream(dev)))
+    cu = None if cu_seqlens is None else _cu("kv_append", cu_seqlens, seqs, dev)
+    _check(_kv_lib().w4a4_kv_append(c, s, cu, tokens, _kv_type(k, "kv_append"), *rows, _kv_stream(dev)))
 
 
 def kv_cache_e2m1(pages, page_size: int, heads: int, head_dim: int, device="cuda") -> torch.Tensor:
@@ -583,10 +618,10 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", sc
     return f.to(torch.float32).to(device), factor
 
 
-def _rotation(what: str, freqs: torch.Tensor, interleaved, inverse, factor, device) -> _Rotation:
+def _rotation(what: str, freqs: torch.Tensor, interleaved, inverse, factor, device) -> bytes:
     if freqs.dtype != torch.float32 or freqs.dim() != 1 or not freqs.is_contiguous() or freqs.device != device:
         raise W4A4Error(2, f"{what}: freqs are contiguous float32 [rot_dim / 2] on {device}")
-    return _Rotation(freqs.data_ptr(), 2 * freqs.shape[0], bool(interleaved), bool(inverse), factor)
+    return _pack(what, _PACK_ROTATION, freqs.data_ptr(), 2 * freqs.shape[0], bool(interleaved), bool(inverse), factor)
 
 
 def _positions(what: str, positions: Optional[torch.Tensor], tokens: int, device) -> Optional[int]:
@@ -600,7 +635,7 @@ def _positions(what: str, positions: Optional[torch.Tensor], tokens: int, device
 
 def _like_rows(what: str, out: Optional[torch.Tensor], x: torch.Tensor) -> torch.Tensor:
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return x.new_empty(x.shape)
     if out.dtype != x.dtype:
         raise W4A4Error(4, f"{what} is {out.dtype}, its input {x.dtype}")
     return out
@@ -620,7 +655,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, inter
     at = _positions("rope", positions, tokens, dev)
     out = _like_rows("rope: out", out, x)
     rows = (*_kv_rows("rope: x", x, tokens, None, dim, dev), *_kv_rows("rope: out", out, tokens, heads, dim, dev))
-    _check(lib().w4a4_rope(r, tokens, at, _kv_type(x, "rope"), heads, dim, *rows, _kv_stream(dev)))
+    _check(_kv_lib().w4a4_rope(r, tokens, at, _kv_type(x, "rope"), heads, dim, *rows, _kv_stream(dev)))
     return out
 
 
@@ -635,15 +670,15 @@ def kv_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, 
     positions int32 [tokens]: what is rotated by; None: the tokens' places in their sequences.
     """
     name, dev = "kv_append_rope", k_cache.device
-    c = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
-    s = _kv_seqs(name, tables, lens, dev)
+    c, _, _, kv_heads, dim = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
+    s, seqs = _kv_seqs(name, tables, lens, dev)
     r = _rotation(name, freqs, interleaved, False, factor, dev)
-    tokens, dim = k.shape[0], c.head_dim
-    rows = (*_kv_rows(name + ": k", k, tokens, c.heads, dim, dev), *_kv_rows(name + ": v", v, tokens, c.heads, dim, dev))
+    tokens = k.shape[0]
+    rows = (*_kv_rows("kv_append_rope: k", k, tokens, kv_heads, dim, dev), *_kv_rows("kv_append_rope: v", v, tokens, kv_heads, dim, dev))
     if k.dtype != v.dtype or (q is not None and q.dtype != k.dtype):
         raise W4A4Error(4, f"{name}: k is {k.dtype}, v is {v.dtype}{'' if q is None else f', q is {q.dtype}'}")
     at = _positions(name, positions, tokens, dev)
-    cu = None if cu_seqlens is None else _cu(name, cu_seqlens, s.seqs, dev)
+    cu = None if cu_seqlens is None else _cu(name, cu_seqlens, seqs, dev)
     q_rows, heads, out = (None, 0, 0, None, 0, 0), 0, None
     if q is not None:
         q_at = _kv_rows(name + ": q", q, tokens, None, dim, dev)
@@ -651,7 +686,7 @@ def kv_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, 
         q_rows = (*q_at, *_kv_rows(name + ": q_out", out, tokens, heads, dim, dev))
     elif q_out is not None:
         raise W4A4Error(2, f"{name}: q_out without q")
-    _check(lib().w4a4_kv_append_rope(c, s, cu, tokens, _kv_type(k, name), r, at, heads, *q_rows, *rows, _kv_stream(dev)))
+    _check(_kv_lib().w4a4_kv_append_rope(c, s, cu, tokens, _kv_type(k, name), r, at, heads, *q_rows, *rows, _kv_stream(dev)))
     return out
 
 
@@ -660,21 +695,20 @@ def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, tables: torch.Tensor, 
             k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None, out=None):
     """w4a4_kv_read: (k, v) [tokens, heads, head_dim] of `dtype`: the rows that kv_append with the same
     cu_seqlens (tokens: its last entry; None: one row per sequence) stores, as the
-    cache holds them.  out: (k, v) to write into."""
+    cache holds them.  out: (k, v) to write into; otherwise the two are halves of one allocation."""
     name, dev = "kv_read", k_cache.device
-    c = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
-    s = _kv_seqs(name, tables, lens, dev)
-    cu = None if cu_seqlens is None else _cu(name, cu_seqlens, s.seqs, dev)
+    c, _, _, heads, dim = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
+    s, seqs = _kv_seqs(name, tables, lens, dev)
+    cu = None if cu_seqlens is None else _cu(name, cu_seqlens, seqs, dev)
     if tokens < 0:
         raise W4A4Error(2, f"{name}: {tokens} tokens")
     if out is None:
-        out = tuple(torch.empty((tokens, c.heads, c.head_dim), dtype=dtype, device=dev) for _ in range(2))
+        out = torch.empty((2, tokens, heads, dim), dtype=dtype, device=dev).unbind()
     k, v = out
     if k.dtype != dtype or v.dtype != dtype:
         raise W4A4Error(4, f"{name}: out is {k.dtype} and {v.dtype}, not {dtype}")
-    rows = (*_kv_rows(name + ": k", k, tokens, c.heads, c.head_dim, dev),
-            *_kv_rows(name + ": v", v, tokens, c.heads, c.head_dim, dev))
-    _check(lib().w4a4_kv_read(c, s, cu, tokens, _kv_type(k, name), *rows, _kv_stream(dev)))
+    rows = (*_kv_rows("kv_read: k", k, tokens, heads, dim, dev), *_kv_rows("kv_read: v", v, tokens, heads, dim, dev))
+    _check(_kv_lib().w4a4_kv_read(c, s, cu, tokens, _kv_type(k, name), *rows, _kv_stream(dev)))
     return k, v
 
 
@@ -689,16 +723,14 @@ def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, sc
           workspace):
     dev = k_cache.device
     _c_ints(name, window, sinks)
-    c = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
-    s = _kv_seqs(name, tables, lens, dev)
-    rows, q_heads, dim = q.shape[0], q.shape[1], c.head_dim
-    q_at = _kv_rows(name + ": q", q, s.seqs if cu is None else rows, None, dim, dev)
+    c, f, page, heads, dim = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
+    s, seqs = _kv_seqs(name, tables, lens, dev)
+    rows, q_heads = q.shape[0], q.shape[1]
+    q_at = _kv_rows(name + ": q", q, seqs if cu is None else rows, None, dim, dev)
     if cu is not None:
-        _int32(name, dev, cu)
-        if cu.numel() != s.seqs + 1:
-            raise W4A4Error(2, f"{name}: cu_seqlens has {cu.numel()} entries for {s.seqs} sequences")
+        _cu(name, cu, seqs, dev)
     if out is None:
-        out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=dev)
+        out = q.new_empty((rows, q_heads, dim))
         out_at = (out.data_ptr(), q_heads * dim, dim)
     else:
         out_at = _kv_rows(name + ": out", out, rows, q_heads, dim, dev)
@@ -706,7 +738,7 @@ def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, sc
             raise W4A4Error(4, f"{name}: out is {out.dtype}, q is {q.dtype}")
     lse = torch.empty((rows, q_heads), dtype=torch.float32, device=dev) if return_lse else None
     if workspace is None:
-        size = _attn_workspace_bytes(cu is not None, c.dtype, c.page_size, c.heads, dim, s.seqs, rows, q_heads)
+        size = _attn_workspace_bytes(cu is not None, f, page, heads, dim, seqs, rows, q_heads)
         if size:
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
@@ -716,7 +748,7 @@ def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, sc
     tail = (_kv_type(q, name), q_heads, *q_at, dim ** -0.5 if scale is None else scale, window, sinks, *out_at,
             None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), size,
             _kv_stream(dev))
-    L = lib()
+    L = _kv_lib()
     _check(L.w4a4_attn_decode(c, s, *tail) if cu is None else L.w4a4_attn_prefill(c, s, cu.data_ptr(), rows, *tail))
     return (out, lse) if return_lse else out
 
@@ -808,10 +840,10 @@ def kv_reserve(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, pag
     """w4a4_kv_reserve: pages for lens[s] tokens of every sequence, the lowest
     free ones first; lacking int32 [1]: the number that was not to be had."""
     _c_ints("kv_reserve", page_size)
-    s = _kv_seqs("kv_reserve", tables, lens, refs.device)
+    s, seqs = _kv_seqs("kv_reserve", tables, lens, refs.device)
     _int32("kv_reserve", refs.device, refs, lacking)
-    ws = _kv_workspace(s.seqs, refs.numel(), refs.device)
-    _check(lib().w4a4_kv_reserve(s, page_size, refs.data_ptr(), refs.numel(),
+    ws = _kv_workspace(seqs, refs.numel(), refs.device)
+    _check(_kv_lib().w4a4_kv_reserve(s, page_size, refs.data_ptr(), refs.numel(),
                                  None if lacking is None else lacking.data_ptr(), ws.data_ptr(), ws.numel(),
                                  _kv_stream(refs.device)))
 
@@ -826,22 +858,22 @@ def kv_fork(caches, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor
     """w4a4_kv_fork: sequence children[i] becomes a copy of parents[i] (int32):
     whole pages shared, a last page that is not full copied in every cache."""
     n, arrays, stride, size, pages, page, dev = _kv_arrays("kv_fork", caches)
-    s = _kv_seqs("kv_fork", tables, lens, dev)
+    s, _ = _kv_seqs("kv_fork", tables, lens, dev)
     _int32("kv_fork", dev, refs, parents, children, lacking)
     _check_pages("kv_fork", refs, pages)
     count = _same_length("kv_fork", parents, children)
     ws = _kv_workspace(count, pages, dev)
-    _check(lib().w4a4_kv_fork(n, arrays, stride, size, s, page, refs.data_ptr(), pages, parents.data_ptr(),
+    _check(_kv_lib().w4a4_kv_fork(n, arrays, stride, size, s, page, refs.data_ptr(), pages, parents.data_ptr(),
                               children.data_ptr(), count, None if lacking is None else lacking.data_ptr(),
                               ws.data_ptr(), ws.numel(), _kv_stream(dev)))
 
 
 def kv_free(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, seqs: Optional[torch.Tensor] = None) -> None:
     """w4a4_kv_free: let go of all pages of the sequences `seqs` (int32; None: all)."""
-    s = _kv_seqs("kv_free", tables, lens, refs.device)
+    s, all_seqs = _kv_seqs("kv_free", tables, lens, refs.device)
     _int32("kv_free", refs.device, refs, seqs)
-    _check(lib().w4a4_kv_free(s, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
-                              s.seqs if seqs is None else seqs.numel(), _kv_stream(refs.device)))
+    _check(_kv_lib().w4a4_kv_free(s, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
+                              all_seqs if seqs is None else seqs.numel(), _kv_stream(refs.device)))
 
 
 def kv_trim(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int, window: int, sinks: int = 0,
@@ -849,21 +881,21 @@ def kv_trim(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_s
     """w4a4_kv_trim: let go of the pages that no later token of the sequences
     `seqs` (None: all) sees under a window with sinks."""
     _c_ints("kv_trim", page_size, window, sinks)
-    s = _kv_seqs("kv_trim", tables, lens, refs.device)
+    s, all_seqs = _kv_seqs("kv_trim", tables, lens, refs.device)
     _int32("kv_trim", refs.device, refs, seqs)
-    _check(lib().w4a4_kv_trim(s, page_size, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
-                              s.seqs if seqs is None else seqs.numel(), window, sinks, _kv_stream(refs.device)))
+    _check(_kv_lib().w4a4_kv_trim(s, page_size, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
+                              all_seqs if seqs is None else seqs.numel(), window, sinks, _kv_stream(refs.device)))
 
 
 def kv_compact(caches, tables: torch.Tensor, refs: torch.Tensor) -> torch.Tensor:
     """w4a4_kv_compact: move the pages in use to the front, in every cache, with
     tables and refs; returns remap int32 [pages]: new index, -1 for free pages."""
     n, arrays, stride, size, pages, _, dev = _kv_arrays("kv_compact", caches)
-    s = _kv_seqs("kv_compact", tables, None, dev)
+    s, _ = _kv_seqs("kv_compact", tables, None, dev)
     _int32("kv_compact", dev, refs)
     _check_pages("kv_compact", refs, pages)
     remap = torch.empty(pages, dtype=torch.int32, device=dev)
     ws = _kv_workspace(0, pages, dev)
-    _check(lib().w4a4_kv_compact(n, arrays, stride, size, s, refs.data_ptr(), pages, remap.data_ptr(), ws.data_ptr(),
+    _check(_kv_lib().w4a4_kv_compact(n, arrays, stride, size, s, refs.data_ptr(), pages, remap.data_ptr(), ws.data_ptr(),
                                  ws.numel(), _kv_stream(dev)))
     return remap
