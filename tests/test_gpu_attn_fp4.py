@@ -47,6 +47,33 @@ def test_decode_matches_the_oracle(kv, group, dim, page, lens, high):
         check_decode(c, y, lse, window, sinks, scale, f"window {window}", rows=range(min(len(lens), 8)))
 
 
+@pytest.mark.parametrize("kv,group,dim,page,lens,high", DECODE)
+def test_decode_in_wide_tables(kv, group, dim, page, lens, high):
+    """Tables that hold far more than the lengths: units are cut and joined."""
+    say(f"[decode4 wide] {kv} x {group} heads of {dim}, page {page}, lens {lens[:6]}, {high}")
+    c = make_fp4(kv, group, dim, page, lens, seed=sum(lens) + dim, high=high, dev=device())
+    wide = np.full((len(lens), 2100 // page + 1), -1, np.int32)
+    n = min(c["tables"].shape[1], wide.shape[1])
+    wide[:, :n] = c["tables"][:, :n]
+    c["tables"] = wide if n == c["tables"].shape[1] else c["tables"]
+    for window, sinks in ((0, 0), (100, 5)):
+        y, lse = run_decode(c, window, sinks)
+        check_decode(c, y, lse, window, sinks, label=f"window {window}", rows=range(min(len(lens), 8)))
+
+
+def test_decode_at_the_limit_of_whole_units():
+    """Tables of exactly as many tokens as units are left whole for, and of one page more, by
+    dimension and units; as many sequences as make more units than workgroups."""
+    for kv, dim, page, seqs, tokens in ((2, 128, 16, 2, 1024), (2, 256, 16, 2, 640), (4, 64, 32, 64, 2048), (16, 64, 8, 40, 2048)):
+        for pages in (tokens // page, tokens // page + 1):
+            say(f"[decode4 limit] {kv} heads of {dim}, {seqs} sequences, {pages} pages of {page}")
+            lens = [pages * page] + [(37 * i) % tokens for i in range(1, seqs)]
+            c = make_fp4(kv, 2, dim, page, lens, seed=dim, dev=device())
+            c["tables"] = np.ascontiguousarray(c["tables"][:, :pages])
+            y, lse = run_decode(c, 0, 0)
+            check_decode(c, y, lse, 0, 0, label=f"{pages} pages", rows=[0, 1, seqs - 1])
+
+
 SIZES = {"few": ([500, 40, 1300], [3, 4, 1]), "few, two blocks": ([500, 40, 1300], [3, 9, 8]),
          "few, three blocks": ([500, 40, 1300], [13, 0, 21]), "whole": ([300, 0], [90, 45]), "split": ([1500, 20], [37, 20])}
 
@@ -80,7 +107,7 @@ def test_prefill_groups(kv, group, dim, page, past, new):
         check_prefill(c, y, lse, window, sinks, label=f"window {window}", most=12)
 
 
-WAYS = {"decode": ([900, 40], [1, 1], 16), "decode, page 11": ([900, 40], [1, 1], 11), "few": ([900, 40], [3, 2], 16),
+WAYS = {"decode": ([900, 40], [1, 1], 16), "decode, cut": ([2500, 40], [1, 1], 16), "decode, page 11": ([900, 40], [1, 1], 11), "few": ([900, 40], [3, 2], 16),
         "few, three blocks": ([900, 40], [13, 9], 16),
         "whole": ([700, 40], [150, 60], 16), "whole, page 11": ([700, 40], [150, 60], 11), "split": ([3000, 40], [30, 20], 16)}
 
@@ -147,7 +174,7 @@ def test_without_a_page_and_empty(way):
     assert torch.isnan(y[:n]).all() and torch.equal(y[n:], clean[n:])
 
 
-@pytest.mark.parametrize("way", ["decode", "few", "whole", "split"])
+@pytest.mark.parametrize("way", ["decode", "decode, cut", "few", "whole", "split"])
 def test_far_pages(way):
     """Pages past 2^31 and 2^32 bytes."""
     dev = device()
@@ -173,7 +200,7 @@ def test_far_pages(way):
     assert torch.equal(y, want) and torch.equal(lse, l2)
 
 
-@pytest.mark.parametrize("way", ["decode", "few", "whole", "split"])
+@pytest.mark.parametrize("way", ["decode", "decode, cut", "few", "whole", "split"])
 def test_in_a_graph(way):
     say(f"[graph4] {way}")
     past, new, page = WAYS[way]
@@ -183,7 +210,7 @@ def test_in_a_graph(way):
     out, ws = torch.empty_like(q), torch.empty(64 << 20, dtype=torch.uint8, device=dev)
 
     def call(o, w):
-        if way == "decode":
+        if way.startswith("decode"):
             return w4.attn_decode(q, c["kd"], c["vd"], tables, lens, window=300, sinks=4, out=o, workspace=w)
         return w4.attn_prefill(q, cu, c["kd"], c["vd"], tables, lens, window=300, sinks=4, out=o, workspace=w)
     call(out, ws)

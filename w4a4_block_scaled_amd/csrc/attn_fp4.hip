@@ -76,8 +76,9 @@ constexpr int kMaxPerCu = 4;
 
 // NB: a unit's blocks of 16 rows.  OCT: the page size is a multiple of 8, so 8 tokens
 // from a multiple of 8 lie on one page.  FEW: the sequences have any number of queries.
+// whole_units: a workgroup has the unit of its number, and nothing is left to join.
 template <class T, int D, bool OCT, bool FEW, int NB>
-__global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(AttnArgs a, Work work) {
+__global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(AttnArgs a, Work work, bool whole_units) {
   typedef Fp4Tile<D, OCT> TileT;
   constexpr int kSteps = TileT::kSteps, kRun = TileT::kRun, kRuns = TileT::kRuns;
   constexpr int kUnit = kRows * NB, kBlocks = D / 16, kRow = D / 2;
@@ -94,9 +95,16 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(A
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
   const int64_t wg = blockIdx.x;
-  if (threadIdx.x == 0) work.cuts[wg].count = 0;
+  const bool whole = !FEW && whole_units;
+  if (!whole && threadIdx.x == 0) work.cuts[wg].count = 0;
   Piece pc;
-  if (!find_piece<FEW>(a, work, kUnit, lane, &pc)) return;
+  if (whole) {
+    const int units = a.kv.heads * ((a.group + kUnit - 1) / kUnit), s = int(wg) / units;
+    const int64_t tiles = seq_span(a, a.kv.lens[s], 1).tiles, first = (int(wg) - s * units) * tiles;
+    pc = {first, first + tiles, units * tiles, units, 0, s, 0, 0};
+  } else if (!find_piece<FEW>(a, work, kUnit, lane, &pc)) {
+    return;
+  }
   int64_t item = pc.item, seq_begin = pc.seq_begin;
   int seq = pc.seq;
   const uint32_t page_stride = uint32_t(a.kv.page_stride);       // less than 2^31 (a launch's condition)
@@ -104,7 +112,7 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(A
 
   while (item < pc.end && seq < a.kv.seqs) {
     const Queries qs = queries_of<FEW>(work, seq);
-    const SeqSpan sp = seq_span(a, seq < 64 ? __builtin_amdgcn_readlane(pc.len0, seq) : a.kv.lens[seq], qs.count);
+    const SeqSpan sp = seq_span(a, !whole && seq < 64 ? __builtin_amdgcn_readlane(pc.len0, seq) : a.kv.lens[seq], qs.count);
     const int blocks_per_head = (qs.count * a.group + kUnit - 1) / kUnit;
     const int units = a.kv.heads * blocks_per_head;
     const int64_t in_seq = item - seq_begin;
@@ -496,6 +504,17 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(A
   }
 }
 
+// Units are not cut where the tables hold this many tokens at most, since the search in the
+// list, the second launch and the partial results cost what some tiles do.  Microseconds per
+// call, cut / not cut, D = 128 with 8 kv heads: one sequence of 513 tokens 13.0 / 10.1, of
+// 1025 13.0 / 11.1, of 1537 13.0 / 13.9; 64 of 64 to 513 19.8 / 10.7, of 256 to 2049
+// 29.7 / 22.9; 128 of 512 to 4097 77.7 / 80.1.  D = 256 with 4 heads: one of 1025
+// 13.4 / 17.2, 64 of 128 to 1025 25.1 / 18.8.
+int64_t whole_tokens(int D, int64_t units) {
+  if (units >= 1 << 24) return 0;                        // more workgroups than a launch takes
+  return units >= 256 ? 2048 : D == 256 ? 640 : 1024;
+}
+
 constexpr int kMaxWgs = 256 * kMaxPerCu;
 
 template <class T, int D, bool OCT, bool FEW, int NB>
@@ -510,7 +529,11 @@ hipError_t launch_kernels(const AttnArgs& a, const int32_t* cu, int64_t tokens, 
                             : a.kv.seqs * a.kv.heads * ((a.group + kRows - 1) / kRows);
   const int64_t tiles = (int64_t(a.kv.max_pages) * a.kv.page.d + kTile - 1) / kTile + 2;
   const unsigned grid = unsigned(std::min<int64_t>(wgs, units * tiles));
-  fp4_kernel<T, D, OCT, FEW, NB><<<grid, 256, 0, stream>>>(a, w);
+  if (!FEW && int64_t(a.kv.max_pages) * a.kv.page.d <= whole_tokens(D, units)) {
+    fp4_kernel<T, D, OCT, FEW, NB><<<unsigned(units), 256, 0, stream>>>(a, w, true);
+    return hipGetLastError();
+  }
+  fp4_kernel<T, D, OCT, FEW, NB><<<grid, 256, 0, stream>>>(a, w, false);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   decode_join_kernel<T, D, 0, FEW, kRows * NB><<<dim3(grid, unsigned(w.rows)), 256, 0, stream>>>(a, w);
