@@ -170,11 +170,8 @@ _PACK_SEQS = struct.Struct("PPqii").pack
 _PACK_ROTATION = struct.Struct("Piiif").pack
 
 
-def _pack(what: str, pack, *fields) -> bytes:
-    try:
-        return pack(*fields)
-    except (struct.error, OverflowError) as e:
-        raise W4A4Error(2, f"{what}: an argument does not fit its C type ({e})") from None
+def _unfit(what: str, e: Exception) -> W4A4Error:
+    return W4A4Error(2, f"{what}: an argument does not fit its C type ({e})")
 
 
 def _fmt(fmt) -> int:
@@ -455,10 +452,17 @@ def _kv_type(t: torch.Tensor, what: str) -> int:
 _I32 = torch.int32
 
 
-def _int32(what: str, device, *tensors) -> None:
+# `device` of the helpers below: a GPU's index, -1 for tensors elsewhere (get_device(), cheaper than
+# comparing torch.device objects; _kv_stream refuses -1 before any call).
+
+def _on(device: int) -> str:
+    return "the cache's device" if device < 0 else f"cuda:{device}"
+
+
+def _int32(what: str, device: int, *tensors) -> None:
     for t in tensors:
-        if t is not None and (t.dtype is not _I32 or t.device != device or not t.is_contiguous()):
-            raise W4A4Error(2, f"{what}: index tensors are int32, on {device}, with contiguous entries")
+        if t is not None and (t.dtype is not _I32 or t.get_device() != device or not t.is_contiguous()):
+            raise W4A4Error(2, f"{what}: index tensors are int32, on {_on(device)}, with contiguous entries")
 
 
 def _c_ints(what: str, *numbers) -> None:
@@ -472,7 +476,7 @@ def _kv_cache(what: str, k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> 
     """(w4a4_kv_cache packed, type, page_size, heads, head_dim)"""
     shape, stride, dtype = k.shape, k.stride(), k.dtype
     if len(shape) != 4 or shape != v.shape or stride != v.stride() or stride[3] != 1 or dtype != v.dtype or \
-            k.device != v.device:
+            k.get_device() != v.get_device():
         raise W4A4Error(2, f"{what}: caches {tuple(k.shape)} and {tuple(v.shape)} must be alike, [pages, page_size, "
                            "heads, head_dim] with a contiguous last dimension")
     f = _KV_TYPES.get(dtype)
@@ -482,7 +486,7 @@ def _kv_cache(what: str, k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> 
     if f == 2:
         for t in (k_scale, v_scale):
             if t is not None and (t.dtype != torch.float32 or t.numel() != shape[2] or not t.is_contiguous() or
-                                  t.device != k.device):
+                                  t.get_device() != k.get_device()):
                 raise W4A4Error(2, f"{what}: scales are contiguous float32 [heads] on the cache's device")
         ks, vs = (0 if t is None else t.data_ptr() for t in (k_scale, v_scale))
     elif k_scale is not None or v_scale is not None:
@@ -497,38 +501,44 @@ def _kv_cache(what: str, k: torch.Tensor, v: torch.Tensor, k_scale, v_scale) -> 
         at = (0, 0, stride[0] if pages > 1 else -(-size // 16) * 16, 0, 0)
     else:
         at = (ks, vs, *stride[:3])
-    return _pack(what, _PACK_CACHE, k.data_ptr(), v.data_ptr(), *at, f, pages, page, heads, dim), f, page, heads, dim
+    try:
+        return _PACK_CACHE(k.data_ptr(), v.data_ptr(), *at, f, pages, page, heads, dim), f, page, heads, dim
+    except (struct.error, OverflowError) as e:
+        raise _unfit(what, e) from None
 
 
-def _kv_seqs(what: str, tables: torch.Tensor, lens: Optional[torch.Tensor], device) -> Tuple[bytes, int]:
+def _kv_seqs(what: str, tables: torch.Tensor, lens: Optional[torch.Tensor], device: int) -> Tuple[bytes, int]:
     """(w4a4_kv_seqs packed, their number)"""
     shape, stride = tables.shape, tables.stride()
     if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1) or tables.dtype is not _I32 or \
-            tables.device != device or (lens is not None and (lens.dim() != 1 or lens.shape[0] != shape[0])):
-        raise W4A4Error(2, f"{what}: tables {tuple(tables.shape)} must be int32 [seqs, max_pages] on {device} with "
+            tables.get_device() != device or (lens is not None and (lens.dim() != 1 or lens.shape[0] != shape[0])):
+        raise W4A4Error(2, f"{what}: tables {tuple(tables.shape)} must be int32 [seqs, max_pages] on {_on(device)} with "
                            "contiguous rows, lens [seqs]")
-    if lens is not None and (lens.dtype is not _I32 or lens.device != device or not lens.is_contiguous()):
+    if lens is not None and (lens.dtype is not _I32 or lens.get_device() != device or not lens.is_contiguous()):
         _int32(what, device, lens)
     seqs, width = shape
-    return _pack(what, _PACK_SEQS, tables.data_ptr(), 0 if lens is None else lens.data_ptr(),
-                 stride[0] if seqs > 1 else width, seqs, width), seqs
+    try:
+        return _PACK_SEQS(tables.data_ptr(), 0 if lens is None else lens.data_ptr(), stride[0] if seqs > 1 else width, seqs,
+                          width), seqs
+    except (struct.error, OverflowError) as e:
+        raise _unfit(what, e) from None
 
 
-def _kv_rows(what: str, x: torch.Tensor, rows: int, heads, dim: int, device) -> Tuple[int, int, int]:
+def _kv_rows(what: str, x: torch.Tensor, rows: int, heads, dim: int, device: int) -> Tuple[int, int, int]:
     """(address, row stride, head stride) of rows x [rows, heads, dim]; heads None: any number."""
     shape, stride = x.shape, x.stride()
     if len(shape) != 3 or shape[0] != rows or shape[2] != dim or (heads is not None and shape[1] != heads) or \
-            stride[2] != 1 or x.device != device:
+            stride[2] != 1 or x.get_device() != device:
         raise W4A4Error(2, f"{what}: {tuple(x.shape)} (need [{rows}, {'heads' if heads is None else heads}, {dim}] with a "
-                           f"contiguous last dimension, on {device})")
+                           f"contiguous last dimension, on {_on(device)})")
     return x.data_ptr(), stride[0], stride[1]
 
 
-def _kv_stream(device: torch.device) -> int:
-    """Handle of the current stream of `device`, which has to be a GPU (_stream without the torch.cuda.Stream object)."""
-    if device.type != "cuda":
-        raise W4A4Error(2, f"the cache and everything with it must be on a GPU, not on {device}")
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _kv_stream(device: int) -> int:
+    """Handle of the current stream of GPU `device` (_stream without the torch.cuda.Stream object)."""
+    if device < 0:
+        raise W4A4Error(2, "the cache and everything with it must be on a GPU")
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -550,7 +560,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     cu_seqlens int32 [seqs + 1]: sequence s has the rows cu[s] .. cu[s + 1] - 1,
     its last tokens; None: one row per sequence.
     """
-    dev = k_cache.device
+    dev = k_cache.get_device()
     c, _, _, heads, dim = _kv_cache("kv_append", k_cache, v_cache, k_scale, v_scale)
     s, seqs = _kv_seqs("kv_append", tables, lens, dev)
     tokens = k.shape[0]
@@ -618,13 +628,16 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", sc
     return f.to(torch.float32).to(device), factor
 
 
-def _rotation(what: str, freqs: torch.Tensor, interleaved, inverse, factor, device) -> bytes:
-    if freqs.dtype != torch.float32 or freqs.dim() != 1 or not freqs.is_contiguous() or freqs.device != device:
-        raise W4A4Error(2, f"{what}: freqs are contiguous float32 [rot_dim / 2] on {device}")
-    return _pack(what, _PACK_ROTATION, freqs.data_ptr(), 2 * freqs.shape[0], bool(interleaved), bool(inverse), factor)
+def _rotation(what: str, freqs: torch.Tensor, interleaved, inverse, factor, device: int) -> bytes:
+    if freqs.dtype is not torch.float32 or freqs.dim() != 1 or not freqs.is_contiguous() or freqs.get_device() != device:
+        raise W4A4Error(2, f"{what}: freqs are contiguous float32 [rot_dim / 2] on {_on(device)}")
+    try:
+        return _PACK_ROTATION(freqs.data_ptr(), 2 * freqs.shape[0], bool(interleaved), bool(inverse), factor)
+    except (struct.error, OverflowError) as e:
+        raise _unfit(what, e) from None
 
 
-def _positions(what: str, positions: Optional[torch.Tensor], tokens: int, device) -> Optional[int]:
+def _positions(what: str, positions: Optional[torch.Tensor], tokens: int, device: int) -> Optional[int]:
     if positions is None:
         return None
     _int32(what, device, positions)
@@ -647,7 +660,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, inter
     (int32 [tokens]) over their first 2 * len(freqs) values; freqs and factor as from
     rope_freqs.  interleaved: pairs (2i, 2i + 1) instead of halves.  inverse: back, or a
     gradient.  out: x itself (in place), or other memory."""
-    dev = x.device
+    dev = x.get_device()
     r = _rotation("rope", freqs, interleaved, inverse, factor, dev)
     if x.dim() != 3:
         raise W4A4Error(2, f"rope: x {tuple(x.shape)} (need [tokens, heads, head_dim])")
@@ -669,7 +682,7 @@ def kv_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, 
 
     positions int32 [tokens]: what is rotated by; None: the tokens' places in their sequences.
     """
-    name, dev = "kv_append_rope", k_cache.device
+    name, dev = "kv_append_rope", k_cache.get_device()
     c, _, _, kv_heads, dim = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
     s, seqs = _kv_seqs(name, tables, lens, dev)
     r = _rotation(name, freqs, interleaved, False, factor, dev)
@@ -696,14 +709,14 @@ def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, tables: torch.Tensor, 
     """w4a4_kv_read: (k, v) [tokens, heads, head_dim] of `dtype`: the rows that kv_append with the same
     cu_seqlens (tokens: its last entry; None: one row per sequence) stores, as the
     cache holds them.  out: (k, v) to write into; otherwise the two are halves of one allocation."""
-    name, dev = "kv_read", k_cache.device
+    name, dev = "kv_read", k_cache.get_device()
     c, _, _, heads, dim = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
     s, seqs = _kv_seqs(name, tables, lens, dev)
     cu = None if cu_seqlens is None else _cu(name, cu_seqlens, seqs, dev)
     if tokens < 0:
         raise W4A4Error(2, f"{name}: {tokens} tokens")
     if out is None:
-        out = torch.empty((2, tokens, heads, dim), dtype=dtype, device=dev).unbind()
+        out = torch.empty((2, tokens, heads, dim), dtype=dtype, device=k_cache.device).unbind()
     k, v = out
     if k.dtype != dtype or v.dtype != dtype:
         raise W4A4Error(4, f"{name}: out is {k.dtype} and {v.dtype}, not {dtype}")
@@ -712,7 +725,7 @@ def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, tables: torch.Tensor, 
     return k, v
 
 
-def _cu(what: str, cu: torch.Tensor, seqs: int, device) -> int:
+def _cu(what: str, cu: torch.Tensor, seqs: int, device: int) -> int:
     _int32(what, device, cu)
     if cu.numel() != seqs + 1:
         raise W4A4Error(2, f"{what}: cu_seqlens has {cu.numel()} entries for {seqs} sequences")
@@ -721,7 +734,7 @@ def _cu(what: str, cu: torch.Tensor, seqs: int, device) -> int:
 
 def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, scale, window, sinks, out, return_lse,
           workspace):
-    dev = k_cache.device
+    dev = k_cache.get_device()
     _c_ints(name, window, sinks)
     c, f, page, heads, dim = _kv_cache(name, k_cache, v_cache, k_scale, v_scale)
     s, seqs = _kv_seqs(name, tables, lens, dev)
@@ -736,14 +749,14 @@ def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, sc
         out_at = _kv_rows(name + ": out", out, rows, q_heads, dim, dev)
         if out.dtype != q.dtype:
             raise W4A4Error(4, f"{name}: out is {out.dtype}, q is {q.dtype}")
-    lse = torch.empty((rows, q_heads), dtype=torch.float32, device=dev) if return_lse else None
+    lse = torch.empty((rows, q_heads), dtype=torch.float32, device=k_cache.device) if return_lse else None
     if workspace is None:
         size = _attn_workspace_bytes(cu is not None, f, page, heads, dim, seqs, rows, q_heads)
         if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(size, dtype=torch.uint8, device=k_cache.device)
     else:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise W4A4Error(2, f"{name}: the workspace must be contiguous, on {dev}")
+        if workspace.device != k_cache.device or not workspace.is_contiguous():
+            raise W4A4Error(2, f"{name}: the workspace must be contiguous, on {_on(dev)}")
         size = workspace.numel() * workspace.element_size()
     tail = (_kv_type(q, name), q_heads, *q_at, dim ** -0.5 if scale is None else scale, window, sinks, *out_at,
             None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), size,
@@ -799,8 +812,8 @@ def _kv_arrays(what: str, caches):
     for t in ((caches,) if isinstance(caches, torch.Tensor) else caches):
         layout = _kv_page_layout(what, t)
         if first is None:
-            first, dev = layout, t.device
-        elif layout != first or t.device != dev:
+            first, dev = layout, t.get_device()
+        elif layout != first or t.get_device() != dev:
             raise W4A4Error(2, f"{what}: the caches must be alike")
         at, elt = [t.data_ptr()], t.element_size()
         for n, st in zip(t.shape[:-4], t.stride()[:-4]):
@@ -817,7 +830,7 @@ def _kv_workspace_bytes(rows: int, pages: int) -> int:
     return lib().w4a4_kv_workspace_bytes(rows, pages)
 
 
-def _kv_workspace(rows: int, pages: int, device) -> torch.Tensor:
+def _kv_workspace(rows: int, pages: int, device: int) -> torch.Tensor:
     return torch.empty(_kv_workspace_bytes(rows, pages), dtype=torch.uint8, device=device)
 
 
@@ -840,12 +853,13 @@ def kv_reserve(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, pag
     """w4a4_kv_reserve: pages for lens[s] tokens of every sequence, the lowest
     free ones first; lacking int32 [1]: the number that was not to be had."""
     _c_ints("kv_reserve", page_size)
-    s, seqs = _kv_seqs("kv_reserve", tables, lens, refs.device)
-    _int32("kv_reserve", refs.device, refs, lacking)
-    ws = _kv_workspace(seqs, refs.numel(), refs.device)
+    dev = refs.get_device()
+    s, seqs = _kv_seqs("kv_reserve", tables, lens, dev)
+    _int32("kv_reserve", dev, refs, lacking)
+    stream, ws = _kv_stream(dev), _kv_workspace(seqs, refs.numel(), dev)
     _check(_kv_lib().w4a4_kv_reserve(s, page_size, refs.data_ptr(), refs.numel(),
                                  None if lacking is None else lacking.data_ptr(), ws.data_ptr(), ws.numel(),
-                                 _kv_stream(refs.device)))
+                                 stream))
 
 
 def _check_pages(what: str, refs: torch.Tensor, pages: int) -> None:
@@ -862,18 +876,18 @@ def kv_fork(caches, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor
     _int32("kv_fork", dev, refs, parents, children, lacking)
     _check_pages("kv_fork", refs, pages)
     count = _same_length("kv_fork", parents, children)
-    ws = _kv_workspace(count, pages, dev)
+    stream, ws = _kv_stream(dev), _kv_workspace(count, pages, dev)
     _check(_kv_lib().w4a4_kv_fork(n, arrays, stride, size, s, page, refs.data_ptr(), pages, parents.data_ptr(),
                               children.data_ptr(), count, None if lacking is None else lacking.data_ptr(),
-                              ws.data_ptr(), ws.numel(), _kv_stream(dev)))
+                              ws.data_ptr(), ws.numel(), stream))
 
 
 def kv_free(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, seqs: Optional[torch.Tensor] = None) -> None:
     """w4a4_kv_free: let go of all pages of the sequences `seqs` (int32; None: all)."""
-    s, all_seqs = _kv_seqs("kv_free", tables, lens, refs.device)
-    _int32("kv_free", refs.device, refs, seqs)
+    s, all_seqs = _kv_seqs("kv_free", tables, lens, refs.get_device())
+    _int32("kv_free", refs.get_device(), refs, seqs)
     _check(_kv_lib().w4a4_kv_free(s, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
-                              all_seqs if seqs is None else seqs.numel(), _kv_stream(refs.device)))
+                              all_seqs if seqs is None else seqs.numel(), _kv_stream(refs.get_device())))
 
 
 def kv_trim(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int, window: int, sinks: int = 0,
@@ -881,10 +895,10 @@ def kv_trim(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_s
     """w4a4_kv_trim: let go of the pages that no later token of the sequences
     `seqs` (None: all) sees under a window with sinks."""
     _c_ints("kv_trim", page_size, window, sinks)
-    s, all_seqs = _kv_seqs("kv_trim", tables, lens, refs.device)
-    _int32("kv_trim", refs.device, refs, seqs)
+    s, all_seqs = _kv_seqs("kv_trim", tables, lens, refs.get_device())
+    _int32("kv_trim", refs.get_device(), refs, seqs)
     _check(_kv_lib().w4a4_kv_trim(s, page_size, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
-                              all_seqs if seqs is None else seqs.numel(), window, sinks, _kv_stream(refs.device)))
+                              all_seqs if seqs is None else seqs.numel(), window, sinks, _kv_stream(refs.get_device())))
 
 
 def kv_compact(caches, tables: torch.Tensor, refs: torch.Tensor) -> torch.Tensor:
@@ -894,8 +908,9 @@ def kv_compact(caches, tables: torch.Tensor, refs: torch.Tensor) -> torch.Tensor
     s, _ = _kv_seqs("kv_compact", tables, None, dev)
     _int32("kv_compact", dev, refs)
     _check_pages("kv_compact", refs, pages)
+    stream = _kv_stream(dev)
     remap = torch.empty(pages, dtype=torch.int32, device=dev)
     ws = _kv_workspace(0, pages, dev)
     _check(_kv_lib().w4a4_kv_compact(n, arrays, stride, size, s, refs.data_ptr(), pages, remap.data_ptr(), ws.data_ptr(),
-                                 ws.numel(), _kv_stream(dev)))
+                                 ws.numel(), stream))
     return remap
