@@ -498,12 +498,11 @@ int64_t all_units(int64_t seqs, int q_heads, int heads) {
 }
 
 template <class T, int D, int E, bool OCT, bool FEW>
-hipError_t launch_kernels(const AttnArgs& a, const Work& w, unsigned grid, hipStream_t stream) {
+hipError_t launch_kernels(const AttnArgs& a, const Work& w, unsigned grid, int64_t units, hipStream_t stream) {
   decode_kernel<T, D, E, OCT, FEW><<<grid, 256, 0, stream>>>(a, w);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  decode_join_kernel<T, D, E, FEW><<<dim3(grid, unsigned(w.rows)), 256, 0, stream>>>(a, w);
-  return hipGetLastError();
+  return launch_join<T, D, E, FEW>(a, w, grid, units, stream);
 }
 
 template <class T, int D, int E>
@@ -518,9 +517,9 @@ hipError_t launch(const AttnArgs& a, const int32_t* cu, int64_t tokens, void* wo
   const int64_t units = cu ? a.kv.heads * (tokens * a.group / kRows + a.kv.seqs) : all_units(a.kv.seqs, a.q_heads, a.kv.heads);
   const int64_t tiles = (int64_t(a.kv.max_pages) * a.kv.page.d + kTile - 1) / kTile + 2;
   const unsigned grid = unsigned(std::min<int64_t>(wgs, units * tiles));
-  if (cu) return launch_kernels<T, D, E, true, true>(a, w, grid, stream);
-  return oct ? launch_kernels<T, D, E, true, false>(a, w, grid, stream)
-             : launch_kernels<T, D, E, false, false>(a, w, grid, stream);
+  if (cu) return launch_kernels<T, D, E, true, true>(a, w, grid, units, stream);
+  return oct ? launch_kernels<T, D, E, true, false>(a, w, grid, units, stream)
+             : launch_kernels<T, D, E, false, false>(a, w, grid, units, stream);
 }
 
 template <class T, int E>

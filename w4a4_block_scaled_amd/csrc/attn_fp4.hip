@@ -536,8 +536,7 @@ hipError_t launch_kernels(const AttnArgs& a, const int32_t* cu, int64_t tokens, 
   fp4_kernel<T, D, OCT, FEW, NB><<<grid, 256, 0, stream>>>(a, w, false);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  decode_join_kernel<T, D, 0, FEW, kRows * NB><<<dim3(grid, unsigned(w.rows)), 256, 0, stream>>>(a, w);
-  return hipGetLastError();
+  return launch_join<T, D, 0, FEW, kRows * NB>(a, w, grid, units, stream);
 }
 
 template <class T, int D>

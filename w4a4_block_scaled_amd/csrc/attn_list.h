@@ -4,6 +4,7 @@
 // and the kernel that joins them.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attn_common.h"
@@ -169,57 +170,77 @@ __device__ __forceinline__ bool find_piece(const AttnArgs& a, const Work& work, 
 }
 
 // Joins the partial results of units (of ROWS rows) that were cut: o = sum o_i 2^(m_i - M),
-// the same for l.  Grid (workgroups, row shares), each workgroup the unit that
-// the one of its number has begun, if any, and one of its rows, so that the
-// chains of dependent reads are short: its launch and their latency bound it.
+// the same for l.  Grid (shares of SHARE workgroups of the list, row shares), each
+// workgroup the units that those of its share have begun, if any, and one of their rows, so
+// that the chains of dependent reads are short: its launch and their latency bound it.
 // D / 4 threads hold a column quad each, the rest of the 256 share the parts.
-// 2.8 us for 8 units of one sequence, 4 to 5 for a batch, 7 where a unit has up
-// to 43 parts.
-template <class T, int D, int E, bool FEW, int ROWS = kRows>
-__global__ void __launch_bounds__(256) decode_join_kernel(AttnArgs a, Work work) {
+template <class T, int D, int E, bool FEW, int ROWS, int SHARE>
+__global__ void __launch_bounds__(256) decode_join_kernel(AttnArgs a, Work work, int wgs) {
   constexpr int kQuads = D / 4, kSplits = 256 / kQuads;
   __shared__ at_f32x4 lds_o[kSplits][kQuads];
   __shared__ float lds_m[kSplits], lds_l[kSplits];
-  const Cut cut = work.cuts[blockIdx.x];
-  if (cut.count <= 1) return;
-  const Queries qs = queries_of<FEW>(work, cut.seq);
-  const SeqSpan sp = seq_span(a, a.kv.lens[cut.seq], qs.count);
-  const int blocks_per_head = (qs.count * a.group + ROWS - 1) / ROWS;
-  const int head = cut.unit / blocks_per_head, unit_row = (cut.unit % blocks_per_head) * ROWS;
-  const int rows = min(qs.count * a.group - unit_row, ROWS);
-  const int quad = threadIdx.x % kQuads, split = threadIdx.x / kQuads;
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    float M = kNegInf, L = 0.0f;
-    at_f32x4 O = {0, 0, 0, 0};
+  const int lane = threadIdx.x & 63;
+  uint64_t left = SHARE == 1 ? 1 : __ballot(lane < SHARE && blockIdx.x * SHARE + lane < wgs &&
+                                            work.cuts[blockIdx.x * SHARE + lane].count > 1);
+  for (; left; left &= left - 1) {
+    const int wg = SHARE == 1 ? blockIdx.x
+                              : blockIdx.x * SHARE + __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)left) - 1);
+    const Cut cut = work.cuts[wg];
+    if (SHARE == 1 && cut.count <= 1) return;
+    const Queries qs = queries_of<FEW>(work, cut.seq);
+    const SeqSpan sp = seq_span(a, a.kv.lens[cut.seq], qs.count);
+    const int blocks_per_head = (qs.count * a.group + ROWS - 1) / ROWS;
+    const int head = cut.unit / blocks_per_head, unit_row = (cut.unit % blocks_per_head) * ROWS;
+    const int rows = min(qs.count * a.group - unit_row, ROWS);
+    const int quad = threadIdx.x % kQuads, split = threadIdx.x / kQuads;
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+      float M = kNegInf, L = 0.0f;
+      at_f32x4 O = {0, 0, 0, 0};
 #pragma unroll 4
-    for (int i = split; i < cut.count; i += kSplits) {
-      const Partial p = partial_at(work, D, blockIdx.x + i, i == 0);
-      const float m = p.m[r], l = p.l[r];
-      const at_f32x4 o = *reinterpret_cast<const at_f32x4*>(p.o + r * D + 4 * quad);
-      const float mn = fmaxf(M, m), f = rebase_joined(M, mn), h = rebase_joined(m, mn);
-      L = L * f + l * h;
-      O = O * f + o * h;
-      M = mn;
+      for (int i = split; i < cut.count; i += kSplits) {
+        const Partial p = partial_at(work, D, wg + i, i == 0);
+        const float m = p.m[r], l = p.l[r];
+        const at_f32x4 o = *reinterpret_cast<const at_f32x4*>(p.o + r * D + 4 * quad);
+        const float mn = fmaxf(M, m), f = rebase_joined(M, mn), h = rebase_joined(m, mn);
+        L = L * f + l * h;
+        O = O * f + o * h;
+        M = mn;
+      }
+      __syncthreads();              // the row before has been read
+      lds_o[split][quad] = O;
+      if (quad == 0) {
+        lds_m[split] = M;
+        lds_l[split] = L;
+      }
+      __syncthreads();
+      if (split) continue;
+      M = lds_m[0];
+      for (int i = 1; i < kSplits; ++i) M = fmaxf(M, lds_m[i]);
+      L = 0.0f;
+      O = (at_f32x4){0, 0, 0, 0};
+      for (int i = 0; i < kSplits; ++i) {
+        const float f = rebase_joined(lds_m[i], M);
+        L += f * lds_l[i];
+        O += lds_o[i][quad] * f;
+      }
+      finish<T, D, E, FEW>(a, work, head, qs, sp, unit_row + r, 4 * quad, M, L, O);
     }
-    __syncthreads();              // the row before has been read
-    lds_o[split][quad] = O;
-    if (quad == 0) {
-      lds_m[split] = M;
-      lds_l[split] = L;
-    }
-    __syncthreads();
-    if (split) continue;
-    M = lds_m[0];
-    for (int i = 1; i < kSplits; ++i) M = fmaxf(M, lds_m[i]);
-    L = 0.0f;
-    O = (at_f32x4){0, 0, 0, 0};
-    for (int i = 0; i < kSplits; ++i) {
-      const float f = rebase_joined(lds_m[i], M);
-      L += f * lds_l[i];
-      O += lds_o[i][quad] * f;
-    }
-    finish<T, D, E, FEW>(a, work, head, qs, sp, unit_row + r, 4 * quad, M, L, O);
   }
+}
+
+// `units`: at most so many.  Where they are few, most workgroups of the list have begun
+// none, and 16 at a time are looked at: microseconds of this kernel with 1 / 16, 12 units of
+// 7 rows in 768 workgroups 7.2 / 5.4, 24 of 32 rows in 512 7.1 / 5.2; where a workgroup
+// in three has begun one the call takes 43.0 / 46.7, in a ragged batch 52.2 / 53.6.
+template <class T, int D, int E, bool FEW, int ROWS = kRows>
+hipError_t launch_join(const AttnArgs& a, const Work& w, unsigned wgs, int64_t units, hipStream_t stream) {
+  constexpr int kShare = 16;
+  if (int64_t(wgs) >= 8 * units)
+    decode_join_kernel<T, D, E, FEW, ROWS, kShare><<<dim3((wgs + kShare - 1) / kShare, unsigned(w.rows)), 256, 0, stream>>>(
+        a, w, int(wgs));
+  else
+    decode_join_kernel<T, D, E, FEW, ROWS, 1><<<dim3(wgs, unsigned(w.rows)), 256, 0, stream>>>(a, w, int(wgs));
+  return hipGetLastError();
 }
 
 size_t workspace_bytes(int rows, int D, int wgs) {
