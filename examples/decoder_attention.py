@@ -6,13 +6,13 @@ the cache is kept tidy.
 
 Every step is what a serving loop does for each layer:
 
-    quantize_act -> linear (QKV) -> kv_append -> attn_prefill / attn_decode
+    quantize_act -> linear (QKV) -> kv_append_rope -> attn_prefill / attn_decode
                  -> quantize_act -> linear (O)
 
 with the page bookkeeping around it once per step: kv_reserve before new tokens
 are stored, kv_fork when a sequence is continued in several ways, kv_trim as the
 window moves on, kv_free when a sequence ends, kv_compact when the cache has
-holes.  The weights are random; the outputs are checked for what holds whatever
+holes, kv_read when rows are to be kept elsewhere.  The weights are random; the outputs are checked for what holds whatever
 they are: branches of one prompt that are fed the same tokens give the same
 outputs, also after the cache has been compacted.  (Bit for bit at these sizes,
 where every tile of the attention's work has a workgroup of its own; in a fuller
@@ -46,6 +46,13 @@ class Linear:
         return w4.linear(codes, scales, t, self.blob, FORMAT, self.n, self.k)
 
 
+def empty_cache(cache_type, pages, page, heads, dim, device):
+    """Keys and values in one tensor [2, pages, ...]; torch.uint8 stands for 4 bits."""
+    if cache_type == torch.uint8:
+        return w4.kv_cache_e2m1((2, pages), page, heads, dim, device=device)
+    return torch.zeros(2, pages, page, heads, dim, dtype=torch.bfloat16, device=device).to(cache_type)
+
+
 class Attention:
     """QKV linear, cache, attention and O linear of one layer."""
 
@@ -54,8 +61,8 @@ class Attention:
         self.q_heads, self.kv_heads = q_heads, kv_heads
         self.qkv = Linear((q_heads + 2 * kv_heads) * self.dim, hidden, gen, device)
         self.o = Linear(hidden, hidden, gen, device)
-        shape = (2, pages, page, kv_heads, self.dim)
-        self.cache = torch.zeros(shape, dtype=torch.bfloat16, device=device).to(cache_type)
+        self.freqs, self.factor = w4.rope_freqs(self.dim, 500000.0, scaling="bands", scale=8.0, original=8192, device=device)
+        self.cache = empty_cache(cache_type, pages, page, kv_heads, self.dim, device)
         self.scales = {}
         if cache_type == torch.float8_e4m3fn:
             self.scales = {"k_scale": torch.full((kv_heads,), 0.02, device=device),
@@ -64,7 +71,7 @@ class Attention:
     def __call__(self, x, tables, lens, cu=None, **mask):
         rows = self.qkv(x).view(len(x), -1, self.dim)
         q, k, v = rows.split([self.q_heads, self.kv_heads, self.kv_heads], dim=1)
-        w4.kv_append(k, v, *self.cache, tables, lens, cu_seqlens=cu, **self.scales)
+        q = w4.kv_append_rope(q, k, v, *self.cache, tables, lens, self.freqs, cu_seqlens=cu, factor=self.factor, **self.scales)
         if cu is None:
             y = w4.attn_decode(q, *self.cache, tables, lens, **mask, **self.scales)
         else:
@@ -100,6 +107,14 @@ def run(hidden=1024, q_heads=8, kv_heads=2, prompt=300, steps=24, branches=3, pa
     assert lacking.item() == 0 and torch.isfinite(y).all()
     say(f"prompts of {prompt} and {half} tokens: {int((refs > 0).sum())} of {pages} pages in use")
 
+    # the second prompt's rows, copied out and stored in another cache, are the same there
+    own, at, rows = tables[1:2], lens[1:2], ids(0, half)
+    k, v = w4.kv_read(*layer.cache, own, at, rows, half, **layer.scales)
+    other = empty_cache(cache_type, pages, page, kv_heads, layer.dim, device)
+    w4.kv_append(k, v, *other, own, at, cu_seqlens=rows, **layer.scales)
+    again = w4.kv_read(*other, own, at, rows, half, **layer.scales)
+    assert torch.equal(again[0], k) and torch.equal(again[1], v)
+
     # the first prompt is continued in several ways: the branches share its whole pages
     children = torch.arange(2, seqs, dtype=torch.int32, device=device)
     w4.kv_fork(layer.cache, tables, lens, refs, torch.zeros_like(children), children, lacking=lacking)
@@ -133,6 +148,7 @@ if __name__ == "__main__":
     ap.add_argument("--prompt", type=int, default=700)
     ap.add_argument("--steps", type=int, default=40)
     ap.add_argument("--e4m3", action="store_true", help="an 8-bit cache")
+    ap.add_argument("--e2m1", action="store_true", help="a 4-bit cache")
     a = ap.parse_args()
     run(a.hidden, a.hidden // 128, max(a.hidden // 512, 1), a.prompt, a.steps,
-        cache_type=torch.float8_e4m3fn if a.e4m3 else torch.bfloat16)
+        cache_type=torch.float8_e4m3fn if a.e4m3 else torch.uint8 if a.e2m1 else torch.bfloat16)

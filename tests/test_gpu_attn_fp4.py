@@ -8,6 +8,7 @@ import torch
 import w4a4_block_scaled_amd as w4
 from gpu_common import device, say
 from kv_common import as_f64, check_attention, ints, values
+from oracle import attention as A
 from rows_common import chunks_fp4, make_fp4, on_gpu
 from test_gpu_attn_decode import check as check_decode
 from test_gpu_attn_decode import run as run_decode
@@ -228,6 +229,48 @@ def test_in_a_graph(way):
         (want @ want.transpose(1, 2).contiguous()).sum().item()
 
 
+@pytest.mark.parametrize("way", ["decode", "decode, cut", "few", "few, three blocks", "whole", "split"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("high", ["bf16", "fp16"])
+def test_queries_with_outliers(way, dim, high):
+    """A value of every block of 32 of the queries 2^11 times the others, where the keys are zero: the scores
+    are the others' alone.  Queries enter them within 2^-19 of their block's largest value (four parts
+    of 4 bits, the last one's step 2^-17 of the largest value's power of two, rounded to half of it), which is
+    added to the bound on the scores' error."""
+    if way == "few, three blocks" and dim == 256:
+        pytest.skip("these go as row tiles")
+    say(f"[outliers4] {way}, D = {dim}, {high}")
+    past, new, page = WAYS[way]
+    c = chunks_fp4(2, 4, dim, page, past, new, seed=dim, high=high, dev=device())
+    q = c["q"].clone()
+    q[..., 7::32] = torch.sign(q[..., 7::32]) * 3000
+    c["q"] = q
+    # the keys' codes of those values: the upper half of a byte each
+    at, heads = page * 2 * dim // 2, 2
+    raw = c["kd"].as_strided((c["kd"].shape[0], c["kd"].stride(0)), (c["kd"].stride(0), 1))
+    raw[:, :at].unflatten(1, (heads, page, dim // 2))[..., 3::16] &= 15
+    k64 = c["f64"][0].copy()
+    k64[..., 7::32] = 0
+    c["f64"] = [k64, c["f64"][1]]
+    y, lse = attend(c, way)
+    got, lse, q64 = as_f64(y), lse.cpu().numpy().astype(np.float64), as_f64(q)
+    u, scale = 2.0 ** -8 if high == "bf16" else 2.0 ** -11, dim ** -0.5
+    # decoding and few rows: BF16 weights in two parts whatever the queries' type
+    weights = u if way == "whole" else 2.0 ** -20 if way == "split" and high == "fp16" else 2.0 ** -15
+    for i in sorted({0, 1, len(q) - 1, int(c["cu"][1]) - 1}):
+        s = int(c["seqs"][i])
+        for h in (0, 5, 7):
+            o, ref, (a, big, size, n) = A.attend(q64[i, h], *c["f64"], c["tables"][s], c["lens"][s], int(c["pos"][i]), h // 4,
+                                                 scale, 0, 0)
+            keys = np.abs(A.rows(k64, c["tables"][s], range(n), h // 4)).reshape(n, -1, 32).sum(-1)
+            parts = (keys * np.abs(q64[i, h]).reshape(-1, 32).max(-1)).sum(-1).max() * scale * 2.0 ** -19
+            eta = (dim + 8) * 2.0 ** -23 * (size + parts) + 2.0 ** -22 + parts
+            bound = u * np.abs(o) + (1 + u) * (weights + 2 * eta + n * 2.0 ** -22) * a + n * (2.0 ** -24 if high == "fp16" else 0) * big + 2.0 ** -25
+            err = np.abs(got[i, h] - o)
+            assert np.all(err <= bound), f"row {i} head {h}: off by {err.max():.3e}, bound {bound[err.argmax()]:.3e}"
+            assert abs(lse[i, h] - ref) <= eta + n * 2.0 ** -22 + 2.0 ** -21 + 2.0 ** -22 * abs(ref)
+
+
 def test_a_layer_step_by_step():
     """Rotate and store, then attend, token by token and in one chunk: the 4-bit cache's bytes
     are the same, and the outputs agree with attention over what kv_read gives."""
@@ -255,3 +298,14 @@ def test_a_layer_step_by_step():
     # two roundings of weights and outputs, each half a step, of values below 4
     assert (y.float() - want.float()).abs().max() <= 4 * 2 * 2.0 ** -8
     assert (torch.cat(steps).float() - want.float()).abs().max() <= 4 * 2 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("page,window", [(16, 128), (8, 20), (24, 60)])
+def test_the_example_with_a_cache_of_4_bits(page, window):
+    import sys
+    from pathlib import Path
+    sys.path.insert(0, str(Path(__file__).resolve().parent.parent / "examples"))
+    import decoder_attention
+    dev = device()
+    say(f"[example4] page {page}, window {window}")
+    decoder_attention.run(cache_type=torch.uint8, page=page, window=window, device=dev, say=say)

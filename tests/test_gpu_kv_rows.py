@@ -159,6 +159,124 @@ def test_queries_in_place_between_their_keys():
     assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp4"])
+@pytest.mark.parametrize("seqs", [63, 64, 65, 300])
+@pytest.mark.parametrize("own", [False, True])
+def test_many_sequences(kind, seqs, own):
+    """More sequences than a wave has lanes, many without new tokens, with the tokens' places or positions
+    of one's own; what was stored is read back."""
+    dev = device()
+    say(f"[append_rope] {seqs} sequences, {kind}, own positions {own}")
+    gen, rng, f = torch.Generator().manual_seed(seqs), np.random.default_rng(seqs), freqs_of(64)
+    page, kv, dim = 8, 1, 64
+    new = rng.integers(0, 4, seqs)
+    new[[0, 1, seqs - 1]] = 0
+    past = rng.integers(0, 20, seqs)
+    lens, cu = list(past + new), np.concatenate([[0], np.cumsum(new)])
+    n, pages = int(cu[-1]), sum(-(-x // page) for x in lens) + 1
+    tables = table_of(lens, page, pages, 4, rng)
+    (kd, kb), (vd, vb) = (cache_of(kind, pages, page, kv, dim, gen, dev) for _ in range(2))
+    rows = values((n, 4, dim), "bf16", gen)
+    q, k, v = rows.to(dev).split([2, 1, 1], dim=1)
+    place = np.concatenate([np.arange(b) + a for a, b in zip(past, new)])
+    pos = rng.integers(0, 200000, n) if own else place
+    out = w4.kv_append_rope(q, k, v, kd, vd, ints(tables, dev), ints(lens, dev), torch.from_numpy(f).to(dev),
+                            cu_seqlens=ints(cu, dev), positions=ints(pos, dev) if own else None)
+    check_rotated(out, rows[:, :2], pos, f, "bf16")
+    k64, v64 = R.rotate(as_f64(rows[:, 2:3]), pos, f), as_f64(rows[:, 3:])
+    read = w4.kv_read(kd, vd, ints(tables, dev), ints(lens, dev), ints(cu, dev), n)
+    at = tables[np.repeat(np.arange(seqs), new), place // page], place % page
+    for got, before, exact, back in ((kd, kb, k64, read[0]), (vd, vb, v64, read[1])):
+        if kind == "fp4":
+            want = expected(kind, before, exact, tables, lens, cu, page, kv, dim, None, "bf16")
+            assert np.array_equal(bytes_of(got), want)
+            rows_at = R.decode_blocks(*R.from_pages(want[:, :R.page_bytes(page, kv, dim)], page, kv, dim))[at]
+            assert np.array_equal(as_f64(back), rows_at)
+        else:
+            assert torch.equal(got[at[0], at[1]], back)
+    if kind == "bf16":
+        check_rotated(read[0], rows[:, 2:3], pos, f, "bf16")
+        assert torch.equal(read[1].cpu(), rows[:, 3:])
+
+
+@pytest.mark.parametrize("high", ["bf16", "fp16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_ties_of_8_bits(high, interleaved):
+    """Halfway between two 8-bit values, and the two neighbours of that in the rows' type: to the even one
+    and to the nearer one, for keys at position 0 (which stay as they are) and for values.  With scale 0.75 the
+    quotients are exact where the product 0.75 * value is."""
+    dev = device()
+    say(f"[append_rope] 8-bit ties, {high}")
+    bits = torch.arange(0x08, 0x7e).to(torch.uint8)                       # normal values and their successors
+    mid = (bits.view(torch.float8_e4m3fn).double() + (bits + 1).view(torch.float8_e4m3fn).double()) / 2
+    assert torch.isfinite(mid).all()
+    for unit in (1.0, 0.75, 2.0 ** -7):
+        x = (mid * unit).to(TYPES[high])
+        near = x.view(torch.int16)
+        x = torch.cat([x, (near + 1).view(x.dtype), (near - 1).view(x.dtype)])
+        x = torch.cat([x, -x, torch.zeros(-2 * len(x) % 64, dtype=x.dtype)]).view(-1, 1, 64)
+        n = len(x)
+        tables = np.arange(n, dtype=np.int32)[:, None]
+        scale = torch.tensor([unit], device=dev)
+        cache = torch.zeros(2, n, 1, 1, 64, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+        w4.kv_append_rope(None, x.to(dev), x.to(dev), *cache, ints(tables, dev), ints([1] * n, dev), torch.from_numpy(freqs_of(64)).to(dev),
+                          interleaved=interleaved, k_scale=scale, v_scale=scale)
+        want = A.e4m3_value(as_f64(x) / unit)
+        for got in cache:
+            assert np.array_equal(as_f64(got)[:, 0], want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rows_of_zeros_inf_and_nan(kind, interleaved):
+    """A pair with NaN or Inf spoils itself (in 4 bits its block), and no other; zeros stay zeros."""
+    dev = device()
+    say(f"[append_rope] zeros, Inf and NaN, {kind}, interleaved {interleaved}")
+    page, kv, dim, n = 16, 2, 128, 20
+    f, pos = freqs_of(128), np.arange(n) + 5
+    rows = values((n, kv, dim), "bf16", torch.Generator().manual_seed(8))
+    rows[3], rows[4, 0] = 0, -0.0
+    at = [(6, 0, 5, float("nan")), (7, 1, 70, float("inf")), (8, 0, 127, -float("inf")), (9, 1, 0, float("nan"))]
+    bad = np.zeros((n, kv, dim), bool)                      # of the turned keys
+    clean = rows.clone()
+    for t, h, d, x in at:
+        rows[t, h, d] = x
+        clean[t, h, d] = 0
+        bad[t, h, [d, d ^ 1 if interleaved else d ^ 64]] = True
+    tables, lens, cu = ints([[0, 1]], dev), ints([n + 5], dev), ints([0, n], dev)
+    ours, other = ([w4.kv_cache_e2m1(3, page, kv, dim, device=dev) if kind == "fp4" else
+                    torch.zeros(3, page, kv, dim, dtype=torch.bfloat16, device=dev).to(TYPES[kind]) for _ in range(2)] for _ in range(2))
+    turn = torch.from_numpy(f).to(dev)
+    w4.kv_append_rope(None, rows.to(dev), rows.to(dev), *ours, tables, lens, turn, cu_seqlens=cu, interleaved=interleaved)
+    w4.kv_append_rope(None, clean.to(dev), clean.to(dev), *other, tables, lens, turn, cu_seqlens=cu, interleaved=interleaved)
+    k, v = (as_f64(x) for x in w4.kv_read(*ours, tables, lens, cu, n))
+    k2, v2 = (as_f64(x) for x in w4.kv_read(*other, tables, lens, cu, n))
+    off = ~np.isfinite(as_f64(rows))
+    if kind == "fp4":
+        bad, off = (np.repeat(m.reshape(n, kv, -1, 32).any(-1), 32, -1).reshape(m.shape) for m in (bad, off))
+        assert np.isnan(k[bad]).all() and np.isnan(v[off]).all()
+    assert not np.isfinite(k[bad]).any() or kind == "fp8"  # (8 bits hold Inf as their largest value)
+    assert np.isnan(k[6, 0, 5]) and np.isnan(k[9, 1, 0])
+    assert np.array_equal(k[~bad], k2[~bad]) and np.array_equal(v[~off], v2[~off])
+    assert not k[3].any() and not v[4, 0].any()
+
+
+@pytest.mark.parametrize("factor", [2.0 ** -120, 1e-30, 3e20, 2.0 ** 100])
+def test_factors_of_any_size_in_4_bits(factor):
+    dev = device()
+    say(f"[append_rope] 4 bit, factor {factor}")
+    page, kv, dim, n = 16, 1, 128, 16
+    f, pos = freqs_of(128), np.arange(n)
+    rows = values((n, kv, dim), "bf16", torch.Generator().manual_seed(9))
+    cache = w4.kv_cache_e2m1((2, 1), page, kv, dim, device=dev)
+    before = bytes_of(cache[0]).copy()
+    w4.kv_append_rope(None, rows.to(dev), rows.to(dev), *cache, ints([[0]], dev), ints([n], dev), torch.from_numpy(f).to(dev),
+                      cu_seqlens=ints([0, n], dev), factor=factor)
+    want = expected("fp4", before, R.rotate(as_f64(rows), pos, f, False, False, factor), np.array([[0]]), [n], [0, n], page, kv,
+                    dim, None, "bf16")
+    assert np.array_equal(bytes_of(cache[0]), want)
+
+
 # ------------------------------------------------------------- 4-bit storing --
 
 @pytest.mark.parametrize("high", ["bf16", "fp16"])
@@ -188,7 +306,7 @@ def test_append_4_bit_is_the_quantizers_bits(high, kv, dim, page):
         assert np.array_equal(bytes_of(got), want)
 
 
-@pytest.mark.parametrize("page", [16, 24])
+@pytest.mark.parametrize("page", [16, 24, 11])
 def test_forks_copies_and_compaction_of_4_bit_pages(page):
     """The bookkeeping moves a page's codes and scales together."""
     dev = device()
@@ -313,3 +431,37 @@ def test_append_and_read_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(a, out) and torch.equal(b, kv_out), f"replay {i}"
         (a[:, 0] @ a[:, 1].t().contiguous()).sum().item()
+
+
+def test_two_streams():
+    """Calls of two streams at once, each on its own rows and caches, give what they give alone."""
+    dev = device()
+    say("[rows] two streams")
+    page, kv, dim, group, n = 16, 4, 128, 4, 2000
+    gen = torch.Generator().manual_seed(11)
+    f = torch.from_numpy(freqs_of(dim)).to(dev)
+    tables, lens, cu = ints(np.arange(126)[None], dev), ints([n], dev), ints([0, n], dev)
+    sets = []
+    for _ in range(2):
+        rows = values((n, kv * (group + 2), dim), "bf16", gen).to(dev)
+        sets.append((rows.split([kv * group, kv, kv], dim=1), w4.kv_cache_e2m1((2, 126), page, kv, dim, device=dev)))
+
+    def call(part):
+        (q, k, v), cache = part
+        q = w4.kv_append_rope(q, k, v, *cache, tables, lens, f, cu_seqlens=cu)
+        return [q, *w4.kv_read(*cache, tables, lens, cu, n), w4.attn_prefill(q, cu, *cache, tables, lens),
+                w4.attn_decode(q[-1:], *cache, tables, lens), w4.rope(q, cu.new_zeros(n), f)]
+    alone = [[t.clone() for t in call(part)] for part in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        got = []
+        for s, part in zip(streams, sets):
+            with torch.cuda.stream(s):
+                got.append(call(part))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
