@@ -301,7 +301,10 @@ struct Parts {
 // rounding of them: in fp32 they are known to within a bound; where both ends of that
 // give the same codes these are the right ones, else (one vector in some hundred) all of
 // it is taken again in fp64.
-template <class T, int CACHE, int STYLE>
+// FLIGHT: vectors in flight per thread, 1 where none has more than one of a kind: the code
+// that the unrolled steps would skip has to be read too (1795 tokens of 16 / 16 heads of 64
+// into E4M3 11.8 us, 12.7 with 4; into FP16 8.1 and 9.4).
+template <class T, int CACHE, int STYLE, int FLIGHT>
 __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int lane_bits, FastDiv by_pairs) {
   constexpr bool SMALL = CACHE == W4A4_E4M3 || CACHE == W4A4_E2M1;
   __shared__ float2 tab[STYLE ? kTable : 1];
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
     const uint16_t* p;
     int64_t step;
     int h, heads;
-    at_u32x4 own[kFlight], other[kFlight];
+    at_u32x4 own[FLIGHT], other[FLIGHT];
   };
   const int partner = d < pairs ? d + pairs : d - pairs;
   auto rows_of = [&](const void* base, int64_t row, int64_t head, int h, int heads) {
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
   };
   auto load = [&](Rows& r, bool turns) {
 #pragma unroll
-    for (int j = 0; j < kFlight; ++j)
+    for (int j = 0; j < FLIGHT; ++j)
       if (here && r.h + j * phases < r.heads) {
         const uint16_t* p = r.p + j * r.step;
         r.own[j] = *reinterpret_cast<const at_u32x4*>(p + d);
@@ -346,8 +349,8 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
       }
   };
   auto advance = [&](Rows& r) {
-    r.p += kFlight * r.step;
-    r.h += kFlight * phases;
+    r.p += FLIGHT * r.step;
+    r.h += FLIGHT * phases;
   };
   Rows rows = kinds & kQueries ? rows_of(a.q, a.q_row, a.q_head, first, a.q_heads)
               : kinds & kKeys  ? rows_of(a.k, a.k_row, a.k_head, first, a.kv.heads)
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
     const int64_t out_step = phases * a.o_head;
     while (rows.h < rows.heads) {
 #pragma unroll
-      for (int j = 0; j < kFlight; ++j)
+      for (int j = 0; j < FLIGHT; ++j)
         if (rows.h + j * phases < rows.heads) {
           float y[8];
           if constexpr (STYLE != kNone) turn8<T, STYLE>(rows.own[j], rows.other[j], rows.p + j * rows.step, d, pairs, turns, y);
@@ -397,7 +400,7 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
           if (STYLE == kHalfAny) __builtin_amdgcn_wave_barrier();
           *reinterpret_cast<at_u32x4*>(out + j * out_step) = pack8<T>(y);
         }
-      out += kFlight * out_step;
+      out += FLIGHT * out_step;
       advance(rows);
       if (rows.h < rows.heads) load(rows, true);
     }
@@ -521,11 +524,11 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
     while (r.h < r.heads) {
       uint32_t doubt = 0;
 #pragma unroll
-      for (int j = 0; j < kFlight; ++j)
+      for (int j = 0; j < FLIGHT; ++j)
         if (r.h + j * phases < r.heads && take(r.h + j * phases, r.own[j], r.other[j], r.p + j * r.step)) doubt |= 1u << j;
       if constexpr (SMALL) {
 #pragma unroll 1
-        for (int j = 0; j < kFlight; ++j)
+        for (int j = 0; j < FLIGHT; ++j)
           if (doubt >> j & 1) again(r.h + j * phases, r.p + j * r.step);
       }
       advance(r);
@@ -642,12 +645,16 @@ Shape shape_of(int64_t tokens, int64_t vectors, int dim) {
 // computes their angles once for all kinds: 14449 tokens, 28 / 4 heads of 128 into 4 bits,
 // 51 us in one part, 63 in three), else a part for each kind, so that the kinds' chains
 // of loads run side by side (one token each of 48 sequences 4.4 us, 5.5 in one part).
-constexpr int kOnePart = 1024;
-Parts parts_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int dim, int64_t* grid, int* lane_bits) {
+constexpr int kOnePart = 512;
+// *most: vectors of a kind that a thread has at most.
+Parts parts_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int dim, int64_t* grid, int* lane_bits, int64_t* most) {
   Parts p = {};
   *grid = 0;
+  *most = 1;
   auto add = [&](int kinds, int64_t heads) {
     const Shape s = shape_of(tokens, heads, dim);
+    const int64_t phases = (256 >> s.lane_bits >> s.tok_bits) * s.y;
+    *most = std::max(*most, (std::max(kinds & kQueries ? q_heads : 0, kinds == kQueries ? 0 : kv_heads) + phases - 1) / phases);
     p.kinds[p.count] = kinds;
     p.begin[p.count] = int(*grid);
     p.tok_bits[p.count] = s.tok_bits;
@@ -670,26 +677,28 @@ Parts parts_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int dim, int64
 
 template <class T, int CACHE>
 hipError_t launch_in(const RowsIn& a, hipStream_t stream) {
-  int64_t grid;
+  int64_t grid, most;
   int lane_bits;
-  const Parts parts = parts_of(a.tokens, a.q_heads, a.kv.heads, a.dim, &grid, &lane_bits);
+  const Parts parts = parts_of(a.tokens, a.q_heads, a.kv.heads, a.dim, &grid, &lane_bits, &most);
   const FastDiv by_pairs = fast_div(uint32_t(std::max(a.rot / 2, 1)));
-  auto go = [&](auto kernel) {
+  auto go = [&](auto style) {
+    constexpr int S = decltype(style)::value;
+    const auto kernel = most == 1 ? rows_in_kernel<T, CACHE, S, 1> : rows_in_kernel<T, CACHE, S, kFlight>;
     kernel<<<unsigned(grid), 256, 0, stream>>>(a, parts, lane_bits, by_pairs);
     return hipGetLastError();
   };
   if constexpr (CACHE == W4A4_E2M1)
-    if (a.rot == 0) return go(rows_in_kernel<T, CACHE, kNone>);
-  if (a.interleaved) return go(rows_in_kernel<T, CACHE, kPairs>);
-  return a.rot % 16 == 0 ? go(rows_in_kernel<T, CACHE, kHalf>) : go(rows_in_kernel<T, CACHE, kHalfAny>);
+    if (a.rot == 0) return go(std::integral_constant<int, kNone>());
+  if (a.interleaved) return go(std::integral_constant<int, kPairs>());
+  return a.rot % 16 == 0 ? go(std::integral_constant<int, kHalf>()) : go(std::integral_constant<int, kHalfAny>());
 }
 
 }  // namespace
 
 int64_t rows_workgroups(int64_t tokens, int64_t q_heads, int64_t kv_heads, int dim) {
-  int64_t grid;
+  int64_t grid, most;
   int lane_bits;
-  parts_of(tokens, q_heads, kv_heads, dim, &grid, &lane_bits);
+  parts_of(tokens, q_heads, kv_heads, dim, &grid, &lane_bits, &most);
   return grid;
 }
 
