@@ -432,8 +432,12 @@ typedef enum { W4A4_BF16 = 0, W4A4_F16 = 1, W4A4_E4M3 = 2, W4A4_E2M1 = 4 } w4a4_
  * the rule of w4a4_quantize_act's MXFP4 (block exponent floor(log2 amax) - 2, codes
  * to nearest even, saturating at 6; a block with Inf or NaN gets byte 255 and zero
  * codes), from FP16 rows with exponents up to 13 (byte 140), so that what is stored
- * stays within FP16.  Attention in FP16, and reading out in it, take scales up to
- * that; larger ones give Inf or NaN.
+ * stays within FP16.  Scales beyond 2^125 (byte 252), and beyond 2^13 where rows are read out in
+ * FP16 or w4a4_attn_prefill takes them with FP16 queries, may give Inf or NaN.
+ *
+ * Attention takes the keys' codes as they are, and the queries in blocks of 32 as sums of
+ * four 6-bit numbers: within 2^-19 of the block's largest value, which is exact for BF16 values
+ * down to 2^-10 of that and for FP16 values down to 2^-7.
  */
 
 typedef struct {
@@ -493,9 +497,10 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs,
  * with -t for t if `inverse` (with the same factor the gradient of the rotation).
  * The other values stay as they are.  freqs holds what the kind of positions asks
  * for: base^(-2i / rot_dim), compressed or stretched by parts for long contexts.
- * Angles are taken from the exact p * freqs[i] in 64 bits, cos and sin to 2^-48; the
- * products are fp32 where the result is a 16-bit value (rounded once), fp64 where it
- * is rounded to 8 or 4 bits.
+ * Angles are taken from p * freqs[i] in 64 bits (right to 2^-48 of a turn at position 131071,
+ * to 1e-6 of one at 2^31 - 1).  16-bit results are within 3.5 * 2^-24 (|a| + |b|) * factor
+ * before their one rounding: fp32 cos and sin and products.  Results of 8 or 4 bits are the
+ * roundings of the 64-bit values.
  */
 typedef struct {
   const float* freqs;      /* device, fp32 [rot_dim / 2], 4-byte aligned         */
@@ -582,7 +587,8 @@ w4a4_status w4a4_kv_read(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, c
  * Scores, softmax statistics and sums are fp32, and the sums of weighted values
  * are divided last: |V| times the visible tokens must stay below 2^119, or they
  * may overflow to Inf.  The work is split evenly over the card by the sequences'
- * visible lengths, read on the device; results do not depend on timing.
+ * visible lengths, read on the device; results do not depend on timing.  (Over an E2M1 cache
+ * whose tables hold few tokens it is not split, so the last bits depend on the tables' width.)
  */
 size_t w4a4_attn_decode_workspace_bytes(const w4a4_kv_cache* cache, int64_t seqs, int q_heads);
 w4a4_status w4a4_attn_decode(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs, w4a4_dtype dtype, int q_heads,
@@ -601,8 +607,9 @@ w4a4_status w4a4_attn_decode(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seq
  * card and the tables can hold long sequences (max_pages * page_size > 1000), the
  * keys are split as well.  The softmax weights are rounded to `dtype` for the matrix
  * cores, in two parts (about 16 bits) where the keys are split or a kv head has up
- * to 16 rows per sequence on average, else in one: so the last bits of a sequence's
- * outputs depend on the tables' width and on what else is in the call.
+ * to 16 rows per sequence on average (48 over an E2M1 cache with head_dim 64 or 128), else in
+ * one: so the last bits of a sequence's outputs depend on the tables' width and on what else
+ * is in the call.
  * Statistics and sums are fp32.
  */
 size_t w4a4_attn_prefill_workspace_bytes(const w4a4_kv_cache* cache, int64_t seqs, int64_t tokens, int q_heads);

@@ -17,6 +17,13 @@
 // of tokens interleaved.  Weights and values are BF16 whatever the queries' type is,
 // the weights in two parts (16 bits together): the widened values are exact, and of the
 // range that the cache's scales have.
+//
+// Measured, whole calls, D = 128: 48 sequences of 37 to 8191 tokens, 8 kv heads of 4, 216 MB
+// 52 us (kernel 47.5, 4.5 TB/s; its loads alone take 43; the vector unit is busy 46%, the
+// matrix cores 16% of the time); 3 of 90001 to 131071, 4 heads of 7, 180 MB 44.7 us (kernel
+// 40, loads alone 36); 5 and 9 tokens on 30000 and 33333, 8 heads of 4, 69 MB 39 us (kernel 37:
+// the chain of scores, softmax and sums with two waves per SIMD).  A second tile in
+// registers does not pay where it fits either (4 tokens on 33000 25.5 us, 28.1 with it).
 #include <algorithm>
 
 #include "attn_fp4.h"

@@ -31,12 +31,15 @@
 // FP4 (4-bit caches): keys lie in LDS as the cache has them, codes and scale bytes, and the
 // scores come from the scaled 32 x 32 x 64 MFMA, the queries in four FP6 parts (attn_fp4.h);
 // values are widened on their way to LDS, as from E4M3.
+// (Ragged chunks over 28 / 4 heads 506 us, 560 with the keys widened to 16 bits too; three
+// parts of the queries, right to 2^-14 of a block's largest value, miss the bound on lse.)
 //
 // Measured, 32 / 8 heads, D = 128, causal 8192 bf16: 512 to 528 us, 1.05 PFLOP/s (a
 // library product of 8192^3 reaches 1.44 here; the MFMAs are busy 55% of the
 // time on the ragged chunks, at 1.65 GHz), E4M3 537 to 557 us, D = 64 320 to 337;
 // 4096 at D = 256 332 to 346 us.  Ragged chunks over 28 / 4 heads, 526 GFLOP:
-// 491 to 514 us.  82 tokens: 10.5 us, 8.7 of them the kernel's.
+// 491 to 514 us.  82 tokens: 10.5 us, 8.7 of them the kernel's.  FP4: causal 8192 514 us, D = 64
+// 320, 4096 at D = 256 176 over 16 / 4 heads; ragged chunks 506 to 528.
 #include <algorithm>
 #include <type_traits>
 #include <utility>

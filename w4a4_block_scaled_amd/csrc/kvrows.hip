@@ -5,8 +5,8 @@
 // All of it moves bytes.  Measured: queries of 8191 tokens, 134 MB, 22.2 us (they fit the
 // last cache in part); keys, values and queries of 14449 tokens into 4 bits, 245 MB, 51 us, 4.8
 // TB/s (a copy of the queries alone by torch 36, by this kernel 34); out of 4 bits 162 MB in
-// 28 us.  Small calls are their launch and the chain of lookups behind it: 3.5 us for 16
-// tokens, 4.4 with a cache.  In between the vector unit counts, some 350 instructions per
+// 28 us.  Small calls are their launch and the chain of lookups behind it: 3.2 us for 16
+// tokens, 4.2 with a cache.  In between the vector unit counts, some 350 instructions per
 // row of keys and wave: 1795 tokens of 16 / 16 heads of 64 into E4M3, 18 MB, 11.7 us.
 #include <algorithm>
 #include <type_traits>
@@ -35,8 +35,9 @@ __device__ __forceinline__ Angle angle_of(int pos, float freq) {
 // cos and sin by the Taylor series around the quarter turn, times factor: in fp64 right
 // to 2^-50, in fp32 to 1.5 * 2^-24.
 static __device__ const double kSeries[14] = {
-    -1.0 / 1307674368000.0, 1.0 / 6227020800.0, -1.0 / 39916800.0, 1.0 / 362880.0, -1.0 / 5040.0, 1.0 / 120.0, -1.0 / 6.0,
-    -1.0 / 87178291200.0, 1.0 / 479001600.0, -1.0 / 3628800.0, 1.0 / 40320.0, -1.0 / 720.0, 1.0 / 24.0, -0.5};
+    -1.0 / 1307674368000.0, 1.0 / 6227020800.0, -1.0 / 39916800.0, 1.0 / 362880.0, -1.0 / 5040.0, 1.0 / 120.0,
+    -1.0 / 6.0, -1.0 / 87178291200.0, 1.0 / 479001600.0, -1.0 / 3628800.0, 1.0 / 40320.0, -1.0 / 720.0, 1.0 / 24.0,
+    -0.5};
 template <typename R>
 struct Turn {
   R cos, sin;
@@ -310,7 +311,8 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
   __shared__ float2 tab[STYLE ? kTable : 1];
   const int block = blockIdx.x;
   int part = 0;
-  if (CACHE != kAlone && parts.count > 1) part = block < parts.begin[1] ? 0 : parts.count == 2 || block < parts.begin[2] ? 1 : 2;
+  if (CACHE != kAlone && parts.count > 1)
+    part = block < parts.begin[1] ? 0 : parts.count == 2 || block < parts.begin[2] ? 1 : 2;
   const int kinds = CACHE == kAlone ? kQueries : parts.kinds[part];
   const int tok_bits = parts.tok_bits[part], splits = parts.splits[part];
   const int at_block = block - parts.begin[part], bx = at_block / splits, by = at_block - bx * splits;
@@ -363,7 +365,8 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
   Place mine = {active, 0, -1, 0};
   int turn = 0;
   float freq0 = 0.0f;         // of the thread's first angle
-  if (STYLE != kNone && int(threadIdx.x) < pairs << tok_bits) freq0 = a.freqs[int(threadIdx.x) - by_pairs.div(threadIdx.x) * pairs];
+  if (STYLE != kNone && int(threadIdx.x) < pairs << tok_bits)
+    freq0 = a.freqs[int(threadIdx.x) - by_pairs.div(threadIdx.x) * pairs];
   if (a.positions && active) turn = a.positions[row0 + lane];
   if constexpr (CACHE != kAlone) {
     mine = place_of(a.kv, a.cu, int(row0) + lane, active);
@@ -395,7 +398,8 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
       for (int j = 0; j < FLIGHT; ++j)
         if (rows.h + j * phases < rows.heads) {
           float y[8];
-          if constexpr (STYLE != kNone) turn8<T, STYLE>(rows.own[j], rows.other[j], rows.p + j * rows.step, d, pairs, turns, y);
+          if constexpr (STYLE != kNone)
+            turn8<T, STYLE>(rows.own[j], rows.other[j], rows.p + j * rows.step, d, pairs, turns, y);
           // out may be q itself: every lane of the row has read its partners
           if (STYLE == kHalfAny) __builtin_amdgcn_wave_barrier();
           *reinterpret_cast<at_u32x4*>(out + j * out_step) = pack8<T>(y);
@@ -466,7 +470,8 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
           if constexpr (STYLE == kHalfAny) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (turns.turned >> e & 1) top = max(top, uint32_t(row[d + e < pairs ? d + e + pairs : d + e - pairs] & 0x7fff));
+              if (turns.turned >> e & 1)
+                top = max(top, uint32_t(row[d + e < pairs ? d + e + pairs : d + e - pairs] & 0x7fff));
           }
           float off = T::low(top) * a.factor * 0x1p-20f;
           if (!turns.turned) off = 0.0f;
@@ -525,7 +530,8 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
       uint32_t doubt = 0;
 #pragma unroll
       for (int j = 0; j < FLIGHT; ++j)
-        if (r.h + j * phases < r.heads && take(r.h + j * phases, r.own[j], r.other[j], r.p + j * r.step)) doubt |= 1u << j;
+        if (r.h + j * phases < r.heads && take(r.h + j * phases, r.own[j], r.other[j], r.p + j * r.step))
+          doubt |= 1u << j;
       if constexpr (SMALL) {
 #pragma unroll 1
         for (int j = 0; j < FLIGHT; ++j)
@@ -643,18 +649,21 @@ Shape shape_of(int64_t tokens, int64_t vectors, int dim) {
 }
 // One part where its workgroups are enough for the card (each looks up its tokens and
 // computes their angles once for all kinds: 14449 tokens, 28 / 4 heads of 128 into 4 bits,
-// 51 us in one part, 63 in three; 1795 of 16 / 16 of 64 into FP16 9.4 and 11.4), else a part for each kind, so that the kinds' chains
-// of loads run side by side (one token each of 48 sequences 4.4 us, 5.5 in one part).
+// 51 us in one part, 63 in three; 1795 of 16 / 16 of 64 into FP16 9.4 and 11.4), else a part
+// for each kind, so that the kinds' chains of loads run side by side (one token each of 48
+// sequences 4.4 us, 5.5 in one part).
 constexpr int kOnePart = 512;
 // *most: vectors of a kind that a thread has at most.
-Parts parts_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int dim, int64_t* grid, int* lane_bits, int64_t* most) {
+Parts parts_of(int64_t tokens, int64_t q_heads, int64_t kv_heads, int dim, int64_t* grid, int* lane_bits,
+               int64_t* most) {
   Parts p = {};
   *grid = 0;
   *most = 1;
   auto add = [&](int kinds, int64_t heads) {
     const Shape s = shape_of(tokens, heads, dim);
     const int64_t phases = (256 >> s.lane_bits >> s.tok_bits) * s.y;
-    *most = std::max(*most, (std::max(kinds & kQueries ? q_heads : 0, kinds == kQueries ? 0 : kv_heads) + phases - 1) / phases);
+    const int64_t rows = std::max(kinds & kQueries ? q_heads : 0, kinds == kQueries ? 0 : kv_heads);
+    *most = std::max(*most, (rows + phases - 1) / phases);
     p.kinds[p.count] = kinds;
     p.begin[p.count] = int(*grid);
     p.tok_bits[p.count] = s.tok_bits;
