@@ -195,3 +195,29 @@ def test_binding_refuses_what_a_c_type_does_not_hold():
     wide = ints(0)[:, None].expand(BIG, 1)
     with pytest.raises(w4.W4A4Error, match="does not fit"):
         w4.kv_append(t["k"], t["v"], t["k_cache"], t["v_cache"], wide, None)
+
+
+def test_calls_go_to_the_device_of_their_tensors(monkeypatch):
+    """With another device current, that of the tensors is made so for the call, and the old one comes back."""
+    state, seen = {"device": 0}, []
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.before, state["device"] = state["device"], self.device
+
+        def __exit__(self, *_):
+            state["device"] = self.before
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state["device"], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1000 + d, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    for device in (0, 1):
+        w4._kv_call(device, lambda *a: seen.append((state["device"], *a)) or 0, "x")
+    assert seen == [(0, "x", 1000), (1, "x", 1001)] and state["device"] == 0
+    with pytest.raises(w4.W4A4Error) as e:
+        w4._kv_call(1, lambda *a: 3)
+    assert e.value.status == 3 and state["device"] == 0
+    with pytest.raises(w4.W4A4Error, match="GPU"):
+        w4._kv_call(-1, lambda *a: 0)

@@ -453,7 +453,7 @@ _I32 = torch.int32
 
 
 # `device` of the helpers below: a GPU's index, -1 for tensors elsewhere (get_device(), cheaper than
-# comparing torch.device objects; _kv_stream refuses -1 before any call).
+# comparing torch.device objects; _on_gpu refuses -1 before any call).
 
 def _on(device: int) -> str:
     return "the cache's device" if device < 0 else f"cuda:{device}"
@@ -534,11 +534,21 @@ def _kv_rows(what: str, x: torch.Tensor, rows: int, heads, dim: int, device: int
     return x.data_ptr(), stride[0], stride[1]
 
 
-def _kv_stream(device: int) -> int:
-    """Handle of the current stream of GPU `device` (_stream without the torch.cuda.Stream object)."""
+def _on_gpu(device: int) -> None:
     if device < 0:
         raise W4A4Error(2, "the cache and everything with it must be on a GPU")
-    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _kv_call(device: int, entry, *args) -> None:
+    """entry(*args, the current stream of GPU `device`), with that as the current device: launches go there."""
+    _on_gpu(device)
+    if torch._C._cuda_getDevice() != device:
+        with torch.cuda.device(device):
+            status = entry(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        status = entry(*args, torch._C._cuda_getCurrentRawStream(device))
+    if status:
+        _check(status)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -568,7 +578,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     if k.dtype != v.dtype:
         raise W4A4Error(4, f"kv_append: k is {k.dtype}, v is {v.dtype}")
     cu = None if cu_seqlens is None else _cu("kv_append", cu_seqlens, seqs, dev)
-    _check(_kv_lib().w4a4_kv_append(c, s, cu, tokens, _kv_type(k, "kv_append"), *rows, _kv_stream(dev)))
+    _kv_call(dev, _kv_lib().w4a4_kv_append, c, s, cu, tokens, _kv_type(k, "kv_append"), *rows)
 
 
 def kv_cache_e2m1(pages, page_size: int, heads: int, head_dim: int, device="cuda") -> torch.Tensor:
@@ -668,7 +678,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, inter
     at = _positions("rope", positions, tokens, dev)
     out = _like_rows("rope: out", out, x)
     rows = (*_kv_rows("rope: x", x, tokens, None, dim, dev), *_kv_rows("rope: out", out, tokens, heads, dim, dev))
-    _check(_kv_lib().w4a4_rope(r, tokens, at, _kv_type(x, "rope"), heads, dim, *rows, _kv_stream(dev)))
+    _kv_call(dev, _kv_lib().w4a4_rope, r, tokens, at, _kv_type(x, "rope"), heads, dim, *rows)
     return out
 
 
@@ -699,7 +709,7 @@ def kv_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, 
         q_rows = (*q_at, *_kv_rows(name + ": q_out", out, tokens, heads, dim, dev))
     elif q_out is not None:
         raise W4A4Error(2, f"{name}: q_out without q")
-    _check(_kv_lib().w4a4_kv_append_rope(c, s, cu, tokens, _kv_type(k, name), r, at, heads, *q_rows, *rows, _kv_stream(dev)))
+    _kv_call(dev, _kv_lib().w4a4_kv_append_rope, c, s, cu, tokens, _kv_type(k, name), r, at, heads, *q_rows, *rows)
     return out
 
 
@@ -721,7 +731,7 @@ def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, tables: torch.Tensor, 
     if k.dtype != dtype or v.dtype != dtype:
         raise W4A4Error(4, f"{name}: out is {k.dtype} and {v.dtype}, not {dtype}")
     rows = (*_kv_rows("kv_read: k", k, tokens, heads, dim, dev), *_kv_rows("kv_read: v", v, tokens, heads, dim, dev))
-    _check(_kv_lib().w4a4_kv_read(c, s, cu, tokens, _kv_type(k, name), *rows, _kv_stream(dev)))
+    _kv_call(dev, _kv_lib().w4a4_kv_read, c, s, cu, tokens, _kv_type(k, name), *rows)
     return k, v
 
 
@@ -759,10 +769,11 @@ def _attn(name: str, q, cu, k_cache, v_cache, tables, lens, k_scale, v_scale, sc
             raise W4A4Error(2, f"{name}: the workspace must be contiguous, on {_on(dev)}")
         size = workspace.numel() * workspace.element_size()
     tail = (_kv_type(q, name), q_heads, *q_at, dim ** -0.5 if scale is None else scale, window, sinks, *out_at,
-            None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), size,
-            _kv_stream(dev))
-    L = _kv_lib()
-    _check(L.w4a4_attn_decode(c, s, *tail) if cu is None else L.w4a4_attn_prefill(c, s, cu.data_ptr(), rows, *tail))
+            None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), size)
+    if cu is None:
+        _kv_call(dev, _kv_lib().w4a4_attn_decode, c, s, *tail)
+    else:
+        _kv_call(dev, _kv_lib().w4a4_attn_prefill, c, s, cu.data_ptr(), rows, *tail)
     return (out, lse) if return_lse else out
 
 
@@ -831,6 +842,7 @@ def _kv_workspace_bytes(rows: int, pages: int) -> int:
 
 
 def _kv_workspace(rows: int, pages: int, device: int) -> torch.Tensor:
+    _on_gpu(device)
     return torch.empty(_kv_workspace_bytes(rows, pages), dtype=torch.uint8, device=device)
 
 
@@ -845,7 +857,7 @@ def kv_copy_pages(caches, src: torch.Tensor, dst: torch.Tensor) -> None:
     n, arrays, stride, size, pages, _, dev = _kv_arrays("kv_copy_pages", caches)
     _int32("kv_copy_pages", dev, src, dst)
     pairs = _same_length("kv_copy_pages", src, dst)
-    _check(lib().w4a4_kv_copy_pages(n, arrays, stride, size, pages, src.data_ptr(), dst.data_ptr(), pairs, _kv_stream(dev)))
+    _kv_call(dev, lib().w4a4_kv_copy_pages, n, arrays, stride, size, pages, src.data_ptr(), dst.data_ptr(), pairs)
 
 
 def kv_reserve(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int, *,
@@ -856,10 +868,9 @@ def kv_reserve(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, pag
     dev = refs.get_device()
     s, seqs = _kv_seqs("kv_reserve", tables, lens, dev)
     _int32("kv_reserve", dev, refs, lacking)
-    stream, ws = _kv_stream(dev), _kv_workspace(seqs, refs.numel(), dev)
-    _check(_kv_lib().w4a4_kv_reserve(s, page_size, refs.data_ptr(), refs.numel(),
-                                 None if lacking is None else lacking.data_ptr(), ws.data_ptr(), ws.numel(),
-                                 stream))
+    ws = _kv_workspace(seqs, refs.numel(), dev)
+    _kv_call(dev, _kv_lib().w4a4_kv_reserve, s, page_size, refs.data_ptr(), refs.numel(),
+             None if lacking is None else lacking.data_ptr(), ws.data_ptr(), ws.numel())
 
 
 def _check_pages(what: str, refs: torch.Tensor, pages: int) -> None:
@@ -876,18 +887,17 @@ def kv_fork(caches, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor
     _int32("kv_fork", dev, refs, parents, children, lacking)
     _check_pages("kv_fork", refs, pages)
     count = _same_length("kv_fork", parents, children)
-    stream, ws = _kv_stream(dev), _kv_workspace(count, pages, dev)
-    _check(_kv_lib().w4a4_kv_fork(n, arrays, stride, size, s, page, refs.data_ptr(), pages, parents.data_ptr(),
-                              children.data_ptr(), count, None if lacking is None else lacking.data_ptr(),
-                              ws.data_ptr(), ws.numel(), stream))
+    ws = _kv_workspace(count, pages, dev)
+    _kv_call(dev, _kv_lib().w4a4_kv_fork, n, arrays, stride, size, s, page, refs.data_ptr(), pages, parents.data_ptr(),
+             children.data_ptr(), count, None if lacking is None else lacking.data_ptr(), ws.data_ptr(), ws.numel())
 
 
 def kv_free(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, seqs: Optional[torch.Tensor] = None) -> None:
     """w4a4_kv_free: let go of all pages of the sequences `seqs` (int32; None: all)."""
     s, all_seqs = _kv_seqs("kv_free", tables, lens, refs.get_device())
     _int32("kv_free", refs.get_device(), refs, seqs)
-    _check(_kv_lib().w4a4_kv_free(s, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
-                              all_seqs if seqs is None else seqs.numel(), _kv_stream(refs.get_device())))
+    _kv_call(refs.get_device(), _kv_lib().w4a4_kv_free, s, refs.data_ptr(), refs.numel(),
+             None if seqs is None else seqs.data_ptr(), all_seqs if seqs is None else seqs.numel())
 
 
 def kv_trim(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int, window: int, sinks: int = 0,
@@ -897,8 +907,8 @@ def kv_trim(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_s
     _c_ints("kv_trim", page_size, window, sinks)
     s, all_seqs = _kv_seqs("kv_trim", tables, lens, refs.get_device())
     _int32("kv_trim", refs.get_device(), refs, seqs)
-    _check(_kv_lib().w4a4_kv_trim(s, page_size, refs.data_ptr(), refs.numel(), None if seqs is None else seqs.data_ptr(),
-                              all_seqs if seqs is None else seqs.numel(), window, sinks, _kv_stream(refs.get_device())))
+    _kv_call(refs.get_device(), _kv_lib().w4a4_kv_trim, s, page_size, refs.data_ptr(), refs.numel(),
+             None if seqs is None else seqs.data_ptr(), all_seqs if seqs is None else seqs.numel(), window, sinks)
 
 
 def kv_compact(caches, tables: torch.Tensor, refs: torch.Tensor) -> torch.Tensor:
@@ -908,9 +918,9 @@ def kv_compact(caches, tables: torch.Tensor, refs: torch.Tensor) -> torch.Tensor
     s, _ = _kv_seqs("kv_compact", tables, None, dev)
     _int32("kv_compact", dev, refs)
     _check_pages("kv_compact", refs, pages)
-    stream = _kv_stream(dev)
+    _on_gpu(dev)
     remap = torch.empty(pages, dtype=torch.int32, device=dev)
     ws = _kv_workspace(0, pages, dev)
-    _check(_kv_lib().w4a4_kv_compact(n, arrays, stride, size, s, refs.data_ptr(), pages, remap.data_ptr(), ws.data_ptr(),
-                                 ws.numel(), stream))
+    _kv_call(dev, _kv_lib().w4a4_kv_compact, n, arrays, stride, size, s, refs.data_ptr(), pages, remap.data_ptr(),
+             ws.data_ptr(), ws.numel())
     return remap
