@@ -74,7 +74,8 @@ constexpr int kAheadOct = 16, kAheadAny = 2;             // tiles that one load 
 // Microseconds with 4 / 3 / 2 / 1: D = 64 (32 sequences of 100 to 6000 tokens) 37.7 / 40.5 /
 // 53.0 / 83.4; D = 128, the ragged batch 62.5 (spills) / 52.3 / 56.0 / 75.3, pages of 11
 // 152 / 70 (spills) / 39.2 / 54.4, 2 tokens of each of 8 sequences on 8000 37.6 / 25.5 / 23.5
-// / 23.6; D = 256 - / 55.5 / 44.4 / 42.1 (the LDS has room for two).
+// / 23.6; D = 256 (32 sequences of 100 to 6000) - / 55.5 (spills) / 40.8 / 40.2, 64 of 128 to 1025
+// 16.8 / 18.9 with two and one (the LDS has room for two).
 constexpr int wgs_per_cu(int D, bool oct, bool few, int nb) {
   if (D == 256 || nb > 1 || !oct) return 2;
   return D == 64 ? 4 : few ? 2 : 3;
@@ -145,55 +146,6 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(A
     const int pos_max = past + (FEW ? work.group.div(unit_row + rows - 1) : 0);
     const float cs = a.scale_log2;
     const int32_t* table = a.kv.tables + seq * a.kv.table_stride;
-
-    // this lane's rows, one of each block: positions and query operands (a row past the
-    // unit's last one is that one again, and is not written)
-    int pos[NB];
-    at_u32x6 q[kLdsQ ? 1 : kOps];
-    uint32_t qscale[kLdsQ ? 1 : kSteps];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const int row = unit_row + min(kRows * n + c, rows - 1);
-      const int tok = FEW ? work.group.div(row) : 0;
-      pos[n] = past + tok;
-      const int at = FEW ? min(max(qs.first + tok, 0), work.tokens - 1) : seq;
-      const uint16_t* qp = static_cast<const uint16_t*>(a.q) + at * a.q_row +
-                           (int64_t(head) * a.group + row - tok * a.group) * a.q_head;
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        if (kLdsQ && (n * kSteps + i) % 4 != wave) continue;       // the waves share them
-        at_u32x6 part[kParts];
-        uint32_t bytes = split_query<T, kParts>(qp + (D == 64 ? 32 * (g & 1) : 128 * i + 32 * g), part);
-        if constexpr (D == 64) {        // quarters 0, 1: parts 0 and 2; quarters 2, 3: parts 1 and 3
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int w = 0; w < 6; ++w) part[k][w] = g < 2 ? part[2 * k][w] : part[2 * k + 1][w];
-          bytes = g < 2 ? bytes : bytes >> 8;       // bytes 0 and 2
-        }
-        constexpr int kOf = kOps / kSteps;
-#pragma unroll
-        for (int p = 0; p < kOf; ++p) {
-          if constexpr (kLdsQ) {
-            const int k = n * kOps + i * kOf + p;
-            lds_q4[k][lane] = (at_u32x4){part[p][0], part[p][1], part[p][2], part[p][3]};
-            lds_q2[k][lane] = (at_u32x2){part[p][4], part[p][5]};
-          } else {
-            q[i * kOf + p] = part[p];
-          }
-        }
-        if constexpr (kLdsQ) lds_qs[n * kSteps + i][lane] = bytes;
-        else qscale[i] = bytes;
-      }
-    }
-    if constexpr (kLdsQ) __syncthreads();
-    auto operand = [&](int n, int k) {
-      if constexpr (!kLdsQ) return q[k];
-      const at_u32x4 u = lds_q4[n * kOps + k][lane];
-      const at_u32x2 v = lds_q2[n * kOps + k][lane];
-      return (at_u32x6){u.x, u.y, u.z, u.w, v.x, v.y};
-    };
-    auto operand_scale = [&](int n, int i) { return kLdsQ ? lds_qs[n * kSteps + i][lane] : qscale[kLdsQ ? 0 : i]; };
 
     // what a lane reads lies at these, plus its tokens' places in their pages
     const uint8_t* const kcode = static_cast<const uint8_t*>(a.kv.k) + head * a.kv.head_stride +
@@ -295,6 +247,70 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(A
         }
       }
     };
+
+    // this lane's rows, one of each block: positions and query operands (a row past the
+    // unit's last one is that one again, and is not written)
+    int pos[NB];
+    at_u32x6 q[kLdsQ ? 1 : kOps];
+    uint32_t qscale[kLdsQ ? 1 : kSteps];
+    auto split_queries = [&] {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const int row = unit_row + min(kRows * n + c, rows - 1);
+        const int tok = FEW ? work.group.div(row) : 0;
+        pos[n] = past + tok;
+        const int at = FEW ? min(max(qs.first + tok, 0), work.tokens - 1) : seq;
+        const uint16_t* qp = static_cast<const uint16_t*>(a.q) + at * a.q_row +
+                             (int64_t(head) * a.group + row - tok * a.group) * a.q_head;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          if (kLdsQ && (n * kSteps + i) % 4 != wave) continue;       // the waves share them
+          at_u32x6 part[kParts];
+          uint32_t bytes = split_query<T, kParts>(qp + (D == 64 ? 32 * (g & 1) : 128 * i + 32 * g), part);
+          if constexpr (D == 64) {        // quarters 0, 1: parts 0 and 2; quarters 2, 3: parts 1 and 3
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int w = 0; w < 6; ++w) part[k][w] = g < 2 ? part[2 * k][w] : part[2 * k + 1][w];
+            bytes = g < 2 ? bytes : bytes >> 8;       // bytes 0 and 2
+          }
+          constexpr int kOf = kOps / kSteps;
+#pragma unroll
+          for (int p = 0; p < kOf; ++p) {
+            if constexpr (kLdsQ) {
+              const int k = n * kOps + i * kOf + p;
+              lds_q4[k][lane] = (at_u32x4){part[p][0], part[p][1], part[p][2], part[p][3]};
+              lds_q2[k][lane] = (at_u32x2){part[p][4], part[p][5]};
+            } else {
+              q[i * kOf + p] = part[p];
+            }
+          }
+          if constexpr (kLdsQ) lds_qs[n * kSteps + i][lane] = bytes;
+          else qscale[i] = bytes;
+        }
+      }
+      if constexpr (kLdsQ) __syncthreads();
+    };
+    auto operand = [&](int n, int k) {
+      if constexpr (!kLdsQ) return q[k];
+      const at_u32x4 u = lds_q4[n * kOps + k][lane];
+      const at_u32x2 v = lds_q2[n * kOps + k][lane];
+      return (at_u32x6){u.x, u.y, u.z, u.w, v.x, v.y};
+    };
+    auto operand_scale = [&](int n, int i) { return kLdsQ ? lds_qs[n * kSteps + i][lane] : qscale[kLdsQ ? 0 : i]; };
+
+    // One tile in registers: its keys make way for the next one's after the scores, its
+    // values after the sums.  D = 256, where registers are short: the queries are split behind
+    // the first loads, so that what that needs is not held beside the places (microseconds
+    // before / behind, 32 sequences of 100 to 6000 tokens 45.4 / 40.9; D = 128, the ragged batch
+    // 52.0 / 52.8, 4 tokens on 33000 25.6 / 26.6).
+    constexpr bool kLoadsFirst = D == 256;
+    if constexpr (!kLoadsFirst) split_queries();
+    TileT x;
+    look(t0);
+    load_keys(x, 0);
+    load_values(x, 0);
+    if constexpr (kLoadsFirst) split_queries();
 
     // `keys_done` and `values_done` run where the tile's keys and values are no longer needed.
     auto compute = [&](TileT& x, int t, auto keys_done, auto values_done) {
@@ -445,12 +461,6 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(A
     };
     auto nothing = [] {};
 
-    // One tile in registers: its keys make way for the next one's after the scores, its
-    // values after the sums.
-    TileT x;
-    look(t0);
-    load_keys(x, 0);
-    load_values(x, 0);
     for (int t = t0; t + 1 < t1; ++t) {
       const int n = (t + 1 - t0) % kAhead;
       if (n == 0) look(t + 1);
@@ -516,7 +526,7 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(A
 // call, cut / not cut, D = 128 with 8 kv heads: one sequence of 513 tokens 13.0 / 10.1, of
 // 1025 13.0 / 11.1, of 1537 13.0 / 13.9; 64 of 64 to 513 19.8 / 10.7, of 256 to 2049
 // 29.7 / 22.9; 128 of 512 to 4097 77.7 / 80.1.  D = 256 with 4 heads: one of 1025
-// 13.4 / 17.2, 64 of 128 to 1025 25.1 / 18.8.
+// 13.6 / 16.0, 64 of 128 to 1025 23.8 / 16.8.
 int64_t whole_tokens(int D, int64_t units) {
   if (units >= 1 << 24) return 0;                        // more workgroups than a launch takes
   return units >= 256 ? 2048 : D == 256 ? 640 : 1024;
