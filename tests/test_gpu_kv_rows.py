@@ -102,6 +102,19 @@ def test_append_rope_matches_the_oracle(kind, high, kv, group, dim, rot, interle
     assert np.array_equal(got, want)                     # every other row as it was
 
 
+@pytest.mark.parametrize("case", [
+    # calls of so many tokens that a workgroup takes queries, keys and values: one vector of a kind per
+    # thread, several, more than are in flight at once; every way the pairs lie
+    ("fp8", "fp16", 16, 1, 64, 16, True, 24, [10, 0, 3], [1000, 1, 99]),
+    ("fp4", "bf16", 4, 7, 128, 128, False, 32, [0, 77], [1500, 1501]),
+    ("bf16", "bf16", 2, 3, 256, 250, False, 16, [0], [2200]),
+    ("fp8", "bf16", 1, 5, 128, 128, False, 64, [5, 0], [8000, 1300]),
+    ("fp4", "fp16", 1, 1, 64, 34, False, 8, [0, 0], [9000, 8000]),
+    ("fp16", "fp16", 3, 2, 128, 96, True, 11, [1], [2500])])
+def test_append_rope_of_many_tokens(case):
+    test_append_rope_matches_the_oracle(*case, "page token head")
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
 def test_rows_without_a_place(kind):
     """Rows of no sequence are left, rows at negative places and without a page are
