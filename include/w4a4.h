@@ -433,7 +433,7 @@ typedef enum { W4A4_BF16 = 0, W4A4_F16 = 1, W4A4_E4M3 = 2, W4A4_E2M1 = 4 } w4a4_
  * to nearest even, saturating at 6; a block with Inf or NaN gets byte 255 and zero
  * codes), from FP16 rows with exponents up to 13 (byte 140), so that what is stored
  * stays within FP16.  Scales beyond 2^125 (byte 252), and beyond 2^13 where rows are read out in
- * FP16 or w4a4_attn_prefill takes them with FP16 queries, may give Inf or NaN.
+ * FP16 or w4a4_attn_prefill takes them with FP16 queries, may give Inf or NaN in what sees them.
  *
  * Attention takes the keys' codes as they are, and the queries in blocks of 32 as sums of
  * four 6-bit numbers: within 2^-19 of the block's largest value, which is exact for BF16 values

@@ -33,6 +33,7 @@ namespace w4a4 {
 namespace {
 
 constexpr int kParts = 4;                                // of a query's block
+constexpr uint32_t kPastRange = 253;     // scale bytes from here on: 4 * 2^126 is past BF16's range, 255 NaN
 
 // Keys in the codes k with the scale byte ks, times part `PART`'s operand; its scale is
 // byte BYTE of qs.
@@ -348,7 +349,8 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(A
                                    (!a.window || base > pos_max - a.window || base + 32 <= a.sinks)
                              : base + 32 <= stop && (base >= sp.low || base + 32 <= a.sinks);
       if (!whole) {
-        bool nan = false;
+        bool odd = false;
+        auto past_range = [&](uint32_t y, int i) { return (OCT ? y >> (8 * (i & 3)) & 0xffu : y) >= kPastRange; };
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const bool any = seen(base + 8 * g + i, stop);
@@ -356,17 +358,16 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(A
           for (int n = 0; n < NB; ++n)
             if (!sees(base + 8 * g + i, stop, pos[n])) s[n][i >> 2][i & 3] = kNegInf;
 #pragma unroll
-          for (int r = 0; r < kRuns; ++r) {      // 0 x NaN would reach the sum
+          for (int r = 0; r < kRuns; ++r) {      // 0 x NaN and 0 x Inf would reach the sum
             uint32_t& y = x.vs[r][OCT ? i >> 2 : i];
-            const uint32_t byte = 0xffu << (OCT ? 8 * (i & 3) : 0);
-            if (!any) y &= ~byte;
-            nan |= (y & byte) == byte;
+            if (!any) y &= ~(0xffu << (OCT ? 8 * (i & 3) : 0));
+            odd |= past_range(y, i);
           }
         }
         if constexpr (FEW) {
-          // Blocks of NaN that some row sees and another one may not: the sums of the rows
-          // that see them become NaN, then the blocks are cleared.
-          if (__any(nan)) {
+          // Blocks of NaN, or with scales that may make Inf, that some row sees and another one may
+          // not: the sums of the rows that see them become NaN, then the blocks are cleared.
+          if (__any(odd)) {
 #pragma unroll
             for (int r = 0; r < kRuns; ++r) {
               at_u32x4 is;
@@ -377,10 +378,9 @@ __global__ void __launch_bounds__(256, wgs_per_cu(D, OCT, FEW, NB)) fp4_kernel(A
                 for (int h = 0; h < 2; ++h) {
                   const int i = 2 * k + h;
                   uint32_t& y = x.vs[r][OCT ? i >> 2 : i];
-                  const uint32_t byte = 0xffu << (OCT ? 8 * (i & 3) : 0);
-                  if ((y & byte) == byte) {
+                  if (past_range(y, i)) {
                     two |= Bf16::kOne << (16 * h);
-                    y &= ~byte;
+                    y &= ~(0xffu << (OCT ? 8 * (i & 3) : 0));
                   }
                 }
                 is[k] = two;
