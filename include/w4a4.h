@@ -436,8 +436,8 @@ typedef enum { W4A4_BF16 = 0, W4A4_F16 = 1, W4A4_E4M3 = 2, W4A4_E2M1 = 4 } w4a4_
  * FP16 or w4a4_attn_prefill takes them with FP16 queries, may give Inf or NaN in what sees them.
  *
  * Attention takes the keys' codes as they are, and the queries in blocks of 32 as sums of
- * four 6-bit numbers: within 2^-19 of the block's largest value, which is exact for BF16 values
- * down to 2^-10 of that and for FP16 values down to 2^-7.
+ * four 6-bit numbers: within 2^-19 of the block's largest value (2^-126 where that is more),
+ * which is exact for BF16 values down to 2^-10 of it and for FP16 values down to 2^-7.
  */
 
 typedef struct {

@@ -1,9 +1,13 @@
 """Attention over a cache held in 4 bits at the ends of its range: scales whose values
-leave BF16's, in places that some rows do not see."""
+leave BF16's, in places that some rows do not see; queries near the smallest normal number."""
+import numpy as np
 import pytest
 import torch
 
+import w4a4_block_scaled_amd as w4
 from gpu_common import device, say
+from kv_common import UNIT, as_f64, ints
+from oracle import attention as A
 from rows_common import chunks_fp4
 from test_gpu_attn_edges import attend
 from test_gpu_attn_fp4 import WAYS
@@ -44,3 +48,45 @@ def test_values_past_the_range_stay_with_the_rows_that_see_them(way, dim, high, 
         assert torch.equal(y[new[0]:], clean[new[0]:])
         codes.copy_(kept[0])
         scales.copy_(kept[1])
+
+
+@pytest.mark.parametrize("way", list(WAYS))
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("shift", [0, 100, 110, 118])
+def test_small_queries(way, dim, shift):
+    """Queries of 2^-shift, one value of each block of 32 2^11 times the others and its keys zero. The others
+    are promised to within 2^-19 of their block's largest value or 2^-126 if that is more, and the scale of
+    the softmax makes up for the shift, so they count as they do without it."""
+    if way == "few, three blocks" and dim == 256:
+        pytest.skip("these go as row tiles")
+    say(f"[small4] {way}, D = {dim}, queries of 2^-{shift}")
+    past, new, page = WAYS[way]
+    c = chunks_fp4(2, 4, dim, page, past, new, seed=dim + shift, dev=device())
+    q = c["q"].clone()
+    q[..., 7::32] = torch.sign(q[..., 7::32]) * 3000
+    c["q"] = (q.float() * 2.0 ** -shift).to(torch.bfloat16)
+    codes, _ = parts_of(c["kd"], page, 2, dim)
+    codes[..., 3::16] &= 15                                # the upper half of a byte each
+    k64 = c["f64"][0].copy()
+    k64[..., 7::32] = 0
+    scale, dev = dim ** -0.5 * 2.0 ** shift, c["dev"]
+    cache = c["kd"], c["vd"], ints(c["tables"], dev), ints(c["lens"], dev)
+    if way.startswith("decode"):
+        y, lse = w4.attn_decode(c["q"].to(dev), *cache, scale=scale, return_lse=True)
+    else:
+        y, lse = w4.attn_prefill(c["q"].to(dev), ints(c["cu"], dev), *cache, scale=scale, return_lse=True)
+    got, lse, q64, u = as_f64(y), lse.cpu().numpy().astype(np.float64), as_f64(c["q"]), UNIT["bf16"]
+    weights = u if way.startswith("whole") else 2.0 ** -15
+    for i in sorted({0, 1, len(q) - 1, int(c["cu"][1]) - 1}):
+        s = int(c["seqs"][i])
+        for h in (0, 5, 7):
+            o, ref, (a, big, size, n) = A.attend(q64[i, h], k64, c["f64"][1], c["tables"][s], c["lens"][s], int(c["pos"][i]),
+                                                 h // 4, scale, 0, 0)
+            keys = np.abs(A.rows(k64, c["tables"][s], range(n), h // 4)).reshape(n, -1, 32).sum(-1)
+            off = np.maximum(np.abs(q64[i, h]).reshape(-1, 32).max(-1) * 2.0 ** -19, 2.0 ** -126)
+            parts = (keys * off).sum(-1).max() * scale
+            eta = (dim + 8) * 2.0 ** -23 * (size + parts) + 2.0 ** -22 + parts
+            bound = u * np.abs(o) + (1 + u) * (weights + 2 * eta + n * 2.0 ** -22) * a + 2.0 ** -25
+            err = np.abs(got[i, h] - o)
+            assert np.all(err <= bound), f"row {i} head {h}: off by {err.max():.3e}, bound {bound[err.argmax()]:.3e}"
+            assert abs(lse[i, h] - ref) <= eta + n * 2.0 ** -22 + 2.0 ** -21 + 2.0 ** -22 * abs(ref)
