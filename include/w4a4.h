@@ -434,10 +434,14 @@ typedef enum { W4A4_BF16 = 0, W4A4_F16 = 1, W4A4_E4M3 = 2, W4A4_E2M1 = 4 } w4a4_
  * codes), from FP16 rows with exponents up to 13 (byte 140), so that what is stored
  * stays within FP16.  Scales beyond 2^125 (byte 252), and beyond 2^13 where rows are read out in
  * FP16 or w4a4_attn_prefill takes them with FP16 queries, may give Inf or NaN in what sees them.
+ * Below 2^-13 FP16 holds their values as multiples of 2^-24: there (w4a4_kv_read in FP16, and row
+ * tiles of w4a4_attn_prefill with FP16 queries) they are off by up to 2^-25.
+ * Decoding, and few rows, take all values that BF16 has exactly.
  *
  * Attention takes the keys' codes as they are, and the queries in blocks of 32 as sums of
  * four 6-bit numbers: within 2^-19 of the block's largest value (2^-126 where that is more),
  * which is exact for BF16 values down to 2^-10 of it and for FP16 values down to 2^-7.
+ * A row of queries with Inf or NaN among its values gives NaN.
  */
 
 typedef struct {

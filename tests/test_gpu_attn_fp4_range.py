@@ -1,5 +1,6 @@
 """Attention over a cache held in 4 bits at the ends of its range: scales whose values
-leave BF16's, in places that some rows do not see; queries near the smallest normal number."""
+leave BF16's, in places that some rows do not see; queries near the smallest normal number; values
+that FP16 holds as subnormals."""
 import numpy as np
 import pytest
 import torch
@@ -8,6 +9,7 @@ import w4a4_block_scaled_amd as w4
 from gpu_common import device, say
 from kv_common import UNIT, as_f64, ints
 from oracle import attention as A
+from oracle import rotary as R
 from rows_common import chunks_fp4
 from test_gpu_attn_edges import attend
 from test_gpu_attn_fp4 import WAYS
@@ -90,3 +92,35 @@ def test_small_queries(way, dim, shift):
             err = np.abs(got[i, h] - o)
             assert np.all(err <= bound), f"row {i} head {h}: off by {err.max():.3e}, bound {bound[err.argmax()]:.3e}"
             assert abs(lse[i, h] - ref) <= eta + n * 2.0 ** -22 + 2.0 ** -21 + 2.0 ** -22 * abs(ref)
+
+
+@pytest.mark.parametrize("way", list(WAYS))
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("exponent", [-14, -18, -22, -24])
+def test_small_values_with_fp16_queries(way, dim, exponent):
+    """Values in steps of 2^(exponent - 1). Where they are widened to FP16 (row tiles) each is rounded to a
+    multiple of 2^-24, by 2^-25 at most, and so is a weighted mean of them."""
+    if way == "few, three blocks" and dim == 256:
+        pytest.skip("these go as row tiles")
+    say(f"[subnormal4] {way}, D = {dim}, values of 2^{exponent}")
+    past, new, page = WAYS[way]
+    c = chunks_fp4(2, 4, dim, page, past, new, seed=dim - exponent, high="fp16", dev=device())
+    codes, scales = parts_of(c["vd"], page, 2, dim)
+    scales.fill_(exponent + 127)
+    size = page * 2 * dim // 2
+    raw = c["vd"].as_strided((c["vd"].shape[0], c["vd"].stride(0)), (c["vd"].stride(0), 1))[:, :size + 2 * (dim // 32) * page]
+    v64 = R.decode_blocks(*R.from_pages(raw.cpu().numpy(), page, 2, dim))
+    y, _ = attend(c, way)
+    got, q64, u, scale = as_f64(y), as_f64(c["q"]), UNIT["fp16"], dim ** -0.5
+    tiles = way.startswith("whole") or way == "split"
+    weights = u if way.startswith("whole") else 2.0 ** -20 if way == "split" else 2.0 ** -15
+    for i in sorted({0, 1, len(q64) - 1, int(c["cu"][1]) - 1}):
+        s = int(c["seqs"][i])
+        for h in (0, 5, 7):
+            o, _, (a, big, dots, n) = A.attend(q64[i, h], c["f64"][0], v64, c["tables"][s], c["lens"][s], int(c["pos"][i]),
+                                               h // 4, scale, 0, 0)
+            eta = (dim + 8) * 2.0 ** -23 * dots + 2.0 ** -22
+            bound = u * np.abs(o) + (1 + u) * ((weights + 2 * eta + n * 2.0 ** -22) * a + n * 2.0 ** -24 * big) + 2.0 ** -25
+            bound = bound + (2.0 ** -25 * (1 + u) * (1 + weights + 2 * eta) if tiles else 0)
+            err = np.abs(got[i, h] - o)
+            assert np.all(err <= bound), f"row {i} head {h}: off by {err.max():.3e}, bound {bound[err.argmax()]:.3e}"
