@@ -502,7 +502,7 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_seqs* seqs,
  * The other values stay as they are.  freqs holds what the kind of positions asks
  * for: base^(-2i / rot_dim), compressed or stretched by parts for long contexts.
  * Angles are taken from p * freqs[i] in 64 bits (right to 2^-48 of a turn at position 131071,
- * to 1e-6 of one at 2^31 - 1).  16-bit results are within 3.5 * 2^-24 (|a| + |b|) * factor
+ * to 1e-6 of one at 2^31 - 1).  16-bit results are within 4 * 2^-24 (|a| + |b|) * factor
  * before their one rounding: fp32 cos and sin and products.  Results of 8 or 4 bits are the
  * roundings of the 64-bit values.
  */

@@ -32,8 +32,8 @@ __device__ __forceinline__ Angle angle_of(int pos, float freq) {
   const double u = 4.0 * ((t - __builtin_rint(t)) + rest), k = __builtin_rint(u);
   return {(u - k) * 0x1.921fb54442d18p+0, int(k) & 3};
 }
-// cos and sin by the Taylor series around the quarter turn, times factor: in fp64 right
-// to 2^-50, in fp32 to 1.5 * 2^-24.
+// cos and sin by the Taylor series around the quarter turn, in fp64 right to 2^-50, in fp32
+// to 1.3 * 2^-24 and to 2.2 * 2^-24 of themselves; times factor, to 2^-24 of the product.
 static __device__ const double kSeries[14] = {
     -1.0 / 1307674368000.0, 1.0 / 6227020800.0, -1.0 / 39916800.0, 1.0 / 362880.0, -1.0 / 5040.0, 1.0 / 120.0,
     -1.0 / 6.0, -1.0 / 87178291200.0, 1.0 / 479001600.0, -1.0 / 3628800.0, 1.0 / 40320.0, -1.0 / 720.0, 1.0 / 24.0,
@@ -196,8 +196,9 @@ __device__ __forceinline__ void widen8(at_u32x4 own, R (&y)[8]) {
   for (int e = 0; e < 8; ++e) y[e] = e & 1 ? T::high(own[e >> 1]) : T::low(own[e >> 1]);
 }
 // The elements own, with their partners' elements other (kHalf) or their row (kHalfAny), in
-// fp32: cos and sin are right to 1.5 * 2^-24, a product and the sum to 2^-24, so y to 3.5 *
-// 2^-24 (|x| + |w|) factor.
+// fp32.  y is right to 4 * 2^-24 (|x| + |w|) factor: of |w| factor the error of s, and 2^-24 |s|
+// each for the factor, the product and the sum, 3.6 * 2^-24 at most together; of |x| less.
+// It is also right to 5.5 * 2^-24 (|x c| + |w s|): 2.2 of s itself and those three.
 // SIZES: size becomes |x| |c| + |w| |s|, 0 for an element that stays as it is.
 template <class T, int STYLE, bool SIZES = false>
 __device__ __forceinline__ void turn8(at_u32x4 own, at_u32x4 other, const uint16_t* row, int d, int pairs,
@@ -443,8 +444,8 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
           float lo[4], hi[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            // y is off by 3.5 * 2^-24 of its size, the quotient by 2 * 2^-24 of itself, and the bounds'
-            // ends are rounded: 2^-21 of both
+            // y is off by 5.5 * 2^-24 of its size, the quotient by 2 * 2^-24 of itself, and the bounds'
+            // ends are rounded by 2^-24 of it: 2^-21 of both
             const float q = y[4 * k + e] * inv;
             const float room = KEY ? __builtin_fmaf(size[4 * k + e], inv, __builtin_fabsf(q)) * 0x1p-21f : q * 0x1p-21f;
             lo[e] = __builtin_amdgcn_fmed3f(q - room, -448.0f, 448.0f);
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(256) rows_in_kernel(RowsIn a, Parts parts, int
         uint32_t codes = 0, scale = 0;
         bool sure = true;
         if constexpr (KEY) {
-          // what the values are off by: 3.5 * 2^-24 of both values of a pair, at most 7 * 2^-24 of
+          // what the values are off by: 4 * 2^-24 of both values of a pair, at most 8 * 2^-24 of
           // the largest one here; the bounds' ends round by 2 * 2^-24 of it
           turn8<T, STYLE>(own, other, row, d, pairs, turns, y);
           uint32_t top = top_bits(own);
