@@ -12,7 +12,9 @@ Every step is what a serving loop does for each layer:
 with the page bookkeeping around it once per step: kv_reserve before new tokens
 are stored, kv_fork when a sequence is continued in several ways, kv_trim as the
 window moves on, kv_free when a sequence ends, kv_compact when the cache has
-holes, kv_read when rows are to be kept elsewhere.  The weights are random; the outputs are checked for what holds whatever
+holes, kv_read when rows are to be kept elsewhere.  With --no-rotary the keys
+are stored by kv_append as they are, for models that have positions elsewhere or none.
+The weights are random; the outputs are checked for what holds whatever
 they are: branches of one prompt that are fed the same tokens give the same
 outputs, also after the cache has been compacted.  (Bit for bit at these sizes,
 where every tile of the attention's work has a workgroup of its own; in a fuller
@@ -56,12 +58,14 @@ def empty_cache(cache_type, pages, page, heads, dim, device):
 class Attention:
     """QKV linear, cache, attention and O linear of one layer."""
 
-    def __init__(self, hidden, q_heads, kv_heads, pages, page, cache_type, gen, device):
+    def __init__(self, hidden, q_heads, kv_heads, pages, page, cache_type, gen, device, rotary=True):
         self.dim = hidden // q_heads
         self.q_heads, self.kv_heads = q_heads, kv_heads
         self.qkv = Linear((q_heads + 2 * kv_heads) * self.dim, hidden, gen, device)
         self.o = Linear(hidden, hidden, gen, device)
-        self.freqs, self.factor = w4.rope_freqs(self.dim, 500000.0, scaling="bands", scale=8.0, original=8192, device=device)
+        self.rotary = rotary
+        if rotary:
+            self.freqs, self.factor = w4.rope_freqs(self.dim, 500000.0, scaling="bands", scale=8.0, original=8192, device=device)
         self.cache = empty_cache(cache_type, pages, page, kv_heads, self.dim, device)
         self.scales = {}
         if cache_type == torch.float8_e4m3fn:
@@ -71,7 +75,10 @@ class Attention:
     def __call__(self, x, tables, lens, cu=None, **mask):
         rows = self.qkv(x).view(len(x), -1, self.dim)
         q, k, v = rows.split([self.q_heads, self.kv_heads, self.kv_heads], dim=1)
-        q = w4.kv_append_rope(q, k, v, *self.cache, tables, lens, self.freqs, cu_seqlens=cu, factor=self.factor, **self.scales)
+        if self.rotary:
+            q = w4.kv_append_rope(q, k, v, *self.cache, tables, lens, self.freqs, cu_seqlens=cu, factor=self.factor, **self.scales)
+        else:
+            w4.kv_append(k, v, *self.cache, tables, lens, cu_seqlens=cu, **self.scales)
         if cu is None:
             y = w4.attn_decode(q, *self.cache, tables, lens, **mask, **self.scales)
         else:
@@ -80,12 +87,12 @@ class Attention:
 
 
 def run(hidden=1024, q_heads=8, kv_heads=2, prompt=300, steps=24, branches=3, page=16, window=128, sinks=4,
-        cache_type=torch.bfloat16, device="cuda", say=print):
+        cache_type=torch.bfloat16, device="cuda", say=print, rotary=True):
     gen = torch.Generator().manual_seed(1)
     seqs = 2 + branches                                  # two prompts, and the branches of the first
     per_seq = -(-(prompt + steps) // page) + 1
     pages = 2 * per_seq + branches * (steps // page + 3) + 4
-    layer = Attention(hidden, q_heads, kv_heads, pages, page, cache_type, gen, device)
+    layer = Attention(hidden, q_heads, kv_heads, pages, page, cache_type, gen, device, rotary)
     tables = torch.full((seqs, per_seq), -1, dtype=torch.int32, device=device)
     lens = torch.zeros(seqs, dtype=torch.int32, device=device)
     refs = torch.zeros(pages, dtype=torch.int32, device=device)
@@ -149,6 +156,8 @@ if __name__ == "__main__":
     ap.add_argument("--steps", type=int, default=40)
     ap.add_argument("--e4m3", action="store_true", help="an 8-bit cache")
     ap.add_argument("--e2m1", action="store_true", help="a 4-bit cache")
+    ap.add_argument("--no-rotary", action="store_true", help="keys stored as they are")
     a = ap.parse_args()
     run(a.hidden, a.hidden // 128, max(a.hidden // 512, 1), a.prompt, a.steps,
-        cache_type=torch.float8_e4m3fn if a.e4m3 else torch.uint8 if a.e2m1 else torch.bfloat16)
+        cache_type=torch.float8_e4m3fn if a.e4m3 else torch.uint8 if a.e2m1 else torch.bfloat16,
+        rotary=not a.no_rotary)
