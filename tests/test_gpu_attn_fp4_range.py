@@ -124,3 +124,26 @@ def test_small_values_with_fp16_queries(way, dim, exponent):
             bound = bound + (2.0 ** -25 * (1 + u) * (1 + weights + 2 * eta) if tiles else 0)
             err = np.abs(got[i, h] - o)
             assert np.all(err <= bound), f"row {i} head {h}: off by {err.max():.3e}, bound {bound[err.argmax()]:.3e}"
+
+
+@pytest.mark.parametrize("way", list(WAYS))
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("high", ["bf16", "fp16"])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_inf_and_nan_among_queries(way, dim, high, value):
+    """A head of a row of queries with Inf or NaN anywhere becomes NaN, and no other row or head changes."""
+    if way == "few, three blocks" and dim == 256:
+        pytest.skip("these go as row tiles")
+    say(f"[odd queries4] {way}, D = {dim}, {high}, {value}")
+    past, new, page = WAYS[way]
+    c = chunks_fp4(2, 4, dim, page, past, new, seed=dim, high=high, dev=device())
+    clean, lse = attend(c, way)
+    odd = torch.zeros(clean.shape[:2], dtype=torch.bool)
+    c["q"] = c["q"].clone()
+    for row, head, d in ((0, 0, 5), (len(odd) - 1, 7, dim - 1), (len(odd) // 2, 3, dim // 2)):
+        c["q"][row, head, d] = value
+        odd[row, head] = True
+    y, l2 = attend(c, way)
+    odd = odd.to(y.device)
+    assert torch.isnan(y[odd]).all() and torch.isnan(l2[odd]).all()
+    assert torch.equal(y[~odd], clean[~odd]) and torch.equal(l2[~odd], lse[~odd])
