@@ -535,7 +535,10 @@ w4a4_status w4a4_rope(const w4a4_rotation* rotation, int64_t tokens, const int32
  * what is stored in 8 or 4 bits comes from the unrounded rotated keys.
  *
  *   cu, tokens, dtype, k, v: as in w4a4_kv_append (E4M3: code = RNE_E4M3(x / scale)
- *              of the fp64 quotient).
+ *              of the fp64 quotient, where w4a4_kv_append rounds the fp32 one: that is
+ *              a tie by its own rounding for one value in some million, whose codes by
+ *              the two entry points are then neighbours.  By powers of two both are
+ *              exact).
  *   positions  device, int32 [tokens]: what q and k are rotated by; NULL: their
  *              places in their sequences (lens[s] - count + i).  Where rows are
  *              stored goes by the places alone.

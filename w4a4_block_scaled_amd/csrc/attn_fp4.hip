@@ -18,12 +18,14 @@
 // the weights in two parts (16 bits together): the widened values are exact, and of the
 // range that the cache's scales have.
 //
-// Measured, whole calls, D = 128: 48 sequences of 37 to 8191 tokens, 8 kv heads of 4, 216 MB
-// 52 us (kernel 47.5, 4.5 TB/s; its loads alone take 43; the vector unit is busy 46%, the
-// matrix cores 16% of the time); 3 of 90001 to 131071, 4 heads of 7, 180 MB 44.7 us (kernel
-// 40, loads alone 36); 5 and 9 tokens on 30000 and 33333, 8 heads of 4, 69 MB 39 us (kernel 37:
-// the chain of scores, softmax and sums with two waves per SIMD).  A second tile in
-// registers does not pay where it fits either (4 tokens on 33000 25.5 us, 28.1 with it).
+// Measured, D = 128, whole calls in a loop, and (in a trace, which is slower) kernel + join: 48
+// sequences of 37 to 8191 tokens, 8 kv heads of 4, 216 MB 52 to 53 us (47.5 + 4.9; the kernel's
+// loads without its arithmetic 43: values come 4 bytes per lane; the vector unit is busy
+// 46%, the matrix cores 16% of the time); 3 of 90001 to 131071, 4 heads of 7, 180 MB 45 to 46 us
+// (40.6 + 5.6; loads 36); 5 and 9 tokens on 30000 and 33333, 8 heads of 4, 69 MB 39 to 40 us (38.1
+// + 5.3: the chain of scores, softmax and sums with two waves per SIMD).  A plain read takes
+// 36, 30 and 12 us.  A second tile in registers does not pay where it fits either (4 tokens
+// on 33000 25.5 us, 28.1 with it).
 #include <algorithm>
 
 #include "attn_fp4.h"
@@ -71,7 +73,8 @@ __device__ __forceinline__ uint32_t widen_byte(uint32_t u, float s, int b) {
 }
 
 constexpr int kAheadOct = 16, kAheadAny = 2;             // tiles that one load of the table serves
-// Workgroups that share a CU: as many as the registers leave without spilling.
+// Workgroups that share a CU: as many as the registers leave without spilling (but for three
+// blocks at D = 128, where 10 go to scratch; these have not been timed with one workgroup).
 // Microseconds with 4 / 3 / 2 / 1: D = 64 (32 sequences of 100 to 6000 tokens) 37.7 / 40.5 /
 // 53.0 / 83.4; D = 128, the ragged batch 62.5 (spills) / 52.3 / 56.0 / 75.3, pages of 11
 // 152 / 70 (spills) / 39.2 / 54.4, 2 tokens of each of 8 sequences on 8000 37.6 / 25.5 / 23.5

@@ -33,13 +33,16 @@
 // values are widened on their way to LDS, as from E4M3.
 // (Ragged chunks over 28 / 4 heads 506 us, 560 with the keys widened to 16 bits too; three
 // parts of the queries, right to 2^-14 of a block's largest value, miss the bound on lse.)
+// The parts do not all fit: at D = 128 19 registers go to scratch (where rows are looked up one
+// by one 29 with BF16 queries, 35 with FP16), at D = 256 4 and 13, with the keys split 73 and 75.
 //
 // Measured, 32 / 8 heads, D = 128, causal 8192 bf16: 512 to 528 us, 1.05 PFLOP/s (a
 // library product of 8192^3 reaches 1.44 here; the MFMAs are busy 55% of the
 // time on the ragged chunks, at 1.65 GHz), E4M3 537 to 557 us, D = 64 320 to 337;
 // 4096 at D = 256 332 to 346 us.  Ragged chunks over 28 / 4 heads, 526 GFLOP:
 // 491 to 514 us.  82 tokens: 10.5 us, 8.7 of them the kernel's.  FP4: causal 8192 514 us, D = 64
-// 320, 4096 at D = 256 176 over 16 / 4 heads; ragged chunks 506 to 528.
+// 320, 4096 at D = 256 176 over 16 / 4 heads; ragged chunks 506 to 528; keys split, 100 and 60
+// tokens on 30000 and 20000, 32 / 8 heads 174 us (bf16 163), 16 / 4 of D = 256 385 (bf16 667).
 #include <algorithm>
 #include <type_traits>
 #include <utility>

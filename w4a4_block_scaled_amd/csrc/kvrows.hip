@@ -7,7 +7,8 @@
 // TB/s (a copy of the queries alone by torch 36, by this kernel 34); out of 4 bits 162 MB in
 // 28 us.  Small calls are their launch and the chain of lookups behind it: 3.2 us for 16
 // tokens, 4.2 with a cache.  In between the vector unit counts, some 350 instructions per
-// row of keys and wave: 1795 tokens of 16 / 16 heads of 64 into E4M3, 18 MB, 11.7 us.
+// row of keys and wave: 1795 tokens of 16 / 16 heads of 64 into E4M3, 18 MB, 11.7 us
+// (by random scales; see rows_in_kernel for those that are powers of two).
 #include <algorithm>
 #include <type_traits>
 
@@ -301,8 +302,16 @@ struct Parts {
 // What is kept in 16 bits is rotated in fp32.  Keys on their way to 8 or 4 bits, and
 // quotients by E4M3's scales, are rounded from the values themselves, not from an fp32
 // rounding of them: in fp32 they are known to within a bound; where both ends of that
-// give the same codes these are the right ones, else (one vector in some hundred) all of
-// it is taken again in fp64.
+// give the same codes these are the right ones, else the wave takes its 512 values again in
+// fp64.  Of random ones by a scale that is no power of two that is one wave in 50 (turned
+// keys into 8 bits), 100 (into 4 bits) or 200 (values into 8 bits).  In doubt are also
+//  - ties, which quotients by a power of two often are: a value in 16 (BF16) or 128 (FP16),
+//    that is nearly every wave of values and of keys that turn in part, also without scales
+//    (1795 tokens of 16 / 16 heads of 64 into E4M3: a quarter of the head turned 18.3 us, 11.5
+//    to 12.6 by other scales; all of it 14.1 and 12.4 to 12.9; by graph replay)
+//  - zeros, for their sign: of E4M3's negative ones, and of turned pairs or blocks into 4
+//    bits (14449 tokens, 28 / 4 heads of 128: none 61 us, half of the rows 77, all 95; one
+//    value in a hundred 62).
 // FLIGHT: vectors in flight per thread, 1 where none has more than one of a kind: the code
 // that the unrolled steps would skip has to be read too (1795 tokens of 16 / 16 heads of 64
 // into E4M3 11.8 us, 12.7 with 4; into FP16 8.1 and 9.4).
