@@ -7,7 +7,7 @@ import torch
 
 import w4a4_block_scaled_amd as w4
 from gpu_common import device, say
-from kv_common import UNIT, as_f64, ints
+from kv_common import UNIT, as_f64, check_attention, ints
 from oracle import attention as A
 from oracle import rotary as R
 from rows_common import chunks_fp4
@@ -147,3 +147,40 @@ def test_inf_and_nan_among_queries(way, dim, high, value):
     odd = odd.to(y.device)
     assert torch.isnan(y[odd]).all() and torch.isnan(l2[odd]).all()
     assert torch.equal(y[~odd], clean[~odd]) and torch.equal(l2[~odd], lse[~odd])
+
+
+@pytest.mark.parametrize("way", PREFILL)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("high", ["bf16", "fp16"])
+@pytest.mark.parametrize("byte", [254, 255])
+def test_keys_past_the_range_stay_with_the_rows_that_see_them(way, dim, high, byte):
+    """A token's keys of 6 * 2^127 (a score past any other) or NaN: the rows that do not see it are as without
+    it. With NaN bit for bit; a score that one row sees moves the references of the softmax of all rows
+    in its wave, and with them which way their weights round, so there the other rows are compared with the
+    64-bit values by the bound on every output, which holds for any reference."""
+    if way == "few, three blocks" and dim == 256:
+        pytest.skip("these go as row tiles")
+    say(f"[range4] {way}, D = {dim}, {high}, keys with scale byte {byte}")
+    past, new, page = WAYS[way]
+    window, sinks = 200, 3
+    c = chunks_fp4(2, 4, dim, page, past, new, seed=dim, high=high, dev=device())
+    clean, lse = attend(c, way, window, sinks)
+    codes, scales = parts_of(c["kd"], page, 2, dim)
+    kept = codes.clone(), scales.clone()
+    # few rows: weights in two parts of BF16, 2^-15 of them, which FP16's "once" (2^-11) covers
+    weights = "two" if way == "split" or (high == "bf16" and way.startswith("few")) else "once"
+    for token, others in ((past[0] - window + 1, slice(1, None)), (c["lens"][0] - 1, slice(0, new[0] - 1))):
+        at = int(c["tables"][0, token // page])
+        codes[at, :, token % page], scales[at, :, :, token % page] = 0x77, byte
+        y, l2 = attend(c, way, window, sinks)
+        assert torch.equal(y[new[0]:], clean[new[0]:])
+        if byte == 254:
+            near = [r for r in (0, 1, new[0] // 2, new[0] - 2, new[0] - 1) if r in range(*others.indices(new[0]))]
+            check_attention(y, l2.cpu(), c["q"], c["f64"], c["tables"], c["lens"], c["pos"], c["seqs"], high, dim ** -0.5, window,
+                            sinks, weights, "other rows", near)
+        else:
+            assert torch.equal(y[others], clean[others]) and torch.equal(l2[others], lse[others])
+            own = 0 if others.start == 1 else new[0] - 1
+            assert torch.isnan(y[own]).all() and torch.isnan(l2[own]).all()
+        codes.copy_(kept[0])
+        scales.copy_(kept[1])

@@ -30,7 +30,9 @@
 //
 // FP4 (4-bit caches): keys lie in LDS as the cache has them, codes and scale bytes, and the
 // scores come from the scaled 32 x 32 x 64 MFMA, the queries in four FP6 parts (attn_fp4.h);
-// values are widened on their way to LDS, as from E4M3.
+// values are widened on their way to LDS, as from E4M3, to the queries' type: to BF16 exactly, to
+// FP16 below 2^-13 in its steps of 2^-24 (half of one is what the output's own rounding is off by
+// there) and past its range to Inf, for products at the 16-bit rate without a second type.
 // (Ragged chunks over 28 / 4 heads 506 us, 560 with the keys widened to 16 bits too; three
 // parts of the queries, right to 2^-14 of a block's largest value, miss the bound on lse.)
 // The parts do not all fit: at D = 128 19 registers go to scratch (where rows are looked up one
